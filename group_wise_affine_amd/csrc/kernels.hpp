@@ -219,4 +219,45 @@ bool qmv_two_chunk_shape(int64_t N, int64_t K, int bits);
 void force_route(Route r);
 Route forced_route();   // the current override (kRouteNone: automatic)
 
+// ------------------------------------------------------------ int8 products
+// rows of x the GEMV takes (W is read once per 32 of them)
+constexpr int64_t kI8GemvMaxM = 32;
+// arrival counters (4 bytes each) at the start of a scratch buffer
+constexpr int64_t kScratchCounters = 16384;
+struct I8Plan {
+  bool gemv;
+  int bm, bn;
+  int64_t tiles, ks, steps, ws_bytes;
+};
+I8Plan i8_plan(int64_t M, int64_t N, int64_t K);
+hipError_t launch_i8_quantize(int dt, const void* x, int64_t ldx, int64_t rows, int64_t K,
+                              int8_t* xq, float* sx, hipStream_t st);
+hipError_t launch_i8_t(int dt, const int8_t* xq, const float* sx, const int8_t* wq,
+                       const float* sw, const void* bias, int64_t M, int64_t N, int64_t K, void* y,
+                       unsigned* cnt, int* ws, hipStream_t st);
+
+// ------------------------------------------------- paged 8-bit cache (kv8)
+struct Kv8;
+hipError_t launch_kv8_append(const Kv8& c, int dt, const void* k, int64_t ldk, const void* v,
+                             int64_t ldv, int64_t T, const int32_t* table, const int32_t* lens,
+                             const int32_t* cu, int64_t S, int64_t W, hipStream_t st);
+hipError_t launch_kv8_read(const Kv8& c, int dt, const int32_t* pages, int64_t n, void* k, void* v,
+                           hipStream_t st);
+hipError_t launch_kv8_copy(const Kv8& to, const Kv8& from, const int32_t* dst, const int32_t* src,
+                           int64_t n, hipStream_t st);
+int64_t kv8_pages_work(int64_t P);   // scratch bytes of the two below
+hipError_t launch_kv8_update(const Kv8& c, const int32_t* ref, const int32_t* table,
+                             const int32_t* lens, const int32_t* parent, const int32_t* new_lens,
+                             int64_t S, int64_t W, int32_t* ref_out, int32_t* table_out,
+                             int32_t* shortage, int32_t* work, hipStream_t st);
+hipError_t launch_kv8_compact(const Kv8& c, const int32_t* ref, const int32_t* table, int64_t S,
+                              int64_t W, int32_t* ref_out, int32_t* table_out, int32_t* remap,
+                              int32_t* used, int32_t* work, hipStream_t st);
+// scratch bytes of the attention (0: none) after the counters
+int64_t kv8_attention_work(const Kv8& c, int64_t T, int64_t Hq, int64_t S, int64_t W);
+hipError_t launch_kv8_attention(const Kv8& c, int dt, const void* q, int64_t ldq, int64_t T,
+                                int64_t Hq, const int32_t* table, const int32_t* lens,
+                                const int32_t* cu, int64_t S, int64_t W, float scale, void* out,
+                                float* lse, unsigned* cnt, float* ws, hipStream_t st);
+
 }  // namespace qmm

@@ -440,6 +440,163 @@ int64_t qmm_crossover_m(qmm_dtype dt, int bits, int group_size, int64_t N, int64
  */
 qmm_status qmm_force_kernel(int kernel);
 
+/* ------------------------------------------------------------------------
+ * Serving in 8 bits: products of 8-bit integers, a paged 8-bit key/value
+ * cache with the attention that reads it, and the bookkeeping of its pages.
+ * The general rules above hold (device pointers, synchronous checks, work
+ * queued on `stream`, no allocation), with these additions:
+ *  - Scratch memory is the caller's: `work` (16-byte aligned) of at least as
+ *    many bytes as the call's qmm_*_work function says (0: work may be NULL).
+ *    Its first QMM_WORK_COUNTERS bytes must be zero before the first call
+ *    that uses the buffer and are zero again after each call; one buffer
+ *    serves every call below, one call at a time (calls on one stream are).
+ *  - Codes are symmetric: v = scale * c, c an int8 in [-127, 127], scale
+ *    fl32(amax / 127). Codes are rint(fl32(v / scale)) (ties to even). A
+ *    block (row, page) that holds an infinity or a NaN gets the scale NaN and
+ *    codes 0, so that what is computed from it is NaN.
+ */
+#define QMM_WORK_COUNTERS 65536
+
+/*
+ * Rows of x [rows, K] (f16 or bf16; row r starts at x + r*ldx elements, ldx a
+ * multiple of 8 and >= K, x 16-byte aligned) to codes [rows, K] and one fp32
+ * scale per row: per-token quantization of activations, or per-channel
+ * quantization of a weight [N, K]. K a multiple of 16 below 2^17 (as for the
+ * products below). Codes 16-byte aligned.
+ */
+qmm_status qmm_i8_quantize(const void* x, int64_t ldx, qmm_dtype dt, int64_t rows, int64_t K,
+                           int8_t* codes, float* scales, void* stream);
+
+/*
+ * y[M,N] (dt) = round(fl32(sx[m] * sw[n]) * sum_k xq[m,k] * wq[n,k] + bias[n])
+ * with codes xq [M, K], wq [N, K], fp32 scales sx [M] (tokens), sw [N]
+ * (channels) and an optional bias [N] in dt (NULL: none). The integer sum is
+ * exact; scales, bias and the one rounding to dt follow in fp32. A GEMV up to
+ * 32 rows, an MFMA tile kernel beyond. xq, wq and y 16-byte aligned.
+ */
+int64_t qmm_i8_t_work(int64_t M, int64_t N, int64_t K);
+qmm_status qmm_i8_t(const int8_t* xq, const float* sx, const int8_t* wq, const float* sw,
+                    const void* bias, qmm_dtype dt, int64_t M, int64_t N, int64_t K, void* y,
+                    void* work, int64_t work_bytes, void* stream);
+
+/*
+ * qmm_i8_quantize of x [M, K] (rows ldx apart) followed by qmm_i8_t: a linear
+ * layer on 8-bit integers, activations quantized on the fly.
+ */
+int64_t qmm_i8_linear_work(int64_t M, int64_t N, int64_t K);
+qmm_status qmm_i8_linear(const void* x, int64_t ldx, const int8_t* wq, const float* sw,
+                         const void* bias, qmm_dtype dt, int64_t M, int64_t N, int64_t K, void* y,
+                         void* work, int64_t work_bytes, void* stream);
+
+/*
+ * A key/value cache in 8 bits. Page p holds page_tokens consecutive tokens of
+ * one sequence for every head: k [pages, heads, page_tokens, head_dim], v
+ * transposed [pages, heads, head_dim, page_tokens], and one scale per page
+ * and head, k_scales and v_scales [pages, heads]. page_tokens 16, 32 or 64,
+ * head_dim 64, 128 or 256, pages <= 2^28; k and v 16-byte aligned.
+ *
+ * A batch of S sequences: table [S, W] int32 page numbers (column j holds
+ * tokens j*page_tokens ..), lens [S] tokens per sequence including the new
+ * ones, cu [S + 1] where each sequence's new tokens start in the packed batch
+ * of T (cu[0] = 0, cu[S] = T, not decreasing). These are read on the device:
+ * values out of range are brought into it, and places whose page number is
+ * outside [0, pages) are left out (nothing is written to them, no query sees
+ * them), so no access leaves the arrays.
+ */
+typedef struct {
+  int8_t* k;
+  int8_t* v;
+  float* k_scales;
+  float* v_scales;
+  int64_t pages;
+  int heads;
+  int page_tokens;
+  int head_dim;
+} qmm_kv8_cache;
+
+/*
+ * Write the new tokens' keys and values, k and v [T, heads, head_dim] (token
+ * t at k + t*ldk elements, ldk a multiple of 8; 16-byte aligned), into the
+ * last places of their sequences. A page's scale is that of its new values
+ * (amax / 127), and no less than its old scale when the page already holds
+ * tokens of the sequence: their codes are then brought to the new scale,
+ * rint(fl32(fl32(c * old) / new)). Places behind the last token of a page
+ * that is written become 0. Sequences must not share a page that is written.
+ */
+qmm_status qmm_kv8_append(const qmm_kv8_cache* cache, const void* k, int64_t ldk, const void* v,
+                          int64_t ldv, qmm_dtype dt, int64_t T, const int32_t* table,
+                          const int32_t* lens, const int32_t* cu, int64_t S, int64_t W,
+                          void* stream);
+
+/*
+ * Pages as values, round(fl32(scale * code)) in dt: k and v [n, heads,
+ * page_tokens, head_dim] for page numbers pages [n] (zeros for a number
+ * outside the cache).
+ */
+qmm_status qmm_kv8_read(const qmm_kv8_cache* cache, const int32_t* pages, int64_t n, qmm_dtype dt,
+                        void* k, void* v, void* stream);
+
+/*
+ * Causal attention of the new tokens' queries q [T, q_heads, head_dim] (token
+ * t at q + t*ldq elements, ldq a multiple of 8; 16-byte aligned) over their
+ * sequences: the i-th of n new tokens of a sequence of `len` sees positions
+ * 0 .. len - n + i. q_heads is a multiple of the cache's heads; query heads
+ * h*G .. h*G + G - 1 read cache head h. Scores are scale * (q . k). out [T,
+ * q_heads, head_dim] in dt, 16-byte aligned; lse [T, q_heads] fp32 (NULL: not
+ * wanted) the natural logarithm of the sum of exponentials of the scores. A
+ * query that sees nothing gets 0 and -inf. Sums, maxima and the normaliser
+ * are held in fp32; exp(score - max) * v scale is rounded to f16 for the
+ * matrix product with the codes.
+ */
+int64_t qmm_kv8_attention_work(const qmm_kv8_cache* cache, int64_t T, int64_t q_heads, int64_t S,
+                               int64_t W);
+qmm_status qmm_kv8_attention(const qmm_kv8_cache* cache, const void* q, int64_t ldq, qmm_dtype dt,
+                             int64_t T, int64_t q_heads, const int32_t* table, const int32_t* lens,
+                             const int32_t* cu, int64_t S, int64_t W, float scale, void* out,
+                             float* lse, void* work, int64_t work_bytes, void* stream);
+
+/*
+ * One step of page bookkeeping for S slots, on the device: slot s continues
+ * the first min(lens[parent[s]], new_lens[s]) tokens of slot parent[s] (s
+ * itself: the sequence goes on; another slot: a fork; outside [0, S): nothing)
+ * and gets pages for new_lens[s] tokens (0: the slot is dropped). ref [pages]
+ * counts each page's holders (0: free). Whole kept pages are shared; a page
+ * that the kept tokens fill in part stays in place when it is the slot's own
+ * and no other slot's new row shares it, else it is copied to a fresh page;
+ * fresh pages are the free ones with the lowest numbers, given out slot by
+ * slot in order. References of the old rows end, so unshared pages of dropped
+ * or replaced sequences are free after the call (not for it). ref_out and
+ * table_out [S, W] (-1 past a row's pages) must not be ref or table; *shortage
+ * becomes the number of pages that were wanted and not there (their columns
+ * hold -1). Holders outside the table keep their counts.
+ */
+int64_t qmm_kv8_pages_work(int64_t pages);
+qmm_status qmm_kv8_update(const qmm_kv8_cache* cache, const int32_t* ref, const int32_t* table,
+                          const int32_t* lens, const int32_t* parent, const int32_t* new_lens,
+                          int64_t S, int64_t W, int32_t* ref_out, int32_t* table_out,
+                          int32_t* shortage, void* work, int64_t work_bytes, void* stream);
+
+/*
+ * Pack the pages in use to the front of the cache: with *used of them, the
+ * i-th page in use at or past *used moves into the i-th free page below it.
+ * remap [pages] gives each page's new number (-1: it was free); table_out
+ * (which may be table) and ref_out (not ref) are the table and the counts
+ * after the move.
+ */
+qmm_status qmm_kv8_compact(const qmm_kv8_cache* cache, const int32_t* ref, const int32_t* table,
+                           int64_t S, int64_t W, int32_t* ref_out, int32_t* table_out,
+                           int32_t* remap, int32_t* used, void* work, int64_t work_bytes,
+                           void* stream);
+
+/*
+ * Copy pages src[i] of one cache to pages dst[i] of another of the same page
+ * shape (or the same cache), codes and scales. The dst are distinct and none
+ * of them is also a src of the same cache; pairs with a number outside their
+ * cache are left out.
+ */
+qmm_status qmm_kv8_copy(const qmm_kv8_cache* to, const int32_t* dst, const qmm_kv8_cache* from,
+                        const int32_t* src, int64_t n, void* stream);
+
 /* Message for the last non-OK status returned on the calling thread. */
 const char* qmm_last_error(void);
 

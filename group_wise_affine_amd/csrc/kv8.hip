@@ -22,9 +22,9 @@ __global__ __launch_bounds__(256) void kv8_append_kernel(Kv8 c, Kv8Seqs q,
   __shared__ uint32_t top_k[4], top_v[4];
   const int tid = threadIdx.x, head = blockIdx.y;
   const int B = 1 << c.bt_log2, D = c.dim, D8 = D / 8;
-  const int s = find_seq(q, blockIdx.x, c.bt_log2, 2);
+  const int s = find_seq(q, blockIdx.x, B, 2);
   const int64_t t0 = q.first(s), n = q.count(s), len = q.length(s, c.bt_log2);
-  const int64_t item = blockIdx.x - ((t0 >> c.bt_log2) + 2 * (int64_t)s);
+  const int64_t item = blockIdx.x - first_item(q, s, B, 2);
   // a sequence whose tokens cannot be placed (fewer places than tokens) gets
   // its last `len` ones
   const int64_t begin = len - n > 0 ? len - n : 0;

@@ -10,8 +10,9 @@
 //
 // Both products run on the f16 matrix units: codes are exact in f16, queries
 // too (bf16 rows are first scaled by a power of two), so only the weights
-// exp(x - m) * vs are rounded to 11 bits on their way into the second
-// product; sums, maxima and the normaliser stay in fp32.
+// exp(x - m) * vs are rounded on their way into the second product (to 11
+// bits for bf16 results, to two f16 terms for f16 ones); sums, maxima and the
+// normaliser stay in fp32.
 #include "kernels.hpp"
 #include "kv8_common.hpp"
 
@@ -28,8 +29,10 @@ struct AttnArgs {
   const uint16_t* x;   // queries, row t at x + t * ldq
   int64_t ldq;
   int G;               // query heads per cache head, 16 at a time
-  int rows_log2, extra;   // new tokens per workgroup, spare items per sequence
-  float scale;         // of the scores, times log2 e
+  int unit, extra;     // new tokens per workgroup, spare items per sequence
+  int many;            // sequences with more query rows than this are the prompt kernel's
+  float scale;         // magnitude of the scores' scale, times log2 e
+  uint32_t flip;       // its sign, as the sign bits of two queries
   uint16_t* out;       // [T][heads * G][D]
   float* lse;          // [T][heads * G] or null
   int splits;          // of a sequence's tiles, over gridDim.z workgroups
@@ -51,7 +54,31 @@ __device__ __forceinline__ half8_t codes_f16(uint32_t a, uint32_t b) {
   return __builtin_bit_cast(half8_t, make_uint4(r[0], r[1], r[2], r[3]));
 }
 
-__device__ __forceinline__ uint32_t max3(uint32_t a, uint32_t b) { return a > b ? a : b; }
+__device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
+
+__device__ __forceinline__ uint4 load_q(const uint16_t* p, uint32_t flip) {
+  const uint4 u = *reinterpret_cast<const uint4*>(p);
+  return make_uint4(u.x ^ flip, u.y ^ flip, u.z ^ flip, u.w ^ flip);
+}
+// bf16 queries: a row times 2^-e, 2^e the power of two below its largest
+// magnitude (bits m), is exact in f16 down to 2^-14 of that (fewer bits below)
+struct Pow2 {
+  float up, down;
+};
+__device__ __forceinline__ Pow2 row_power(uint32_t m) {
+  int e = (int)(m >> 7) - 127;
+  e = e < -100 ? -100 : e > 100 ? 100 : e;
+  return {__builtin_bit_cast(float, (uint32_t)(127 + e) << 23),
+          __builtin_bit_cast(float, (uint32_t)(127 - e) << 23)};
+}
+__device__ __forceinline__ half8_t bf16_to_f16(const uint4& u, float down) {
+  float f[8];
+  unpack8(BF16{}, u, f);
+  half8_t r;
+#pragma unroll
+  for (int i = 0; i < 8; i++) r[i] = (_Float16)(f[i] * down);
+  return r;
+}
 
 // ------------------------------------------------------------------- decode
 // Up to 16 query rows (tokens x heads of one group) per workgroup, NW
@@ -68,19 +95,21 @@ __device__ __forceinline__ uint32_t max3(uint32_t a, uint32_t b) { return a > b 
 template <class T, int D, int NW>
 __global__ __launch_bounds__(64 * NW) void kv8_decode_kernel(AttnArgs a) {
   constexpr int KD = D / 64, VD = D / 16;
+  // f16 results: the weights go in as two f16 terms, since 11 bits of them would
+  // cost as much as rounding the result
+  constexpr bool kTwo = __is_same(T, F16);
   const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
   const int col = lane % 16, g = lane / 16;
   const int blocks = (a.G + 15) / 16;   // of heads in a group
   const int head = blockIdx.y / blocks, h0 = blockIdx.y % blocks * 16, split = blockIdx.z;
   const int G = min(16, a.G - h0);
   const Kv8& c = a.c;
-  const int s = find_seq(a.q, blockIdx.x, a.rows_log2, a.extra);
+  const int s = find_seq(a.q, blockIdx.x, a.unit, a.extra);
   const int64_t t0 = a.q.first(s), n = a.q.count(s), len = a.q.length(s, c.bt_log2);
-  const int64_t item = blockIdx.x - ((t0 >> a.rows_log2) + (int64_t)a.extra * s);
-  const int tok = 1 << a.rows_log2;          // new tokens per workgroup
-  const int64_t i0 = item << a.rows_log2;
-  if (item < 0 || i0 >= n) return;
-  const int ntok = n - i0 < tok ? (int)(n - i0) : tok;
+  const int64_t item = blockIdx.x - first_item(a.q, s, a.unit, a.extra);
+  const int64_t i0 = item * a.unit;
+  if (item < 0 || i0 >= n || n * a.G > a.many) return;
+  const int ntok = n - i0 < a.unit ? (int)(n - i0) : a.unit;
   const int rows = ntok * G;                 // <= 16
   // positions that the last row sees, tiles of them, this workgroup's share
   const int64_t most = len - n + i0 + ntok;
@@ -107,7 +136,7 @@ __global__ __launch_bounds__(64 * NW) void kv8_decode_kernel(AttnArgs a) {
     for (int b = 0; b < KD; b++)
 #pragma unroll
       for (int h = 0; h < 2; h++) {
-        u[b][h] = *reinterpret_cast<const uint4*>(qr + b * 64 + h * 8);
+        u[b][h] = load_q(qr + b * 64 + h * 8, a.flip);
         m = amax_pair(amax_pair(amax_pair(amax_pair(m, u[b][h].x), u[b][h].y), u[b][h].z), u[b][h].w);
       }
     if constexpr (__is_same(T, F16)) {
@@ -116,24 +145,15 @@ __global__ __launch_bounds__(64 * NW) void kv8_decode_kernel(AttnArgs a) {
 #pragma unroll
         for (int h = 0; h < 2; h++) qf[b][h] = __builtin_bit_cast(half8_t, u[b][h]);
     } else {
-      // bf16: times 2^-e with 2^e the row's largest power of two, exact in
-      // f16 down to 2^-14 of it (and to 2^-24 with fewer bits)
       m = amax_halves(m);
-      m = max3(m, (uint32_t)__shfl_xor((int)m, 16));
-      m = max3(m, (uint32_t)__shfl_xor((int)m, 32));
-      int e = (int)(m >> 7) - 127;
-      e = e < -100 ? -100 : e > 100 ? 100 : e;
-      const float down = __builtin_bit_cast(float, (uint32_t)(127 - e) << 23);
-      qs *= __builtin_bit_cast(float, (uint32_t)(127 + e) << 23);
+      m = umax(m, (uint32_t)__shfl_xor((int)m, 16));
+      m = umax(m, (uint32_t)__shfl_xor((int)m, 32));
+      const Pow2 e = row_power(m);
+      qs *= e.up;
 #pragma unroll
       for (int b = 0; b < KD; b++)
 #pragma unroll
-        for (int h = 0; h < 2; h++) {
-          float f[8];
-          unpack8(BF16{}, u[b][h], f);
-#pragma unroll
-          for (int i = 0; i < 8; i++) qf[b][h][i] = (_Float16)(f[i] * down);
-        }
+        for (int h = 0; h < 2; h++) qf[b][h] = bf16_to_f16(u[b][h], e.down);
     }
   }
 
@@ -216,7 +236,7 @@ __global__ __launch_bounds__(64 * NW) void kv8_decode_kernel(AttnArgs a) {
       v_exp = ve;
     }
     const float r = ldexpf(vs, -v_exp);
-    half8_t pf[2];
+    half8_t pf[2], pl[2];
 #pragma unroll
     for (int i = 0; i < 16; i++) {
       const float e = __builtin_amdgcn_exp2f(p[i] - mu);
@@ -224,13 +244,16 @@ __global__ __launch_bounds__(64 * NW) void kv8_decode_kernel(AttnArgs a) {
       float w = e * r;
       if (!whole) w = i <= left ? w : 0.0f;
       pf[i / 8][i % 8] = (_Float16)w;
+      if constexpr (kTwo) pl[i / 8][i % 8] = (_Float16)(w - (float)pf[i / 8][i % 8]);
     }
 #pragma unroll
     for (int i = 0; i < VD; i++)
 #pragma unroll
-      for (int h = 0; h < 2; h++)
-        o[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes_f16(vw[i][2 * h], vw[i][2 * h + 1]),
-                                                      pf[h], o[i], 0, 0, 0);
+      for (int h = 0; h < 2; h++) {
+        const half8_t vf = codes_f16(vw[i][2 * h], vw[i][2 * h + 1]);
+        o[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, pf[h], o[i], 0, 0, 0);
+        if constexpr (kTwo) o[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, pl[h], o[i], 0, 0, 0);
+      }
   }
   l_run += __shfl_xor(l_run, 16);
   l_run += __shfl_xor(l_run, 32);
@@ -313,19 +336,297 @@ __global__ __launch_bounds__(64 * NW) void kv8_decode_kernel(AttnArgs a) {
   }
 }
 
+// ------------------------------------------------------------------ prompts
+// 32 query rows per wavefront, NW wavefronts, tiles of 64 tokens through two
+// LDS buffers. The codes are turned into f16 once per workgroup on their way
+// into LDS (keys [64][D], rows in the order in which the products want them;
+// values [D][64]); the 16-byte pieces of a row are permuted by an exclusive-or
+// with the row number, so that the 16 rows that are read together touch all
+// banks.
+//
+// S^T = K Q^T with v_mfma_f32_32x32x16_f16; D row 8 i + 4 h + r of lane half h
+// is made token 16 (i/2) + 8 h + 4 (i%2) + r, so that a lane's registers are,
+// eight by eight, the B operand of O^T = V^T P^T. A page's scales are uniform
+// over groups of 16 tokens, hence scalars. The running maximum is only raised
+// when it grows by more than 2^8: until then weights reach 256, which f16 and
+// the fp32 sums hold as well, and nothing is rescaled.
+template <class T, int D, int NW>
+__global__ __launch_bounds__(64 * NW) void kv8_prompt_kernel(AttnArgs a) {
+  constexpr int KS = D / 16, VD = D / 32, kThreads = 64 * NW;
+  constexpr int kUnits = kTile * D / 16 / kThreads;   // 16 codes per unit
+  // f16 results: the weights go in as two f16 terms, since 11 bits of them would
+  // cost as much as rounding the result
+  constexpr bool kTwo = __is_same(T, F16);
+  static_assert(kUnits >= 1, "a unit per thread");
+  __shared__ __attribute__((aligned(16))) uint16_t lk[2][kTile * D], lv[2][kTile * D];
+  __shared__ float lsk[2][4], lsv[2][4];
+  // position of 16-byte piece p of key row r (rows of D * 2 bytes)
+  auto key_piece = [](int r, int p) QMM_INLINE {
+    return (p ^ (D == 64 ? r >> 1 : r)) & (D / 8 - 1);
+  };
+  const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
+  const int col = lane % 32, h = lane / 32;
+  const int head = blockIdx.y;
+  const Kv8& c = a.c;
+  // long sequences' last items have most to do: they come first
+  const int64_t index = (int64_t)gridDim.x - 1 - blockIdx.x;
+  const int s = find_seq(a.q, index, a.unit, a.extra);
+  const int64_t t0 = a.q.first(s), n = a.q.count(s), len = a.q.length(s, c.bt_log2);
+  const int64_t item = index - first_item(a.q, s, a.unit, a.extra);
+  const int64_t i0 = item * a.unit;
+  if (item < 0 || i0 >= n || n * a.G <= a.many) return;
+  const int ntok = n - i0 < a.unit ? (int)(n - i0) : a.unit;
+  const int rows = ntok * a.G;
+  const int64_t most = len - n + i0 + ntok;
+  const int tiles = most > 0 ? (int)((most + kTile - 1) / kTile) : 0;
+
+  // this lane's query row; rows past the last repeat it, and nothing reads them
+  const int rr = min(wave * 32 + col, rows - 1);
+  const int ct = rr / a.G, ch = rr % a.G;
+  const int64_t limit = len - n + i0 + ct;
+  const int64_t wave_min = len - n + i0 + min(wave * 32, rows - 1) / a.G;
+  const int64_t wave_max = len - n + i0 + min(wave * 32 + 31, rows - 1) / a.G;
+  const int64_t at = (t0 + i0 + ct) * (c.heads * a.G) + head * a.G + ch;
+  half8_t qf[KS];
+  float qs = a.scale;
+  {
+    const uint16_t* qr = a.x + (t0 + i0 + ct) * a.ldq + (int64_t)(head * a.G + ch) * D + h * 8;
+    uint4 u[KS];
+#pragma unroll
+    for (int i = 0; i < KS; i++) u[i] = load_q(qr + i * 16, a.flip);
+    if constexpr (__is_same(T, F16)) {
+#pragma unroll
+      for (int i = 0; i < KS; i++) qf[i] = __builtin_bit_cast(half8_t, u[i]);
+    } else {
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < KS; i++)
+        m = amax_pair(amax_pair(amax_pair(amax_pair(m, u[i].x), u[i].y), u[i].z), u[i].w);
+      m = amax_halves(m);
+      m = umax(m, (uint32_t)__shfl_xor((int)m, 32));
+      const Pow2 e = row_power(m);
+      qs *= e.up;
+#pragma unroll
+      for (int i = 0; i < KS; i++) qf[i] = bf16_to_f16(u[i], e.down);
+    }
+  }
+  float16_t o[VD];
+#pragma unroll
+  for (int i = 0; i < VD; i++)
+#pragma unroll
+    for (int e = 0; e < 16; e++) o[i][e] = 0.0f;
+  float m_run = -__builtin_inff(), l_run = 0.0f;
+  int v_exp = -126;   // O holds sums of codes weighted with p * vs / 2^v_exp
+
+  const int32_t* row = a.q.table + (int64_t)s * a.q.W;
+  const int bt = c.bt_log2;
+  auto page_at = [&](int64_t t) QMM_INLINE {
+    const int64_t j = t >> bt;
+    const int p = j < a.q.W && t < most ? row[j] : -1;
+    return p < c.pages ? p : -1;
+  };
+  // Each tile's pages are looked up two tiles ahead and its codes and scales
+  // loaded one tile ahead, so that no step waits for a load it has just asked
+  // for. Unit u of a thread: 16 columns of key token u / (D/16), 16 tokens of
+  // value column u / 4; threads 0 .. 3 carry the scales of their 16 tokens.
+  int kp[kUnits], vp[kUnits];
+  auto look_up = [&](int tile) QMM_INLINE {
+#pragma unroll
+    for (int i = 0; i < kUnits; i++) {
+      const int u = i * kThreads + tid;
+      kp[i] = page_at((int64_t)tile * kTile + u / (D / 16));
+      vp[i] = page_at((int64_t)tile * kTile + u % 4 * 16);
+    }
+  };
+  u32x4_t kw[kUnits], vw[kUnits];
+  float sk = 0, sv = 0;
+  bool miss = false;
+  auto fetch = [&]() QMM_INLINE {
+    if (tid < 4) {
+      miss = vp[0] < 0;
+      const int64_t blk = (int64_t)(miss ? 0 : vp[0]) * c.heads + head;
+      sk = c.ks[blk];
+      sv = c.vs[blk];
+    }
+#pragma unroll
+    for (int i = 0; i < kUnits; i++) {
+      const int u = i * kThreads + tid;
+      const int tk = u / (D / 16), kc = u % (D / 16), vd = u / 4, vc = u % 4 * 16;
+      kw[i] = *reinterpret_cast<const u32x4_t*>(c.k + c.block(kp[i] < 0 ? 0 : kp[i], head) +
+                                                (tk & ((1 << bt) - 1)) * D + kc * 16);
+      vw[i] = *reinterpret_cast<const u32x4_t*>(c.v + c.block(vp[i] < 0 ? 0 : vp[i], head) +
+                                                ((int64_t)vd << bt) + (vc & ((1 << bt) - 1)));
+    }
+  };
+  auto put = [&](int buf) QMM_INLINE {
+    if (tid < 4) {
+      lsk[buf][tid] = sk;
+      lsv[buf][tid] = miss ? -1.0f : sv;   // no scale is negative: not seen
+    }
+#pragma unroll
+    for (int i = 0; i < kUnits; i++) {
+      const int u = i * kThreads + tid;
+      const int tk = u / (D / 16), kc = u % (D / 16);
+      const int kr = (tk & 32) + 8 * ((tk >> 4 & 1) * 2 + (tk >> 2 & 1)) + 4 * (tk >> 3 & 1) + (tk & 3);
+      const int vd = u / 4, vc = u % 4;
+#pragma unroll
+      for (int j = 0; j < 2; j++) {
+        *reinterpret_cast<half8_t*>(&lk[buf][kr * D + key_piece(kr, kc * 2 + j) * 8]) =
+            codes_f16(kw[i][2 * j], kw[i][2 * j + 1]);
+        *reinterpret_cast<half8_t*>(&lv[buf][vd * kTile + (((vc * 2 + j) ^ vd >> 1) & 7) * 8]) =
+            codes_f16(vw[i][2 * j], vw[i][2 * j + 1]);
+      }
+    }
+  };
+  // one tile's softmax and second product; MASK: some of its tokens are not
+  // seen by some of the wavefront's rows
+  auto weigh = [&]<bool MASK>(float16_t* sc, const float* f, const float* vs, int ve, int left,
+                              uint32_t missing, int buf) QMM_INLINE {
+    // element e of sc[j]: token 32 j + 16 (e/8) + 8 h + e%8
+    float mx = -__builtin_inff();
+#pragma unroll
+    for (int g = 0; g < 4; g++) {
+      float top = -__builtin_inff();
+#pragma unroll
+      for (int e = 0; e < 8; e++) {
+        float x = sc[g / 2][g % 2 * 8 + e];
+        if constexpr (MASK) {
+          x = g * 16 + e <= left && !(missing >> g & 1) ? x * f[g] : -__builtin_inff();
+          sc[g / 2][g % 2 * 8 + e] = x;
+        }
+        top = fmaxf(top, x);
+      }
+      mx = fmaxf(mx, MASK ? top : top * f[g]);
+    }
+    mx = fmaxf(mx, __shfl_xor(mx, 32));
+    if (__any(mx > m_run + 8.0f || ve != v_exp)) {
+      const float mn = fmaxf(m_run, mx);
+      const float al = mn == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(m_run - mn);
+      const float down = ldexpf(al, v_exp - ve);
+      l_run *= al;
+#pragma unroll
+      for (int i = 0; i < VD; i++) o[i] *= down;
+      m_run = mn;
+      v_exp = ve;
+    }
+    const float mu = m_run == -__builtin_inff() ? 0.0f : m_run;
+#pragma unroll
+    for (int g = 0; g < 4; g++) {
+      const float r = ldexpf(vs[g], -v_exp);
+      half8_t hi, lo;
+#pragma unroll
+      for (int e = 0; e < 8; e++) {
+        const float x = sc[g / 2][g % 2 * 8 + e];
+        const float p = __builtin_amdgcn_exp2f(MASK ? x - mu : fmaf(x, f[g], -mu));
+        l_run += p;
+        float w = p * r;
+        if constexpr (MASK) w = g * 16 + e <= left && !(missing >> g & 1) ? w : 0.0f;
+        hi[e] = (_Float16)w;
+        if constexpr (kTwo) lo[e] = (_Float16)(w - (float)hi[e]);
+      }
+#pragma unroll
+      for (int i = 0; i < VD; i++) {
+        const int d = i * 32 + col;
+        const half8_t vf = *reinterpret_cast<const half8_t*>(
+            &lv[buf][d * kTile + (((g * 2 + h) ^ d >> 1) & 7) * 8]);
+        o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, hi, o[i], 0, 0, 0);
+        if constexpr (kTwo) o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, lo, o[i], 0, 0, 0);
+      }
+    }
+  };
+  if (tiles > 0) {
+    look_up(0);
+    fetch();
+    look_up(1);
+    put(0);
+  }
+  for (int tile = 0; tile < tiles; tile++) {
+    const int buf = tile & 1;
+    __syncthreads();
+    if (tile + 1 < tiles) {
+      fetch();
+      look_up(tile + 2);
+    }
+    const int64_t base = (int64_t)tile * kTile;
+    if (base <= wave_max) {
+      float f[4], vs[4];
+      int ve = v_exp;
+      uint32_t missing = 0;
+#pragma unroll
+      for (int g = 0; g < 4; g++) {
+        f[g] = lsk[buf][g] * qs;
+        vs[g] = lsv[buf][g];
+        const int e = (int)(__builtin_bit_cast(uint32_t, vs[g]) >> 23 & 255) - 127;
+        const bool gone = __builtin_bit_cast(uint32_t, vs[g]) == 0xbf800000u;
+        if (!gone && e <= 127) ve = max(ve, e);   // NaN and infinity leave it
+        missing |= gone ? 1u << g : 0u;
+      }
+      float16_t sc[2];
+#pragma unroll
+      for (int j = 0; j < 2; j++)
+#pragma unroll
+        for (int e = 0; e < 16; e++) sc[j][e] = 0.0f;
+#pragma unroll
+      for (int ks = 0; ks < KS; ks++)
+#pragma unroll
+        for (int j = 0; j < 2; j++) {
+          const int r = j * 32 + col;
+          const half8_t kf =
+              *reinterpret_cast<const half8_t*>(&lk[buf][r * D + key_piece(r, ks * 2 + h) * 8]);
+          sc[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, qf[ks], sc[j], 0, 0, 0);
+        }
+      const int64_t far = limit - base - h * 8;   // tokens g * 16 + e up to this are seen
+      const int left = (int)(far < 64 ? far < 0 ? -1 : far : 64);
+      if (base + kTile - 1 <= wave_min && missing == 0)
+        weigh.template operator()<false>(sc, f, vs, ve, left, missing, buf);
+      else
+        weigh.template operator()<true>(sc, f, vs, ve, left, missing, buf);
+    }
+    if (tile + 1 < tiles) put(buf ^ 1);
+  }
+  if (wave * 32 + col >= rows) return;
+  l_run += __shfl_xor(l_run, 32);
+  const bool any = l_run > 0.0f || l_run != l_run;
+  const float back = any ? ldexpf(1.0f, v_exp) / l_run : 0.0f;
+#pragma unroll
+  for (int i = 0; i < VD; i++)
+#pragma unroll
+    for (int q = 0; q < 4; q++) {
+      uint16_t w[4];
+#pragma unroll
+      for (int e = 0; e < 4; e++) w[e] = from_f32(T{}, any ? o[i][q * 4 + e] * back : 0.0f);
+      *reinterpret_cast<uint2*>(a.out + at * D + i * 32 + q * 8 + h * 4) =
+          make_uint2(w[0] | (uint32_t)w[1] << 16, w[2] | (uint32_t)w[3] << 16);
+    }
+  if (h == 0 && a.lse) a.lse[at] = any ? fmaf(m_run, kLn2, logf(l_run)) : -__builtin_inff();
+}
+
+// Sequences with at most this many query rows (new tokens x heads of a group)
+// go to the decode kernel, 16 rows at a time; the others to the prompt kernel.
+constexpr int kFewRows = 64;
+
 struct Plan {
-  int rows_log2, extra, splits, nw;
+  int unit, extra, splits, nw, many;
   int64_t items, columns;   // grid: items x heads and blocks of a group's heads
+  bool prompts;
+  int p_unit;
+  int64_t p_items;
 };
 
 Plan plan(const Kv8& c, int64_t T, int64_t Hq, int64_t S, int64_t W) {
   Plan p{};
   const int64_t G = Hq / c.heads;
-  p.rows_log2 = 0;
-  while (2 * G << p.rows_log2 <= 16 && (T >> p.rows_log2) > S) p.rows_log2++;
-  p.extra = p.rows_log2 > 0 ? 1 : 0;
-  p.items = (T >> p.rows_log2) + p.extra * S;
+  const int prompt_rows = c.dim == 128 ? 256 : 128;
+  // the packed batch says how many new tokens a sequence can have at most
+  const int64_t longest = T;
+  p.prompts = longest * G > kFewRows && T > S && G <= prompt_rows;
+  p.many = p.prompts ? kFewRows : INT32_MAX;
+  p.unit = T > S && G <= 8 ? (int)(16 / G) : 1;
+  p.extra = p.unit > 1 ? 1 : 0;
+  p.items = T / p.unit + p.extra * S;
   p.columns = c.heads * ((G + 15) / 16);
+  p.p_unit = (int)(prompt_rows / (G < prompt_rows ? G : prompt_rows));
+  p.p_items = T / p.p_unit + S;
   p.nw = c.dim == 256 ? 4 : 8;
   const int64_t units = (T < p.items ? T : p.items) * p.columns;
   const int64_t tiles = ((W << c.bt_log2) + kTile - 1) / kTile;
@@ -353,12 +654,19 @@ hipError_t launch_kv8_attention(const Kv8& c, int dt, const void* q, int64_t ldq
                                 float* lse, unsigned* cnt, float* ws, hipStream_t st) {
   const Plan p = plan(c, T, Hq, S, W);
   AttnArgs a{c, {table, lens, cu, (int)S, (int)W, T}, static_cast<const uint16_t*>(q), ldq,
-             (int)(Hq / c.heads), p.rows_log2, p.extra, scale * kLog2e, static_cast<uint16_t*>(out), lse,
-             p.splits, ws, cnt};
+             (int)(Hq / c.heads), p.unit, p.extra, p.many, fabsf(scale) * kLog2e,
+             scale < 0 ? 0x80008000u : 0u, static_cast<uint16_t*>(out), lse, p.splits, ws, cnt};
   const dim3 grid((unsigned)p.items, (unsigned)p.columns, (unsigned)p.splits);
   auto go = [&]<class T_, int D, int NW>() {
     const size_t lds = (size_t)NW * 16 * D * 4;
     hipLaunchKernelGGL((kv8_decode_kernel<T_, D, NW>), grid, dim3(64 * NW), lds, st, a);
+    if (!p.prompts) return;
+    AttnArgs b = a;
+    b.unit = p.p_unit;
+    b.extra = 1;
+    hipLaunchKernelGGL((kv8_prompt_kernel<T_, D, D == 256 ? 4 : D == 128 ? 8 : 4>),
+                       dim3((unsigned)p.p_items, (unsigned)c.heads), dim3(D == 128 ? 512 : 256), 0,
+                       st, b);
   };
   auto by_dim = [&]<class T_>() {
     if (c.dim == 64) go.template operator()<T_, 64, 8>();

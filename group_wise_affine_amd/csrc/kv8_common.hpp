@@ -43,14 +43,17 @@ struct Kv8Seqs {
   }
 };
 
-// Work items of a ragged batch: sequence s owns items cu[s] / unit + extra * s
-// .. cu[s+1] / unit + extra * (s+1), at least count / unit + extra of them.
-// Returns the sequence that owns item i (binary search).
-__device__ __forceinline__ int find_seq(const Kv8Seqs& q, int64_t i, int unit_log2, int extra) {
+// Work items of a ragged batch, `unit` new tokens each: sequence s owns items
+// cu[s] / unit + extra * s .. cu[s+1] / unit + extra * (s+1), at least count /
+// unit + extra of them. Returns the sequence that owns item i (binary search).
+__device__ __forceinline__ int64_t first_item(const Kv8Seqs& q, int s, int unit, int extra) {
+  return (uint32_t)q.first(s) / (uint32_t)unit + (int64_t)extra * s;   // T < 2^32
+}
+__device__ __forceinline__ int find_seq(const Kv8Seqs& q, int64_t i, int unit, int extra) {
   int lo = 0, hi = q.S;   // the item belongs to a sequence in [lo, hi)
   while (hi - lo > 1) {
     const int mid = (lo + hi) / 2;
-    if ((q.first(mid) >> unit_log2) + (int64_t)extra * mid <= i) lo = mid;
+    if (first_item(q, mid, unit, extra) <= i) lo = mid;
     else hi = mid;
   }
   return lo;

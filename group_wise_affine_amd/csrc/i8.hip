@@ -144,9 +144,9 @@ __global__ __launch_bounds__(64 * kGvWaves) void i8_gemv_kernel(
 
 // ---------------------------------------------------------------- tile GEMM
 // BM rows of x by BN rows of W per workgroup, WM x WN wavefronts. K advances
-// in steps of 128 bytes through a ring of NS LDS slots filled by direct
+// in steps of 128 bytes through two LDS slots filled by direct
 // global-to-LDS copies; inside a slot row r's 16-byte piece c sits at
-// position c ^ (r & 7), so the eight rows that are read together touch all
+// position c ^ (r / 2 & 7), so the 16 rows that are read together touch all
 // banks. W is the A operand, so a lane ends up with runs of four consecutive
 // n of one row of y.
 struct I8Args {
@@ -172,15 +172,88 @@ __device__ __forceinline__ void ring_wait() {
   asm volatile("" ::: "memory");
 }
 
-template <class T, int BM, int BN, int WM, int WN, int NS>
-__global__ __launch_bounds__(64 * WM * WN) void i8_tile_kernel(I8Args a) {
+// Operand reads of one 32-byte K piece: TN pieces of W and TM of x, 32 rows
+// (4096 bytes) apart in LDS.
+//
+// The reads are assembly, because before any LDS read of its own the compiler
+// waits for every global-to-LDS copy in flight, which the ring is there to keep
+// flying. Each block waits for what it reads. multiply_read() puts the reads
+// of the next piece between the products of the present one, so that their
+// wait at the block's end finds them done.
+template <int R>
+struct Operands {
+  u32x4_t a[R], b[R];
+};
+#define QMM_LD(d, p, o) "ds_read_b128 %[" #d "], %[" #p "] offset:" #o "\n\t"
+#define QMM_MM(i, j) "v_mfma_i32_32x32x32_i8 %[c" #i #j "], %[a" #i "], %[b" #j "], %[c" #i #j "]\n\t"
+__device__ __forceinline__ void read_operands(uint32_t pa, uint32_t pb, Operands<2>& n) {
+  asm volatile(QMM_LD(na0, pa, 0) QMM_LD(nb0, pb, 0) QMM_LD(na1, pa, 4096) QMM_LD(nb1, pb, 4096)
+               "s_waitcnt lgkmcnt(0)"
+               : [na0] "=&v"(n.a[0]), [na1] "=&v"(n.a[1]), [nb0] "=&v"(n.b[0]), [nb1] "=&v"(n.b[1])
+               : [pa] "v"(pa), [pb] "v"(pb)
+               : "memory");
+}
+__device__ __forceinline__ void read_operands(uint32_t pa, uint32_t pb, Operands<4>& n) {
+  asm volatile(QMM_LD(na0, pa, 0) QMM_LD(nb0, pb, 0) QMM_LD(na1, pa, 4096) QMM_LD(nb1, pb, 4096)
+               QMM_LD(na2, pa, 8192) QMM_LD(nb2, pb, 8192) QMM_LD(na3, pa, 12288)
+               QMM_LD(nb3, pb, 12288) "s_waitcnt lgkmcnt(0)"
+               : [na0] "=&v"(n.a[0]), [na1] "=&v"(n.a[1]), [na2] "=&v"(n.a[2]), [na3] "=&v"(n.a[3]),
+                 [nb0] "=&v"(n.b[0]), [nb1] "=&v"(n.b[1]), [nb2] "=&v"(n.b[2]), [nb3] "=&v"(n.b[3])
+               : [pa] "v"(pa), [pb] "v"(pb)
+               : "memory");
+}
+__device__ __forceinline__ void multiply_read(int16v_t (&c)[2][2], const Operands<2>& u,
+                                              uint32_t pa, uint32_t pb, Operands<2>& n) {
+  asm volatile(QMM_MM(0, 0) QMM_LD(na0, pa, 0) QMM_LD(nb0, pb, 0)
+               QMM_MM(0, 1) QMM_LD(na1, pa, 4096) QMM_LD(nb1, pb, 4096)
+               QMM_MM(1, 0) QMM_MM(1, 1) "s_waitcnt lgkmcnt(0)"
+               : [c00] "+a"(c[0][0]), [c01] "+a"(c[0][1]), [c10] "+a"(c[1][0]), [c11] "+a"(c[1][1]),
+                 [na0] "=&v"(n.a[0]), [na1] "=&v"(n.a[1]), [nb0] "=&v"(n.b[0]), [nb1] "=&v"(n.b[1])
+               : [a0] "v"(u.a[0]), [a1] "v"(u.a[1]), [b0] "v"(u.b[0]), [b1] "v"(u.b[1]),
+                 [pa] "v"(pa), [pb] "v"(pb)
+               : "memory");
+}
+__device__ __forceinline__ void multiply_read(int16v_t (&c)[4][4], const Operands<4>& u,
+                                              uint32_t pa, uint32_t pb, Operands<4>& n) {
+  asm volatile(QMM_MM(0, 0) QMM_LD(na0, pa, 0) QMM_MM(0, 1) QMM_LD(nb0, pb, 0)
+               QMM_MM(0, 2) QMM_LD(nb1, pb, 4096) QMM_MM(0, 3) QMM_LD(nb2, pb, 8192)
+               QMM_MM(1, 0) QMM_LD(nb3, pb, 12288) QMM_MM(1, 1) QMM_LD(na1, pa, 4096)
+               QMM_MM(1, 2) QMM_LD(na2, pa, 8192) QMM_MM(1, 3) QMM_LD(na3, pa, 12288)
+               QMM_MM(2, 0) QMM_MM(2, 1) QMM_MM(2, 2) QMM_MM(2, 3)
+               QMM_MM(3, 0) QMM_MM(3, 1) QMM_MM(3, 2) QMM_MM(3, 3) "s_waitcnt lgkmcnt(0)"
+               : [c00] "+a"(c[0][0]), [c01] "+a"(c[0][1]), [c02] "+a"(c[0][2]), [c03] "+a"(c[0][3]),
+                 [c10] "+a"(c[1][0]), [c11] "+a"(c[1][1]), [c12] "+a"(c[1][2]), [c13] "+a"(c[1][3]),
+                 [c20] "+a"(c[2][0]), [c21] "+a"(c[2][1]), [c22] "+a"(c[2][2]), [c23] "+a"(c[2][3]),
+                 [c30] "+a"(c[3][0]), [c31] "+a"(c[3][1]), [c32] "+a"(c[3][2]), [c33] "+a"(c[3][3]),
+                 [na0] "=&v"(n.a[0]), [na1] "=&v"(n.a[1]), [na2] "=&v"(n.a[2]), [na3] "=&v"(n.a[3]),
+                 [nb0] "=&v"(n.b[0]), [nb1] "=&v"(n.b[1]), [nb2] "=&v"(n.b[2]), [nb3] "=&v"(n.b[3])
+               : [a0] "v"(u.a[0]), [a1] "v"(u.a[1]), [a2] "v"(u.a[2]), [a3] "v"(u.a[3]),
+                 [b0] "v"(u.b[0]), [b1] "v"(u.b[1]), [b2] "v"(u.b[2]), [b3] "v"(u.b[3]),
+                 [pa] "v"(pa), [pb] "v"(pb)
+               : "memory");
+}
+// the products' results may be read: the compiler does not see them in the
+// assembly and would not leave the cycles that they need
+template <int R>
+__device__ __forceinline__ void settle(int16v_t (&c)[R][R]) {
+#pragma unroll
+  for (int i = 0; i < R; i++)
+#pragma unroll
+    for (int j = 0; j < R; j++) asm volatile("s_nop 15\n\ts_nop 15" : "+a"(c[i][j]));
+}
+#undef QMM_LD
+#undef QMM_MM
+
+template <class T, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN, BM * BN == 65536 ? 1 : 2) void i8_tile_kernel(I8Args a) {
   constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
   constexpr int TM = BM / WM / 32, TN = BN / WN / 32;   // 32x32 tiles per wavefront
   constexpr int kRows = BM + BN;
   constexpr int kLoads = kRows * 8 / kThreads;          // 16-byte pieces per thread and step
-  static_assert(BM * 8 % kThreads == 0 && BN * 8 % kThreads == 0, "copy shape");
-  __shared__ __attribute__((aligned(128))) uint8_t lds[NS][kRows * 128];
-  const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
+  static_assert(BM * 8 % kThreads == 0 && BN * 8 % kThreads == 0 && TM == TN, "shape");
+  __shared__ __attribute__((aligned(128))) uint8_t lds[2][kRows * 128];
+  const int tid = threadIdx.x, lane = tid % 64;
+  const int wave = __builtin_amdgcn_readfirstlane(tid / 64);   // uniform: scalar
   const int tiles_n = (a.N + BN - 1) / BN, tiles_m = (a.M + BM - 1) / BM;
   // The eight XCDs take workgroups in turn: give each a run of consecutive
   // tiles, walked in bands of 8 row tiles, so that the tiles an XCD works on
@@ -205,20 +278,20 @@ __global__ __launch_bounds__(64 * WM * WN) void i8_tile_kernel(I8Args a) {
   const int total = (a.K + 127) / 128;
   const int steps = total - split * a.steps < a.steps ? total - split * a.steps : a.steps;
 
-  // piece i of this thread: row (i * kThreads + tid) / 8 of [x rows | W rows]
-  const int c = (tid % 8) ^ (tid / 8 % 8);
+  // piece i of this thread: row (i * kThreads + tid) / 8 of [x rows | W rows];
+  // pieces past K are out of every row's range and become zeros
+  const int c = (tid % 8) ^ (tid / 16 % 8);
   auto copy = [&](int step) QMM_INLINE {
-    uint8_t* slot = lds[step % NS];
-    const int k = k_begin + step * 128 + c * 16;
-    const bool in_k = k < a.K;
+    uint8_t* slot = lds[step % 2];
+    const uint32_t k = (uint32_t)(k_begin + step * 128 + c * 16);
+    const uint32_t off = (tid / 8) * (uint32_t)a.K + (k < (uint32_t)a.K ? k : kOob);
 #pragma unroll
     for (int i = 0; i < kLoads; i++) {
       constexpr int kX = BM * 8 / kThreads;
-      const int rr = (i * kThreads + tid) / 8 - (i < kX ? 0 : BM);
-      const uint32_t off = in_k ? (uint32_t)rr * (uint32_t)a.K + (uint32_t)k : kOob;
+      const int row = (i < kX ? i : i - kX) * (kThreads / 8);
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          i < kX ? rx : rw, (lds_ptr_t*)(slot + (i * kThreads + wave * 64) * 16), 16, (int)off, 0,
-          0, 0);
+          i < kX ? rx : rw, (lds_ptr_t*)(slot + (i * kThreads + wave * 64) * 16), 16,
+          (int)(off + (uint32_t)row * (uint32_t)a.K), 0, 0, 0);
     }
   };
   int16v_t acc[TN][TM];
@@ -230,38 +303,39 @@ __global__ __launch_bounds__(64 * WM * WN) void i8_tile_kernel(I8Args a) {
       for (int e = 0; e < 16; e++) acc[i][j][e] = 0;
   const int wm = wave % WM, wn = wave / WM;
   const int lr = lane % 32, lh = lane / 32;
-#pragma unroll
-  for (int s = 0; s < NS - 1; s++) copy(s);   // past the last step: zeros or unused
+  // LDS byte addresses of this lane's operand rows; the permuted position of
+  // a K piece depends on the row's low bits only, which are the same for all
+  // of a wavefront's tiles
+  const uint32_t base = (uint32_t)(uintptr_t)(lds_ptr_t*)&lds[0][0];
+  const uint32_t at_x = base + (uint32_t)(wm * TM * 32 + lr) * 128;
+  const uint32_t at_w = base + (uint32_t)(BM + wn * TN * 32 + lr) * 128;
+  auto piece = [&](int step, int ks) QMM_INLINE {
+    return (uint32_t)(step % 2) * (kRows * 128) + (uint32_t)(((ks * 2 + lh) ^ (lr >> 1)) & 7) * 16;
+  };
+  Operands<TN> u[2];
+  copy(0);
+  ring_wait<0>();
+  copy(1);   // past the last step: zeros, or the next split's, and unused
+  read_operands(at_w + piece(0, 0), at_x + piece(0, 0), u[0]);
   for (int step = 0; step < steps; step++) {
-    // the copies of the NS - 2 later steps may still be in flight
-    ring_wait<(NS - 2) * kLoads>();
-    copy(step + NS - 1);
-    const uint8_t* slot = lds[step % NS];
 #pragma unroll
     for (int ks = 0; ks < 4; ks++) {
-      u32x4_t fa[TN], fb[TM];
-      auto frag = [&](int row) QMM_INLINE {
-        return *reinterpret_cast<const u32x4_t*>(slot + row * 128 +
-                                                 (((ks * 2 + lh) ^ (row & 7)) * 16));
-      };
-#pragma unroll
-      for (int j = 0; j < TM; j++) fb[j] = frag((wm * TM + j) * 32 + lr);
-#pragma unroll
-      for (int i = 0; i < TN; i++) fa[i] = frag(BM + (wn * TN + i) * 32 + lr);
-#pragma unroll
-      for (int i = 0; i < TN; i++)
-#pragma unroll
-        for (int j = 0; j < TM; j++)
-          acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(
-              __builtin_bit_cast(int4_t, fa[i]), __builtin_bit_cast(int4_t, fb[j]), acc[i][j], 0,
-              0, 0);
+      if (ks == 3) {
+        // every wavefront has read the last piece of this step's slot, and the
+        // copies of the next step, issued one step ago, have landed
+        ring_wait<0>();
+        copy(step + 2);
+      }
+      const uint32_t p = ks < 3 ? piece(step, ks + 1) : piece(step + 1, 0);
+      multiply_read(acc, u[ks % 2], at_w + p, at_x + p, u[(ks + 1) % 2]);
     }
   }
+  settle(acc);
   __builtin_amdgcn_s_waitcnt(0);   // no copy is left in flight when LDS is given up
 
   // acc[i][j][e]: n = n0 + 32 * (wn * TN + i) + 8 * (e / 4) + 4 * lh + e % 4,
   //               m = m0 + 32 * (wm * TM + j) + lr
-  if (a.ks > 1) {
+  if (BM * BN < 65536 && a.ks > 1) {   // (many large tiles: never split)
     // every split leaves its tile in the workspace; the last to arrive adds
     // them (integer sums: the order does not matter). Relaxed agent-scope
     // accesses are coherent across the XCDs' L2 caches; the stores have
@@ -297,32 +371,68 @@ __global__ __launch_bounds__(64 * WM * WN) void i8_tile_kernel(I8Args a) {
                                               __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
   }
-  const bool quad = a.N % 4 == 0;   // four outputs start on 8 bytes
+  // Each wavefront turns its outputs round in LDS (its own TM * 32 rows of m
+  // by TN * 32 columns of n; the copies have drained), so that y is written in
+  // whole rows: 16-byte piece p of row r sits at p ^ r modulo the row's pieces.
+  constexpr int kRow = TN * 64, kPieces = kRow / 16;   // bytes, pieces of a row
+  __syncthreads();
+  uint8_t* mine = &lds[0][0] + wave * (TM * 32 * kRow);
+  auto at = [&](int r, int p) QMM_INLINE {
+    return mine + r * kRow + ((p ^ (kPieces == 8 ? r >> 1 : r)) & (kPieces - 1)) * 16;
+  };
+  const int nw = wn * TN * 32, mw = wm * TM * 32;   // within the tile
+  const __amdgpu_buffer_rsrc_t rs = make_rsrc(a.sw + n0, (uint32_t)wrows * 4);
+  float sm[TM];
 #pragma unroll
   for (int j = 0; j < TM; j++) {
-    const int64_t m = m0 + 32 * (wm * TM + j) + lr;
-    if (m >= a.M) continue;
-    const float sm = a.sx[m];
-    uint16_t* yr = a.y + m * a.N;
+    const int64_t m = m0 + mw + 32 * j + lr;
+    sm[j] = a.sx[m < a.M ? m : a.M - 1];
+  }
 #pragma unroll
-    for (int i = 0; i < TN; i++)
+  for (int i = 0; i < TN; i++) {
 #pragma unroll
-      for (int q = 0; q < 4; q++) {
-        const int64_t n = n0 + 32 * (wn * TN + i) + 8 * q + 4 * lh;
-        if (quad) {
-          if (n >= a.N) continue;
-          uint16_t o[4];
+    for (int q = 0; q < 4; q++) {
+      const int n = nw + 32 * i + 8 * q + 4 * lh;
+      const float4_t sn = __builtin_bit_cast(
+          float4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, n * 4, 0, 0));   // 0 past N
+      float bn[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      if (a.bias)
 #pragma unroll
-          for (int e = 0; e < 4; e++)
-            o[e] = i8_out<T>(acc[i][j][q * 4 + e], sm, a.sw[n + e], a.bias, n + e);
-          *reinterpret_cast<uint2*>(yr + n) =
-              make_uint2(o[0] | (uint32_t)o[1] << 16, o[2] | (uint32_t)o[3] << 16);
-        } else {
+        for (int e = 0; e < 4; e++)
+          bn[e] = to_f32(T{}, a.bias[n0 + n + e < a.N ? n0 + n + e : a.N - 1]);
 #pragma unroll
-          for (int e = 0; e < 4; e++)
-            if (n + e < a.N) yr[n + e] = i8_out<T>(acc[i][j][q * 4 + e], sm, a.sw[n + e], a.bias, n + e);
+      for (int j = 0; j < TM; j++) {
+        uint16_t o[4];
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+          const float s = sm[j] * sn[e], v = (float)acc[i][j][q * 4 + e];
+          o[e] = from_f32(T{}, a.bias ? fmaf(s, v, bn[e]) : s * v);
         }
+        *reinterpret_cast<uint2*>(at(32 * j + lr, i * 4 + q) + lh * 8) =
+            make_uint2(o[0] | (uint32_t)o[1] << 16, o[2] | (uint32_t)o[3] << 16);
       }
+    }
+  }
+  // rows of y start on 16, 4 or 2 bytes, as N allows
+  const int64_t n = n0 + nw + lane % kPieces * 8;
+  const int left = (int)(a.N - n < 8 ? a.N - n : 8);
+#pragma unroll 4
+  for (int r = lane / kPieces; r < TM * 32; r += 64 / kPieces) {
+    const int64_t m = m0 + mw + r;
+    if (m >= a.M || left <= 0) break;
+    const u32x4_t w = *reinterpret_cast<const u32x4_t*>(at(r, lane % kPieces));
+    uint16_t* yr = a.y + m * a.N + n;
+    if (a.N % 8 == 0) {
+      *reinterpret_cast<u32x4_t*>(yr) = w;
+    } else if (a.N % 2 == 0) {
+#pragma unroll
+      for (int e = 0; e < 4; e++)
+        if (2 * e < left) reinterpret_cast<uint32_t*>(yr)[e] = w[e];
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; e++)
+        if (e < left) yr[e] = (uint16_t)(w[e / 2] >> (16 * (e % 2)));
+    }
   }
 }
 
@@ -385,9 +495,9 @@ hipError_t launch_i8_t(int dt, const int8_t* xq, const float* sx, const int8_t* 
     I8Args a{xq, sx, wq, sw, b, yo, (int)M, (int)N, (int)K, (int)p.ks, (int)p.steps, ws, cnt};
     const dim3 grid((unsigned)p.tiles, (unsigned)p.ks);
     if (p.bm == 256)
-      hipLaunchKernelGGL((i8_tile_kernel<T, 256, 256, 2, 4, 2>), grid, dim3(512), 0, st, a);
+      hipLaunchKernelGGL((i8_tile_kernel<T, 256, 256, 2, 2>), grid, dim3(256), 0, st, a);
     else
-      hipLaunchKernelGGL((i8_tile_kernel<T, 128, 128, 2, 2, 2>), grid, dim3(256), 0, st, a);
+      hipLaunchKernelGGL((i8_tile_kernel<T, 128, 128, 2, 2>), grid, dim3(256), 0, st, a);
   };
   if (dt == 0) go.template operator()<F16>();
   else go.template operator()<BF16>();

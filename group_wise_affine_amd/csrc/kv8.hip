@@ -23,17 +23,17 @@ __global__ __launch_bounds__(256) void kv8_append_kernel(Kv8 c, Kv8Seqs q,
   const int tid = threadIdx.x, head = blockIdx.y;
   const int B = 1 << c.bt_log2, D = c.dim, D8 = D / 8;
   const int s = find_seq(q, blockIdx.x, B, 2);
-  const int64_t t0 = q.first(s), n = q.count(s), len = q.length(s, c.bt_log2);
-  const int64_t item = blockIdx.x - first_item(q, s, B, 2);
+  const int t0 = q.first(s), n = q.count(s), len = q.length(s, c.bt_log2);
+  const int item = blockIdx.x - first_item(q, s, B, 2);
   // a sequence whose tokens cannot be placed (fewer places than tokens) gets
   // its last `len` ones
-  const int64_t begin = len - n > 0 ? len - n : 0;
-  const int64_t pi = (begin >> c.bt_log2) + item;
-  if (n <= 0 || item < 0 || pi * B >= len || pi >= q.W) return;
-  const int page = q.table[(int64_t)s * q.W + pi];
+  const int begin = len - n > 0 ? len - n : 0;
+  const int pi = (begin >> c.bt_log2) + item;
+  if (n <= 0 || item < 0 || (int64_t)pi * B >= len || pi >= q.W) return;
+  const int page = __builtin_amdgcn_readfirstlane(q.table[(int64_t)s * q.W + pi]);
   if (page < 0 || page >= c.pages) return;
-  const int o0 = begin > pi * B ? (int)(begin - pi * B) : 0;              // first new slot
-  const int o1 = len - pi * B < B ? (int)(len - pi * B) : B;              // end of the tokens
+  const int o0 = begin > pi * B ? begin - pi * B : 0;                     // first new slot
+  const int o1 = len - pi * B < B ? len - pi * B : B;                     // end of the tokens
   const int64_t row0 = t0 + n - len + pi * B;                             // row of slot 0
   const uint16_t* kr = kx + (int64_t)head * D;
   const uint16_t* vr = vx + (int64_t)head * D;
@@ -183,7 +183,7 @@ __global__ __launch_bounds__(256) void kv8_copy_kernel(Kv8 to, Kv8 from,
 
 Kv8Seqs seqs(const int32_t* table, const int32_t* lens, const int32_t* cu, int64_t S, int64_t W,
              int64_t T) {
-  return {table, lens, cu, (int)S, (int)W, T};
+  return {table, lens, cu, (int)S, (int)W, (int)T};
 }
 
 }  // namespace

@@ -22,6 +22,8 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kTile = 64;   // tokens per step of a wavefront
+constexpr int kDecodeWaves = 4;
+constexpr int kMaxSplits = 64;   // parts of a sequence that one workgroup joins
 
 struct AttnArgs {
   Kv8 c;
@@ -35,7 +37,7 @@ struct AttnArgs {
   uint32_t flip;       // its sign, as the sign bits of two queries
   uint16_t* out;       // [T][heads * G][D]
   float* lse;          // [T][heads * G] or null
-  int splits;          // of a sequence's tiles, over gridDim.z workgroups
+  int splits, per;     // workgroups of a sequence (gridDim.z), tiles of each
   float* ws;
   unsigned* cnt;
 };
@@ -92,8 +94,8 @@ __device__ __forceinline__ half8_t bf16_to_f16(const uint4& u, float down) {
 // lane%16: exactly the order in which the B operand of O^T = V^T P^T wants
 // the weights, and in which V^T is read (16 tokens of one column per 16-byte
 // load). Nothing moves between lanes but the maximum.
-template <class T, int D, int NW>
-__global__ __launch_bounds__(64 * NW) void kv8_decode_kernel(AttnArgs a) {
+template <class T, int D, int BT, int NW>   // pages of 1 << BT tokens
+__global__ __launch_bounds__(64 * NW, D == 64 ? 4 : D == 128 ? 3 : 1) void kv8_decode_kernel(AttnArgs a) {
   constexpr int KD = D / 64, VD = D / 16;
   // f16 results: the weights go in as two f16 terms, since 11 bits of them would
   // cost as much as rounding the result
@@ -105,16 +107,16 @@ __global__ __launch_bounds__(64 * NW) void kv8_decode_kernel(AttnArgs a) {
   const int G = min(16, a.G - h0);
   const Kv8& c = a.c;
   const int s = find_seq(a.q, blockIdx.x, a.unit, a.extra);
-  const int64_t t0 = a.q.first(s), n = a.q.count(s), len = a.q.length(s, c.bt_log2);
-  const int64_t item = blockIdx.x - first_item(a.q, s, a.unit, a.extra);
-  const int64_t i0 = item * a.unit;
-  if (item < 0 || i0 >= n || n * a.G > a.many) return;
-  const int ntok = n - i0 < a.unit ? (int)(n - i0) : a.unit;
+  const int t0 = a.q.first(s), n = a.q.count(s), len = a.q.length(s, BT);
+  const int item = blockIdx.x - first_item(a.q, s, a.unit, a.extra);
+  const int i0 = item * a.unit;
+  if (item < 0 || i0 >= n || (int64_t)n * a.G > a.many) return;
+  const int ntok = min(n - i0, a.unit);
   const int rows = ntok * G;                 // <= 16
   // positions that the last row sees, tiles of them, this workgroup's share
-  const int64_t most = len - n + i0 + ntok;
-  const int tiles = most > 0 ? (int)((most + kTile - 1) / kTile) : 0;
-  const int per = max((tiles + a.splits - 1) / a.splits, NW);   // tiles per workgroup
+  const int most = len - n + i0 + ntok;
+  const int tiles = most > 0 ? (most + kTile - 1) / kTile : 0;
+  const int per = a.per;
   const int parts = tiles > 0 ? (tiles + per - 1) / per : 1;
   if (split >= parts) return;
   const int first = split * per, last = min(first + per, tiles);
@@ -124,8 +126,8 @@ __global__ __launch_bounds__(64 * NW) void kv8_decode_kernel(AttnArgs a) {
   const int ct = col < rows ? col / G : 0, ch = col < rows ? col % G : 0;
   const int64_t trow = t0 + i0 + ct;
   const int qh = head * a.G + h0 + ch;
-  const int64_t min_limit = len - n + i0;   // last position that every row sees
-  const int64_t limit = min_limit + ct;     // that this one sees
+  const int min_limit = len - n + i0;   // last position that every row sees
+  const int limit = min_limit + ct;     // that this one sees
   half8_t qf[KD][2];
   float qs = a.scale;
   {
@@ -166,68 +168,62 @@ __global__ __launch_bounds__(64 * NW) void kv8_decode_kernel(AttnArgs a) {
   int v_exp = -126;
 
   const int32_t* row = a.q.table + (int64_t)s * a.q.W;
-  const int bt = c.bt_log2;
-  // page of token t of the sequence; tokens past the row's pages read page 0
-  auto page_at = [&](int64_t t) QMM_INLINE {
-    const int64_t j = t >> bt;
-    const int p = j < a.q.W && t < most ? row[j] : -1;
+  // page of token t of the sequence (-1: none, its tokens are not seen)
+  auto page_at = [&](int t) QMM_INLINE {
+    const int j = t >> BT;
+    const int p = t < most ? row[j] : -1;   // most <= W << BT
     return p < c.pages ? p : -1;
   };
+  // The loads run ahead of their use: a tile's pages are looked up one tile
+  // before its codes are asked for, its key codes while the tile before is
+  // weighed, its value codes once the values of the tile before are spent.
   const int kg = (col / 4) * 16;   // first token of this lane's K rows in a tile
-  for (int tile = first + wave; tile < last; tile += NW) {
-    const int64_t base = (int64_t)tile * kTile;
-    const int pk = page_at(base + kg), pv = page_at(base + g * 16);
+  int pk, pv;
+  auto look_up = [&](int tile) QMM_INLINE {
+    pk = page_at(tile * kTile + kg);
+    pv = page_at(tile * kTile + g * 16);
+  };
+  u32x4_t kw[4][KD], vw[VD];
+  auto fetch_keys = [&]() QMM_INLINE {
     const int8_t* kp = c.k + c.block(pk < 0 ? 0 : pk, head) +
-                       ((kg & ((1 << bt) - 1)) + col % 4) * D + g * 16;
-    const int8_t* vp = c.v + c.block(pv < 0 ? 0 : pv, head) + ((int64_t)col << bt) +
-                       ((g * 16) & ((1 << bt) - 1));
-    u32x4_t kw[4][KD], vw[VD];
+                       ((kg & ((1 << BT) - 1)) + col % 4) * D + g * 16;
 #pragma unroll
     for (int j = 0; j < 4; j++)
 #pragma unroll
       for (int b = 0; b < KD; b++)
         kw[j][b] = __builtin_nontemporal_load(
             reinterpret_cast<const u32x4_t*>(kp + j * 4 * D + b * 64));
+  };
+  auto fetch_values = [&](int page) QMM_INLINE {
+    const int8_t* vp = c.v + c.block(page < 0 ? 0 : page, head) + (col << BT) +
+                       ((g * 16) & ((1 << BT) - 1));
 #pragma unroll
     for (int i = 0; i < VD; i++)
       vw[i] = __builtin_nontemporal_load(
-          reinterpret_cast<const u32x4_t*>(vp + ((int64_t)(i * 16) << bt)));
-    const int64_t blk = (int64_t)(pv < 0 ? 0 : pv) * c.heads + head;
-    const float ks = c.ks[blk], vs = c.vs[blk];
-
-    float4_t sc[4];
-#pragma unroll
-    for (int j = 0; j < 4; j++) {
-      sc[j] = float4_t{0, 0, 0, 0};
-#pragma unroll
-      for (int b = 0; b < KD; b++)
-#pragma unroll
-        for (int h = 0; h < 2; h++)
-          sc[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-              codes_f16(kw[j][b][2 * h], kw[j][b][2 * h + 1]), qf[b][h], sc[j], 0, 0, 0);
-    }
-    const float f = ks * qs;
+          reinterpret_cast<const u32x4_t*>(vp + ((i * 16) << BT)));
+  };
+  float ks = 0.0f, vs = 0.0f;   // scales of this lane's 16 tokens
+  auto fetch_scales = [&](int page) QMM_INLINE {
+    const int64_t blk = (int64_t)(page < 0 ? 0 : page) * c.heads + head;
+    ks = c.ks[blk];
+    vs = c.vs[blk];
+  };
+  // one tile's weights; MASK: some of its tokens are not seen by some row
+  half8_t pf[2], pl[2];
+  auto weigh = [&]<bool MASK>(const float4_t* sc, float f, float vs, int ve, int left) QMM_INLINE {
     float p[16];
     float mx = m_run;
-    // every token of the tile seen by every row? (then nothing is masked)
-    const bool whole = base + kTile - 1 <= min_limit && __all(pv >= 0);
-    const int64_t left = pv < 0 ? -1 : limit - (base + g * 16);   // tokens 0 .. left are seen
 #pragma unroll
     for (int i = 0; i < 16; i++) {
       p[i] = sc[i / 4][i % 4] * f;
-      if (!whole) p[i] = i <= left ? p[i] : -__builtin_inff();
+      if constexpr (MASK) p[i] = i <= left ? p[i] : -__builtin_inff();
       mx = fmaxf(mx, p[i]);
     }
     mx = fmaxf(mx, __shfl_xor(mx, 16));
     mx = fmaxf(mx, __shfl_xor(mx, 32));
     const float mu = mx == -__builtin_inff() ? 0.0f : mx;
-    // the largest value scale's exponent (NaN and infinity leave it)
-    int ve = (int)(__builtin_bit_cast(uint32_t, vs) >> 23 & 255) - 127;
-    if (ve > 127 || pv < 0) ve = -126;
-    ve = max(ve, __shfl_xor(ve, 16));
-    ve = max(max(ve, __shfl_xor(ve, 32)), v_exp);
     if (__any(mx != m_run || ve != v_exp)) {
-      const float al = __builtin_amdgcn_exp2f(m_run - mu) ;
+      const float al = __builtin_amdgcn_exp2f(m_run - mu);
       const float down = ldexpf(al, v_exp - ve);
       l_run *= al;
 #pragma unroll
@@ -236,15 +232,58 @@ __global__ __launch_bounds__(64 * NW) void kv8_decode_kernel(AttnArgs a) {
       v_exp = ve;
     }
     const float r = ldexpf(vs, -v_exp);
-    half8_t pf[2], pl[2];
 #pragma unroll
     for (int i = 0; i < 16; i++) {
       const float e = __builtin_amdgcn_exp2f(p[i] - mu);
       l_run += e;
       float w = e * r;
-      if (!whole) w = i <= left ? w : 0.0f;
+      if constexpr (MASK) w = i <= left ? w : 0.0f;
       pf[i / 8][i % 8] = (_Float16)w;
       if constexpr (kTwo) pl[i / 8][i % 8] = (_Float16)(w - (float)pf[i / 8][i % 8]);
+    }
+  };
+  int tile = first + wave;
+  if (tile < last) {
+    look_up(tile);
+    fetch_keys();
+    fetch_values(pv);
+    fetch_scales(pv);
+  }
+  for (; tile < last; tile += NW) {
+    const int base = tile * kTile;
+    const int page = pv;
+    const bool more = tile + NW < last;
+    if (more) look_up(tile + NW);
+    float4_t sc[4];
+#pragma unroll
+    for (int j = 0; j < 4; j++) sc[j] = float4_t{0, 0, 0, 0};
+#pragma unroll
+    for (int b = 0; b < KD; b++)
+#pragma unroll
+      for (int h = 0; h < 2; h++) {
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+          sc[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+              codes_f16(kw[j][b][2 * h], kw[j][b][2 * h + 1]), qf[b][h], sc[j], 0, 0, 0);
+        // (the compiler would convert the whole tile first and run out of registers)
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    const float f = ks * qs, vs_now = vs;
+    if (more) {
+      fetch_keys();
+      fetch_scales(pv);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    // the largest value scale's exponent (NaN and infinity leave it)
+    int ve = (int)(__builtin_bit_cast(uint32_t, vs_now) >> 23 & 255) - 127;
+    if (ve > 127 || page < 0) ve = -126;
+    ve = max(ve, __shfl_xor(ve, 16));
+    ve = max(max(ve, __shfl_xor(ve, 32)), v_exp);
+    if (base + kTile - 1 <= min_limit && __all(page >= 0)) {
+      weigh.template operator()<false>(sc, f, vs_now, ve, 0);
+    } else {   // tokens 0 .. left of this lane's 16 are seen
+      const int left = page < 0 ? -1 : limit - (base + g * 16);
+      weigh.template operator()<true>(sc, f, vs_now, ve, left);
     }
 #pragma unroll
     for (int i = 0; i < VD; i++)
@@ -253,7 +292,10 @@ __global__ __launch_bounds__(64 * NW) void kv8_decode_kernel(AttnArgs a) {
         const half8_t vf = codes_f16(vw[i][2 * h], vw[i][2 * h + 1]);
         o[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, pf[h], o[i], 0, 0, 0);
         if constexpr (kTwo) o[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, pl[h], o[i], 0, 0, 0);
+        if (h == 1 && i % 2 == 1) __builtin_amdgcn_sched_barrier(0);
       }
+    if (more) fetch_values(pv);
+    __builtin_amdgcn_sched_barrier(0);
   }
   l_run += __shfl_xor(l_run, 16);
   l_run += __shfl_xor(l_run, 32);
@@ -272,36 +314,48 @@ __global__ __launch_bounds__(64 * NW) void kv8_decode_kernel(AttnArgs a) {
     *reinterpret_cast<float4_t*>(jo + ((wave * 16 + col) * D + i * 16 + g * 4)) = o[i] * vref;
   __syncthreads();
   const int Hq = c.heads * a.G;
-  auto finish = [&](int r, int d, float v, float m, float l) QMM_INLINE {
-    const int64_t at = (t0 + i0 + r / G) * Hq + head * a.G + h0 + r % G;
-    a.out[at * D + d] = from_f32(T{}, l > 0.0f || l != l ? v / l : 0.0f);
-    if (d == 0 && a.lse)
-      a.lse[at] = l > 0.0f || l != l ? fmaf(m, kLn2, logf(l)) : -__builtin_inff();
+  auto finish = [&](int r, int d, float v0, float v1, float m, float l) QMM_INLINE {
+    const int64_t at = (int64_t)(t0 + i0 + r / G) * Hq + head * a.G + h0 + r % G;
+    const bool any = l > 0.0f || l != l;
+    const float back = any ? 1.0f / l : 0.0f;
+    *reinterpret_cast<uint32_t*>(a.out + at * D + d) =
+        from_f32(T{}, any ? v0 * back : 0.0f) | (uint32_t)from_f32(T{}, any ? v1 * back : 0.0f) << 16;
+    if (d == 0 && a.lse) a.lse[at] = any ? fmaf(m, kLn2, logf(l)) : -__builtin_inff();
   };
+  // a part in the workspace: per row the maximum and the sum, then the rows
+  constexpr int kPart = 16 * (D + 2);
   const int64_t unit = (int64_t)blockIdx.x * gridDim.y + blockIdx.y;
-  float* part = a.ws + unit * a.splits * (16 * (D + 2));
-  for (int i = tid; i < rows * D; i += 64 * NW) {
-    const int r = i / D, d = i % D;
+  float* part = a.ws + unit * a.splits * kPart;
+  auto put2 = [&](float* p, float x, float y) QMM_INLINE {
+    const uint64_t w = __builtin_bit_cast(uint32_t, x) | (uint64_t)__builtin_bit_cast(uint32_t, y) << 32;
+    __hip_atomic_store(reinterpret_cast<uint64_t*>(p), w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  };
+  auto get2 = [&](const float* p) QMM_INLINE {
+    const uint64_t w = __hip_atomic_load(reinterpret_cast<const uint64_t*>(p), __ATOMIC_RELAXED,
+                                         __HIP_MEMORY_SCOPE_AGENT);
+    return make_float2(__builtin_bit_cast(float, (uint32_t)w), __builtin_bit_cast(float, (uint32_t)(w >> 32)));
+  };
+  for (int i = tid; i < rows * (D / 2); i += 64 * NW) {
+    const int r = i / (D / 2), d = i % (D / 2) * 2;
     float m = -__builtin_inff();
 #pragma unroll
     for (int w = 0; w < NW; w++) m = fmaxf(m, jm[w][r]);
     const float mu = m == -__builtin_inff() ? 0.0f : m;
-    float l = 0.0f, v = 0.0f;
+    float l = 0.0f, v0 = 0.0f, v1 = 0.0f;
 #pragma unroll
     for (int w = 0; w < NW; w++) {
       const float e = __builtin_amdgcn_exp2f(jm[w][r] - mu);
+      const float2 v = *reinterpret_cast<const float2*>(jo + (w * 16 + r) * D + d);
       l += jl[w][r] * e;
-      v += jo[(w * 16 + r) * D + d] * e;
+      v0 += v.x * e;
+      v1 += v.y * e;
     }
     if (parts == 1) {
-      finish(r, d, v, m, l);
+      finish(r, d, v0, v1, m, l);
     } else {
-      float* mine = part + split * (16 * (D + 2));
-      __hip_atomic_store(mine + 32 + r * D + d, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      if (d == 0) {
-        __hip_atomic_store(mine + r, m, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        __hip_atomic_store(mine + 16 + r, l, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      }
+      float* mine = part + split * kPart;
+      put2(mine + 32 + r * D + d, v0, v1);
+      if (d == 0) put2(mine + 2 * r, m, l);
     }
   }
   if (parts == 1) return;
@@ -317,22 +371,57 @@ __global__ __launch_bounds__(64 * NW) void kv8_decode_kernel(AttnArgs a) {
                                             "agent") == (unsigned)(parts - 1);
   __syncthreads();
   if (!is_last) return;
-  auto get = [&](const float* p) QMM_INLINE {
-    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  };
-  for (int i = tid; i < rows * D; i += 64 * NW) {
-    const int r = i / D, d = i % D;
-    float m = -__builtin_inff(), l = 0.0f, v = 0.0f;
-    for (int w = 0; w < parts; w++) {
-      const float* p = part + w * (16 * (D + 2));
-      const float mw = get(p + r), lw = get(p + 16 + r), vw = get(p + 32 + r * D + d);
-      const float mn = fmaxf(m, mw), mu = mn == -__builtin_inff() ? 0.0f : mn;
-      const float ea = __builtin_amdgcn_exp2f(m - mu), eb = __builtin_amdgcn_exp2f(mw - mu);
-      l = l * ea + lw * eb;
-      v = v * ea + vw * eb;
-      m = mn;
+  // every part's factor exp2(m - max) per row, and the rows' sums
+  float* fac = jo;                       // [parts][16]; parts <= kMaxSplits
+  for (int i = tid; i < parts * rows; i += 64 * NW) {
+    const float2 ml = get2(part + i / rows * kPart + 2 * (i % rows));
+    fac[i / rows * 16 + i % rows] = ml.x;
+    fac[(kMaxSplits + i / rows) * 16 + i % rows] = ml.y;
+  }
+  __syncthreads();
+  for (int r = wave; r < rows; r += NW) {   // a wavefront per row
+    float m = -__builtin_inff();
+    for (int w = lane; w < parts; w += 64) m = fmaxf(m, fac[w * 16 + r]);
+#pragma unroll
+    for (int x = 32; x >= 1; x >>= 1) m = fmaxf(m, __shfl_xor(m, x));
+    const float mu = m == -__builtin_inff() ? 0.0f : m;
+    float l = 0.0f;
+    for (int w = lane; w < parts; w += 64) {
+      const float e = __builtin_amdgcn_exp2f(fac[w * 16 + r] - mu);
+      fac[w * 16 + r] = e;
+      l += fac[(kMaxSplits + w) * 16 + r] * e;
     }
-    finish(r, d, v, m, l);
+#pragma unroll
+    for (int x = 32; x >= 1; x >>= 1) l += __shfl_xor(l, x);
+    if (lane == 0) {
+      jm[0][r] = m;
+      jl[0][r] = l;
+    }
+  }
+  __syncthreads();
+  for (int i = tid; i < rows * (D / 2); i += 64 * NW) {
+    const int r = i / (D / 2), d = i % (D / 2) * 2;
+    float v0 = 0.0f, v1 = 0.0f;
+    const float* p = part + 32 + r * D + d;
+    int w = 0;
+    for (; w + 8 <= parts; w += 8) {   // eight loads in flight
+      float2 v[8];
+#pragma unroll
+      for (int x = 0; x < 8; x++) v[x] = get2(p + (w + x) * kPart);
+#pragma unroll
+      for (int x = 0; x < 8; x++) {
+        const float e = fac[(w + x) * 16 + r];
+        v0 = fmaf(v[x].x, e, v0);
+        v1 = fmaf(v[x].y, e, v1);
+      }
+    }
+    for (; w < parts; w++) {
+      const float2 v = get2(p + w * kPart);
+      const float e = fac[w * 16 + r];
+      v0 = fmaf(v.x, e, v0);
+      v1 = fmaf(v.y, e, v1);
+    }
+    finish(r, d, v0, v1, jm[0][r], jl[0][r]);
   }
 }
 
@@ -369,28 +458,28 @@ __global__ __launch_bounds__(64 * NW) void kv8_prompt_kernel(AttnArgs a) {
   const int head = blockIdx.y;
   const Kv8& c = a.c;
   // long sequences' last items have most to do: they come first
-  const int64_t index = (int64_t)gridDim.x - 1 - blockIdx.x;
+  const int index = gridDim.x - 1 - blockIdx.x;
   const int s = find_seq(a.q, index, a.unit, a.extra);
-  const int64_t t0 = a.q.first(s), n = a.q.count(s), len = a.q.length(s, c.bt_log2);
-  const int64_t item = index - first_item(a.q, s, a.unit, a.extra);
-  const int64_t i0 = item * a.unit;
-  if (item < 0 || i0 >= n || n * a.G <= a.many) return;
-  const int ntok = n - i0 < a.unit ? (int)(n - i0) : a.unit;
+  const int t0 = a.q.first(s), n = a.q.count(s), len = a.q.length(s, c.bt_log2);
+  const int item = index - first_item(a.q, s, a.unit, a.extra);
+  const int i0 = item * a.unit;
+  if (item < 0 || i0 >= n || (int64_t)n * a.G <= a.many) return;
+  const int ntok = min(n - i0, a.unit);
   const int rows = ntok * a.G;
-  const int64_t most = len - n + i0 + ntok;
-  const int tiles = most > 0 ? (int)((most + kTile - 1) / kTile) : 0;
+  const int most = len - n + i0 + ntok;
+  const int tiles = most > 0 ? (most + kTile - 1) / kTile : 0;
 
   // this lane's query row; rows past the last repeat it, and nothing reads them
   const int rr = min(wave * 32 + col, rows - 1);
   const int ct = rr / a.G, ch = rr % a.G;
-  const int64_t limit = len - n + i0 + ct;
-  const int64_t wave_min = len - n + i0 + min(wave * 32, rows - 1) / a.G;
-  const int64_t wave_max = len - n + i0 + min(wave * 32 + 31, rows - 1) / a.G;
-  const int64_t at = (t0 + i0 + ct) * (c.heads * a.G) + head * a.G + ch;
+  const int limit = len - n + i0 + ct;
+  const int wave_min = len - n + i0 + min(wave * 32, rows - 1) / a.G;
+  const int wave_max = len - n + i0 + min(wave * 32 + 31, rows - 1) / a.G;
+  const int64_t at = (int64_t)(t0 + i0 + ct) * (c.heads * a.G) + head * a.G + ch;
   half8_t qf[KS];
   float qs = a.scale;
   {
-    const uint16_t* qr = a.x + (t0 + i0 + ct) * a.ldq + (int64_t)(head * a.G + ch) * D + h * 8;
+    const uint16_t* qr = a.x + (int64_t)(t0 + i0 + ct) * a.ldq + (int64_t)(head * a.G + ch) * D + h * 8;
     uint4 u[KS];
 #pragma unroll
     for (int i = 0; i < KS; i++) u[i] = load_q(qr + i * 16, a.flip);
@@ -420,9 +509,8 @@ __global__ __launch_bounds__(64 * NW) void kv8_prompt_kernel(AttnArgs a) {
 
   const int32_t* row = a.q.table + (int64_t)s * a.q.W;
   const int bt = c.bt_log2;
-  auto page_at = [&](int64_t t) QMM_INLINE {
-    const int64_t j = t >> bt;
-    const int p = j < a.q.W && t < most ? row[j] : -1;
+  auto page_at = [&](int t) QMM_INLINE {
+    const int p = t < most ? row[t >> bt] : -1;   // most <= W << bt
     return p < c.pages ? p : -1;
   };
   // Each tile's pages are looked up two tiles ahead and its codes and scales
@@ -434,8 +522,8 @@ __global__ __launch_bounds__(64 * NW) void kv8_prompt_kernel(AttnArgs a) {
 #pragma unroll
     for (int i = 0; i < kUnits; i++) {
       const int u = i * kThreads + tid;
-      kp[i] = page_at((int64_t)tile * kTile + u / (D / 16));
-      vp[i] = page_at((int64_t)tile * kTile + u % 4 * 16);
+      kp[i] = page_at(tile * kTile + u / (D / 16));
+      vp[i] = page_at(tile * kTile + u % 4 * 16);
     }
   };
   u32x4_t kw[kUnits], vw[kUnits];
@@ -547,7 +635,7 @@ __global__ __launch_bounds__(64 * NW) void kv8_prompt_kernel(AttnArgs a) {
       fetch();
       look_up(tile + 2);
     }
-    const int64_t base = (int64_t)tile * kTile;
+    const int base = tile * kTile;
     if (base <= wave_max) {
       float f[4], vs[4];
       int ve = v_exp;
@@ -575,8 +663,7 @@ __global__ __launch_bounds__(64 * NW) void kv8_prompt_kernel(AttnArgs a) {
               *reinterpret_cast<const half8_t*>(&lk[buf][r * D + key_piece(r, ks * 2 + h) * 8]);
           sc[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, qf[ks], sc[j], 0, 0, 0);
         }
-      const int64_t far = limit - base - h * 8;   // tokens g * 16 + e up to this are seen
-      const int left = (int)(far < 64 ? far < 0 ? -1 : far : 64);
+      const int left = limit - base - h * 8;   // tokens g * 16 + e up to this are seen
       if (base + kTile - 1 <= wave_min && missing == 0)
         weigh.template operator()<false>(sc, f, vs, ve, left, missing, buf);
       else
@@ -606,7 +693,7 @@ __global__ __launch_bounds__(64 * NW) void kv8_prompt_kernel(AttnArgs a) {
 constexpr int kFewRows = 64;
 
 struct Plan {
-  int unit, extra, splits, nw, many;
+  int unit, extra, splits, per, nw, many;
   int64_t items, columns;   // grid: items x heads and blocks of a group's heads
   bool prompts;
   int p_unit;
@@ -627,16 +714,19 @@ Plan plan(const Kv8& c, int64_t T, int64_t Hq, int64_t S, int64_t W) {
   p.columns = c.heads * ((G + 15) / 16);
   p.p_unit = (int)(prompt_rows / (G < prompt_rows ? G : prompt_rows));
   p.p_items = T / p.p_unit + S;
-  p.nw = c.dim == 256 ? 4 : 8;
+  p.nw = kDecodeWaves;
   const int64_t units = (T < p.items ? T : p.items) * p.columns;
   const int64_t tiles = ((W << c.bt_log2) + kTile - 1) / kTile;
-  // enough workgroups to fill the chip several times over, each with at least
-  // one tile per wavefront
-  int64_t sp = 1024 / (units < 1 ? 1 : units);
-  sp = sp < 1 ? 1 : sp;
-  sp = sp < tiles / p.nw ? sp : tiles / p.nw;
-  sp = sp < 1 ? 1 : sp > 128 ? 128 : sp;
-  if (p.items * p.columns > kScratchCounters) sp = 1;
+  // Every workgroup takes the same number of tiles (a multiple of the
+  // wavefronts), so that ragged sequences load the chip evenly: as many as
+  // make about 2048 workgroups of sequences that fill their table rows, and
+  // no sequence is cut into more parts than one workgroup joins.
+  int64_t per = (units * tiles + 2047) / 2048;
+  per = per > (tiles + kMaxSplits - 1) / kMaxSplits ? per : (tiles + kMaxSplits - 1) / kMaxSplits;
+  if (p.items * p.columns > kScratchCounters) per = tiles;
+  per = (per + p.nw - 1) / p.nw * p.nw;
+  p.per = (int)per;
+  const int64_t sp = (tiles + per - 1) / per;
   p.splits = (int)sp;
   return p;
 }
@@ -653,13 +743,19 @@ hipError_t launch_kv8_attention(const Kv8& c, int dt, const void* q, int64_t ldq
                                 const int32_t* cu, int64_t S, int64_t W, float scale, void* out,
                                 float* lse, unsigned* cnt, float* ws, hipStream_t st) {
   const Plan p = plan(c, T, Hq, S, W);
-  AttnArgs a{c, {table, lens, cu, (int)S, (int)W, T}, static_cast<const uint16_t*>(q), ldq,
+  AttnArgs a{c, {table, lens, cu, (int)S, (int)W, (int)T}, static_cast<const uint16_t*>(q), ldq,
              (int)(Hq / c.heads), p.unit, p.extra, p.many, fabsf(scale) * kLog2e,
-             scale < 0 ? 0x80008000u : 0u, static_cast<uint16_t*>(out), lse, p.splits, ws, cnt};
+             scale < 0 ? 0x80008000u : 0u, static_cast<uint16_t*>(out), lse, p.splits, p.per, ws, cnt};
   const dim3 grid((unsigned)p.items, (unsigned)p.columns, (unsigned)p.splits);
-  auto go = [&]<class T_, int D, int NW>() {
+  auto go = [&]<class T_, int D>() {
+    constexpr int NW = kDecodeWaves;
     const size_t lds = (size_t)NW * 16 * D * 4;
-    hipLaunchKernelGGL((kv8_decode_kernel<T_, D, NW>), grid, dim3(64 * NW), lds, st, a);
+    auto decode = [&]<int BT>() {
+      hipLaunchKernelGGL((kv8_decode_kernel<T_, D, BT, NW>), grid, dim3(64 * NW), lds, st, a);
+    };
+    if (c.bt_log2 == 4) decode.template operator()<4>();
+    else if (c.bt_log2 == 5) decode.template operator()<5>();
+    else decode.template operator()<6>();
     if (!p.prompts) return;
     AttnArgs b = a;
     b.unit = p.p_unit;
@@ -669,9 +765,9 @@ hipError_t launch_kv8_attention(const Kv8& c, int dt, const void* q, int64_t ldq
                        st, b);
   };
   auto by_dim = [&]<class T_>() {
-    if (c.dim == 64) go.template operator()<T_, 64, 8>();
-    else if (c.dim == 128) go.template operator()<T_, 128, 8>();
-    else go.template operator()<T_, 256, 4>();
+    if (c.dim == 64) go.template operator()<T_, 64>();
+    else if (c.dim == 128) go.template operator()<T_, 128>();
+    else go.template operator()<T_, 256>();
   };
   if (dt == 0) by_dim.template operator()<F16>();
   else by_dim.template operator()<BF16>();

@@ -27,29 +27,31 @@ struct Kv8Seqs {
   const int32_t* table;   // [S][W] page numbers
   const int32_t* lens;    // [S]
   const int32_t* cu;      // [S + 1]
-  int S, W;
-  int64_t T;
-  __device__ int64_t first(int s) const {
-    const int64_t c = cu[s];
+  int S, W, T;            // T <= 2^24
+  // (values of one sequence are the same in every lane: they belong in scalar
+  // registers, which the compiler does not see through the loads)
+  __device__ int first(int s) const {
+    const int c = __builtin_amdgcn_readfirstlane(cu[s]);
     return c < 0 ? 0 : c > T ? T : c;
   }
-  __device__ int64_t count(int s) const {
-    const int64_t n = first(s + 1) - first(s);
+  __device__ int count(int s) const {
+    const int n = first(s + 1) - first(s);
     return n < 0 ? 0 : n;
   }
-  __device__ int64_t length(int s, int bt_log2) const {
-    const int64_t most = (int64_t)W << bt_log2, n = lens[s];
-    return n < 0 ? 0 : n > most ? most : n;
+  __device__ int length(int s, int bt_log2) const {
+    const int64_t most = (int64_t)W << bt_log2;
+    const int n = __builtin_amdgcn_readfirstlane(lens[s]);
+    return n < 0 ? 0 : n > most ? (int)most : n;
   }
 };
 
 // Work items of a ragged batch, `unit` new tokens each: sequence s owns items
 // cu[s] / unit + extra * s .. cu[s+1] / unit + extra * (s+1), at least count /
 // unit + extra of them. Returns the sequence that owns item i (binary search).
-__device__ __forceinline__ int64_t first_item(const Kv8Seqs& q, int s, int unit, int extra) {
-  return (uint32_t)q.first(s) / (uint32_t)unit + (int64_t)extra * s;   // T < 2^32
+__device__ __forceinline__ int first_item(const Kv8Seqs& q, int s, int unit, int extra) {
+  return (uint32_t)q.first(s) / (uint32_t)unit + extra * s;
 }
-__device__ __forceinline__ int find_seq(const Kv8Seqs& q, int64_t i, int unit, int extra) {
+__device__ __forceinline__ int find_seq(const Kv8Seqs& q, int i, int unit, int extra) {
   int lo = 0, hi = q.S;   // the item belongs to a sequence in [lo, hi)
   while (hi - lo > 1) {
     const int mid = (lo + hi) / 2;

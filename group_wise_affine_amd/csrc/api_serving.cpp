@@ -249,8 +249,7 @@ qmm_status qmm_kv8_attention(const qmm_kv8_cache* cache, const void* q, int64_t 
   if (qmm_status s = check_work(tag, work, work_bytes, need > 0 ? kCounterBytes + need : 0)) return s;
   return launched(
       qmm::launch_kv8_attention(c, (int)dt, q, ldq, T, q_heads, table, lens, cu, S, W, scale, out,
-                                lse, static_cast<unsigned*>(work),
-                                work ? reinterpret_cast<float*>(past_counters(work)) : nullptr,
+                                lse, work ? reinterpret_cast<float*>(past_counters(work)) : nullptr,
                                 (hipStream_t)stream),
       tag);
 }

@@ -253,11 +253,11 @@ hipError_t launch_kv8_update(const Kv8& c, const int32_t* ref, const int32_t* ta
 hipError_t launch_kv8_compact(const Kv8& c, const int32_t* ref, const int32_t* table, int64_t S,
                               int64_t W, int32_t* ref_out, int32_t* table_out, int32_t* remap,
                               int32_t* used, int32_t* work, hipStream_t st);
-// scratch bytes of the attention (0: none) after the counters
+// scratch bytes of the attention (0: none)
 int64_t kv8_attention_work(const Kv8& c, int64_t T, int64_t Hq, int64_t S, int64_t W);
 hipError_t launch_kv8_attention(const Kv8& c, int dt, const void* q, int64_t ldq, int64_t T,
                                 int64_t Hq, const int32_t* table, const int32_t* lens,
                                 const int32_t* cu, int64_t S, int64_t W, float scale, void* out,
-                                float* lse, unsigned* cnt, float* ws, hipStream_t st);
+                                float* lse, float* ws, hipStream_t st);
 
 }  // namespace qmm

@@ -22,9 +22,8 @@ __global__ __launch_bounds__(256) void kv8_append_kernel(Kv8 c, Kv8Seqs q,
   __shared__ uint32_t top_k[4], top_v[4];
   const int tid = threadIdx.x, head = blockIdx.y;
   const int B = 1 << c.bt_log2, D = c.dim, D8 = D / 8;
-  const int s = find_seq(q, blockIdx.x, B, 2);
-  const int t0 = q.first(s), n = q.count(s), len = q.length(s, c.bt_log2);
-  const int item = blockIdx.x - first_item(q, s, B, 2);
+  const SeqAt at_seq = locate(q, blockIdx.x, B, 2, c.bt_log2);
+  const int s = at_seq.s, t0 = at_seq.first, n = at_seq.count, len = at_seq.len, item = at_seq.item;
   // a sequence whose tokens cannot be placed (fewer places than tokens) gets
   // its last `len` ones
   const int begin = len - n > 0 ? len - n : 0;

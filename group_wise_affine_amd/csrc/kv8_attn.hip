@@ -22,8 +22,7 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kTile = 64;   // tokens per step of a wavefront
-constexpr int kDecodeWaves = 4;
-constexpr int kMaxSplits = 64;   // parts of a sequence that one workgroup joins
+constexpr int kMaxSplits = 128;   // parts of a sequence
 
 struct AttnArgs {
   Kv8 c;
@@ -39,7 +38,6 @@ struct AttnArgs {
   float* lse;          // [T][heads * G] or null
   int splits, per;     // workgroups of a sequence (gridDim.z), tiles of each
   float* ws;
-  unsigned* cnt;
 };
 
 // eight signed codes (two words) as f16: 1024 + (code + 128) - 1152, exact
@@ -82,6 +80,25 @@ __device__ __forceinline__ half8_t bf16_to_f16(const uint4& u, float down) {
   return r;
 }
 
+// two outputs of a row, and whether it has seen a key at all
+struct Share {
+  uint32_t pair;
+  bool any;
+};
+template <class T>
+__device__ __forceinline__ Share share(float v0, float v1, float l) {
+  Share s;
+  s.any = l > 0.0f || l != l;
+  const float back = s.any ? 1.0f / l : 0.0f;
+  s.pair = from_f32(T{}, s.any ? v0 * back : 0.0f) |
+           (uint32_t)from_f32(T{}, s.any ? v1 * back : 0.0f) << 16;
+  return s;
+}
+// floats of a part in the scratch buffer: per row the maximum and the sum,
+// then the rows
+template <int D>
+constexpr int kPart = 16 * (D + 2);
+
 // ------------------------------------------------------------------- decode
 // Up to 16 query rows (tokens x heads of one group) per workgroup, NW
 // wavefronts. A wavefront takes every NW-th tile of 64 tokens and holds its
@@ -95,20 +112,20 @@ __device__ __forceinline__ half8_t bf16_to_f16(const uint4& u, float down) {
 // the weights, and in which V^T is read (16 tokens of one column per 16-byte
 // load). Nothing moves between lanes but the maximum.
 template <class T, int D, int BT, int NW>   // pages of 1 << BT tokens
-__global__ __launch_bounds__(64 * NW, D == 64 ? 4 : D == 128 ? 3 : 1) void kv8_decode_kernel(AttnArgs a) {
+__global__ __launch_bounds__(64 * NW, D == 256 ? 1 : D == 128 ? 2 : 3) void kv8_decode_kernel(AttnArgs a) {
   constexpr int KD = D / 64, VD = D / 16;
   // f16 results: the weights go in as two f16 terms, since 11 bits of them would
   // cost as much as rounding the result
   constexpr bool kTwo = __is_same(T, F16);
-  const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
+  const int tid = threadIdx.x, lane = tid % 64;
+  const int wave = __builtin_amdgcn_readfirstlane(tid / 64);   // uniform: scalar
   const int col = lane % 16, g = lane / 16;
   const int blocks = (a.G + 15) / 16;   // of heads in a group
   const int head = blockIdx.y / blocks, h0 = blockIdx.y % blocks * 16, split = blockIdx.z;
   const int G = min(16, a.G - h0);
   const Kv8& c = a.c;
-  const int s = find_seq(a.q, blockIdx.x, a.unit, a.extra);
-  const int t0 = a.q.first(s), n = a.q.count(s), len = a.q.length(s, BT);
-  const int item = blockIdx.x - first_item(a.q, s, a.unit, a.extra);
+  const SeqAt seq = locate(a.q, blockIdx.x, a.unit, a.extra, BT);
+  const int s = seq.s, t0 = seq.first, n = seq.count, len = seq.len, item = seq.item;
   const int i0 = item * a.unit;
   if (item < 0 || i0 >= n || (int64_t)n * a.G > a.many) return;
   const int ntok = min(n - i0, a.unit);
@@ -128,25 +145,29 @@ __global__ __launch_bounds__(64 * NW, D == 64 ? 4 : D == 128 ? 3 : 1) void kv8_d
   const int qh = head * a.G + h0 + ch;
   const int min_limit = len - n + i0;   // last position that every row sees
   const int limit = min_limit + ct;     // that this one sees
-  half8_t qf[KD][2];
-  float qs = a.scale;
+  uint4 u[KD][2];   // asked for first, looked at when the codes are on their way
   {
     const uint16_t* qr = a.x + trow * a.ldq + (int64_t)qh * D + g * 16;
-    uint4 u[KD][2];
-    uint32_t m = 0;
 #pragma unroll
     for (int b = 0; b < KD; b++)
 #pragma unroll
-      for (int h = 0; h < 2; h++) {
-        u[b][h] = load_q(qr + b * 64 + h * 8, a.flip);
-        m = amax_pair(amax_pair(amax_pair(amax_pair(m, u[b][h].x), u[b][h].y), u[b][h].z), u[b][h].w);
-      }
+      for (int h = 0; h < 2; h++) u[b][h] = load_q(qr + b * 64 + h * 8, a.flip);
+  }
+  half8_t qf[KD][2];
+  float qs = a.scale;
+  auto take_queries = [&]() QMM_INLINE {
     if constexpr (__is_same(T, F16)) {
 #pragma unroll
       for (int b = 0; b < KD; b++)
 #pragma unroll
         for (int h = 0; h < 2; h++) qf[b][h] = __builtin_bit_cast(half8_t, u[b][h]);
     } else {
+      uint32_t m = 0;
+#pragma unroll
+      for (int b = 0; b < KD; b++)
+#pragma unroll
+        for (int h = 0; h < 2; h++)
+          m = amax_pair(amax_pair(amax_pair(amax_pair(m, u[b][h].x), u[b][h].y), u[b][h].z), u[b][h].w);
       m = amax_halves(m);
       m = umax(m, (uint32_t)__shfl_xor((int)m, 16));
       m = umax(m, (uint32_t)__shfl_xor((int)m, 32));
@@ -157,7 +178,7 @@ __global__ __launch_bounds__(64 * NW, D == 64 ? 4 : D == 128 ? 3 : 1) void kv8_d
 #pragma unroll
         for (int h = 0; h < 2; h++) qf[b][h] = bf16_to_f16(u[b][h], e.down);
     }
-  }
+  };
 
   float4_t o[VD];
 #pragma unroll
@@ -168,20 +189,27 @@ __global__ __launch_bounds__(64 * NW, D == 64 ? 4 : D == 128 ? 3 : 1) void kv8_d
   int v_exp = -126;
 
   const int32_t* row = a.q.table + (int64_t)s * a.q.W;
-  // page of token t of the sequence (-1: none, its tokens are not seen)
-  auto page_at = [&](int t) QMM_INLINE {
-    const int j = t >> BT;
-    const int p = t < most ? row[j] : -1;   // most <= W << BT
-    return p < c.pages ? p : -1;
+  // Every wavefront walks a run of tiles. The numbers and scales of the next 64
+  // pages sit one per lane, so that nothing but the codes is loaded in the
+  // loop, and the loads run ahead of their use: a tile's keys are asked for
+  // when those of the tile before have been multiplied, its values when those
+  // of the tile before are spent.
+  constexpr int kPer = kTile >> BT;   // pages of a tile
+  const int kg = (col / 4) * 16;      // first token of this lane's K rows in a tile
+  int pages = -1;                     // page `lane` of the chunk of 64
+  float pages_ks = 0.0f, pages_vs = 0.0f;
+  auto chunk = [&](int tile) QMM_INLINE {   // pages from this tile's first on
+    const int t = tile * kTile + (lane << BT);
+    const int p = t < most ? row[t >> BT] : -1;   // most <= W << BT
+    pages = p < c.pages ? p : -1;
+    const int64_t blk = (int64_t)(pages < 0 ? 0 : pages) * c.heads + head;
+    pages_ks = c.ks[blk];
+    pages_vs = c.vs[blk];
   };
-  // The loads run ahead of their use: a tile's pages are looked up one tile
-  // before its codes are asked for, its key codes while the tile before is
-  // weighed, its value codes once the values of the tile before are spent.
-  const int kg = (col / 4) * 16;   // first token of this lane's K rows in a tile
-  int pk, pv;
-  auto look_up = [&](int tile) QMM_INLINE {
-    pk = page_at(tile * kTile + kg);
-    pv = page_at(tile * kTile + g * 16);
+  int pk, pv;      // this lane's pages of keys and values in a tile
+  auto look_up = [&](int i) QMM_INLINE {   // the chunk's i-th tile
+    pk = __shfl(pages, i * kPer + (kg >> BT));
+    pv = __shfl(pages, i * kPer + (g * 16 >> BT));
   };
   u32x4_t kw[4][KD], vw[VD];
   auto fetch_keys = [&]() QMM_INLINE {
@@ -191,7 +219,7 @@ __global__ __launch_bounds__(64 * NW, D == 64 ? 4 : D == 128 ? 3 : 1) void kv8_d
     for (int j = 0; j < 4; j++)
 #pragma unroll
       for (int b = 0; b < KD; b++)
-        kw[j][b] = __builtin_nontemporal_load(
+        kw[j][b] = *(
             reinterpret_cast<const u32x4_t*>(kp + j * 4 * D + b * 64));
   };
   auto fetch_values = [&](int page) QMM_INLINE {
@@ -199,61 +227,32 @@ __global__ __launch_bounds__(64 * NW, D == 64 ? 4 : D == 128 ? 3 : 1) void kv8_d
                        ((g * 16) & ((1 << BT) - 1));
 #pragma unroll
     for (int i = 0; i < VD; i++)
-      vw[i] = __builtin_nontemporal_load(
+      vw[i] = *(
           reinterpret_cast<const u32x4_t*>(vp + ((i * 16) << BT)));
   };
-  float ks = 0.0f, vs = 0.0f;   // scales of this lane's 16 tokens
-  auto fetch_scales = [&](int page) QMM_INLINE {
-    const int64_t blk = (int64_t)(page < 0 ? 0 : page) * c.heads + head;
-    ks = c.ks[blk];
-    vs = c.vs[blk];
-  };
-  // one tile's weights; MASK: some of its tokens are not seen by some row
-  half8_t pf[2], pl[2];
-  auto weigh = [&]<bool MASK>(const float4_t* sc, float f, float vs, int ve, int left) QMM_INLINE {
-    float p[16];
-    float mx = m_run;
-#pragma unroll
-    for (int i = 0; i < 16; i++) {
-      p[i] = sc[i / 4][i % 4] * f;
-      if constexpr (MASK) p[i] = i <= left ? p[i] : -__builtin_inff();
-      mx = fmaxf(mx, p[i]);
-    }
-    mx = fmaxf(mx, __shfl_xor(mx, 16));
-    mx = fmaxf(mx, __shfl_xor(mx, 32));
-    const float mu = mx == -__builtin_inff() ? 0.0f : mx;
-    if (__any(mx != m_run || ve != v_exp)) {
-      const float al = __builtin_amdgcn_exp2f(m_run - mu);
-      const float down = ldexpf(al, v_exp - ve);
-      l_run *= al;
-#pragma unroll
-      for (int i = 0; i < VD; i++) o[i] *= down;
-      m_run = mx;
-      v_exp = ve;
-    }
-    const float r = ldexpf(vs, -v_exp);
-#pragma unroll
-    for (int i = 0; i < 16; i++) {
-      const float e = __builtin_amdgcn_exp2f(p[i] - mu);
-      l_run += e;
-      float w = e * r;
-      if constexpr (MASK) w = i <= left ? w : 0.0f;
-      pf[i / 8][i % 8] = (_Float16)w;
-      if constexpr (kTwo) pl[i / 8][i % 8] = (_Float16)(w - (float)pf[i / 8][i % 8]);
-    }
-  };
-  int tile = first + wave;
-  if (tile < last) {
-    look_up(tile);
+  const int run = per / NW;   // tiles of a wavefront
+  const int w_first = first + wave * run, w_last = min(w_first + run, last);
+  auto begin = [&](int tile) QMM_INLINE {
+    chunk(tile);
+    look_up(0);
     fetch_keys();
     fetch_values(pv);
-    fetch_scales(pv);
-  }
-  for (; tile < last; tile += NW) {
-    const int base = tile * kTile;
+    // an (empty) use: the wait for the scales belongs here, and not in the
+    // loop, where it would take the code loads in flight with it
+    asm volatile("" : "+v"(pages), "+v"(pages_ks), "+v"(pages_vs));
+  };
+  if (w_first < w_last) begin(w_first);
+  take_queries();
+  for (int from = w_first; from < w_last; from += 1 << BT) {   // a chunk: 64 pages
+   const int count = min(w_last - from, 1 << BT);
+   if (from != w_first) begin(from);
+   for (int i = 0; i < count; i++) {
+    const int base = (from + i) * kTile;
     const int page = pv;
-    const bool more = tile + NW < last;
-    if (more) look_up(tile + NW);
+    const float ks = __shfl(pages_ks, i * kPer + (g * 16 >> BT));
+    const float vs_now = __shfl(pages_vs, i * kPer + (g * 16 >> BT));
+    const bool more = i + 1 < count;
+    if (more) look_up(i + 1);
     float4_t sc[4];
 #pragma unroll
     for (int j = 0; j < 4; j++) sc[j] = float4_t{0, 0, 0, 0};
@@ -268,34 +267,63 @@ __global__ __launch_bounds__(64 * NW, D == 64 ? 4 : D == 128 ? 3 : 1) void kv8_d
         // (the compiler would convert the whole tile first and run out of registers)
         __builtin_amdgcn_sched_barrier(0);
       }
-    const float f = ks * qs, vs_now = vs;
-    if (more) {
-      fetch_keys();
-      fetch_scales(pv);
-    }
+    const float f = ks * qs;
+    if (more) fetch_keys();
     __builtin_amdgcn_sched_barrier(0);
+    float p[16];
+#pragma unroll
+    for (int i = 0; i < 16; i++) p[i] = sc[i / 4][i % 4] * f;
+    float r = vs_now;
+    if (!(base + kTile - 1 <= min_limit && __all(page >= 0))) {
+      // tokens 0 .. left of this lane's 16 are seen; what is not seen weighs
+      // nothing, whatever its scale
+      const int left = page < 0 ? -1 : limit - (base + g * 16);
+#pragma unroll
+      for (int i = 0; i < 16; i++) p[i] = i <= left ? p[i] : -__builtin_inff();
+      r = left < 0 ? 0.0f : r;
+    }
+    float mx = m_run;
+#pragma unroll
+    for (int i = 0; i < 16; i++) mx = fmaxf(mx, p[i]);
+    mx = fmaxf(mx, __shfl_xor(mx, 16));
+    mx = fmaxf(mx, __shfl_xor(mx, 32));
+    const float mu = mx == -__builtin_inff() ? 0.0f : mx;
     // the largest value scale's exponent (NaN and infinity leave it)
-    int ve = (int)(__builtin_bit_cast(uint32_t, vs_now) >> 23 & 255) - 127;
-    if (ve > 127 || page < 0) ve = -126;
+    int ve = (int)(__builtin_bit_cast(uint32_t, r) >> 23 & 255) - 127;
+    ve = ve > 127 ? -126 : ve;
     ve = max(ve, __shfl_xor(ve, 16));
     ve = max(max(ve, __shfl_xor(ve, 32)), v_exp);
-    if (base + kTile - 1 <= min_limit && __all(page >= 0)) {
-      weigh.template operator()<false>(sc, f, vs_now, ve, 0);
-    } else {   // tokens 0 .. left of this lane's 16 are seen
-      const int left = page < 0 ? -1 : limit - (base + g * 16);
-      weigh.template operator()<true>(sc, f, vs_now, ve, left);
-    }
+    const float al = __builtin_amdgcn_exp2f(m_run - mu);
+    const float down = ldexpf(al, v_exp - ve);   // what the values so far shrink by
+    l_run *= al;
+    m_run = mx;
+    v_exp = ve;
+    r = ldexpf(r, -v_exp);
+    // (always: a branch around it costs more registers than it saves cycles)
 #pragma unroll
-    for (int i = 0; i < VD; i++)
+    for (int i = 0; i < VD; i++) o[i] *= down;
 #pragma unroll
-      for (int h = 0; h < 2; h++) {
-        const half8_t vf = codes_f16(vw[i][2 * h], vw[i][2 * h + 1]);
-        o[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, pf[h], o[i], 0, 0, 0);
-        if constexpr (kTwo) o[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, pl[h], o[i], 0, 0, 0);
-        if (h == 1 && i % 2 == 1) __builtin_amdgcn_sched_barrier(0);
+    for (int h = 0; h < 2; h++) {
+      half8_t pf, pl;
+#pragma unroll
+      for (int i = 0; i < 8; i++) {
+        const float e = __builtin_amdgcn_exp2f(p[8 * h + i] - mu);
+        l_run += e;
+        const float w = e * r;
+        pf[i] = (_Float16)w;
+        if constexpr (kTwo) pl[i] = (_Float16)(w - (float)pf[i]);
       }
+#pragma unroll
+      for (int i = 0; i < VD; i++) {
+        const half8_t vf = codes_f16(vw[i][2 * h], vw[i][2 * h + 1]);
+        o[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, pf, o[i], 0, 0, 0);
+        if constexpr (kTwo) o[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, pl, o[i], 0, 0, 0);
+        if (i % 2 == 1) __builtin_amdgcn_sched_barrier(0);
+      }
+    }
     if (more) fetch_values(pv);
     __builtin_amdgcn_sched_barrier(0);
+   }
   }
   l_run += __shfl_xor(l_run, 16);
   l_run += __shfl_xor(l_run, 32);
@@ -313,28 +341,7 @@ __global__ __launch_bounds__(64 * NW, D == 64 ? 4 : D == 128 ? 3 : 1) void kv8_d
   for (int i = 0; i < VD; i++)
     *reinterpret_cast<float4_t*>(jo + ((wave * 16 + col) * D + i * 16 + g * 4)) = o[i] * vref;
   __syncthreads();
-  const int Hq = c.heads * a.G;
-  auto finish = [&](int r, int d, float v0, float v1, float m, float l) QMM_INLINE {
-    const int64_t at = (int64_t)(t0 + i0 + r / G) * Hq + head * a.G + h0 + r % G;
-    const bool any = l > 0.0f || l != l;
-    const float back = any ? 1.0f / l : 0.0f;
-    *reinterpret_cast<uint32_t*>(a.out + at * D + d) =
-        from_f32(T{}, any ? v0 * back : 0.0f) | (uint32_t)from_f32(T{}, any ? v1 * back : 0.0f) << 16;
-    if (d == 0 && a.lse) a.lse[at] = any ? fmaf(m, kLn2, logf(l)) : -__builtin_inff();
-  };
-  // a part in the workspace: per row the maximum and the sum, then the rows
-  constexpr int kPart = 16 * (D + 2);
-  const int64_t unit = (int64_t)blockIdx.x * gridDim.y + blockIdx.y;
-  float* part = a.ws + unit * a.splits * kPart;
-  auto put2 = [&](float* p, float x, float y) QMM_INLINE {
-    const uint64_t w = __builtin_bit_cast(uint32_t, x) | (uint64_t)__builtin_bit_cast(uint32_t, y) << 32;
-    __hip_atomic_store(reinterpret_cast<uint64_t*>(p), w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  };
-  auto get2 = [&](const float* p) QMM_INLINE {
-    const uint64_t w = __hip_atomic_load(reinterpret_cast<const uint64_t*>(p), __ATOMIC_RELAXED,
-                                         __HIP_MEMORY_SCOPE_AGENT);
-    return make_float2(__builtin_bit_cast(float, (uint32_t)w), __builtin_bit_cast(float, (uint32_t)(w >> 32)));
-  };
+  float* part = a.ws + (((int64_t)blockIdx.x * gridDim.y + blockIdx.y) * a.splits + split) * kPart<D>;
   for (int i = tid; i < rows * (D / 2); i += 64 * NW) {
     const int r = i / (D / 2), d = i % (D / 2) * 2;
     float m = -__builtin_inff();
@@ -351,78 +358,92 @@ __global__ __launch_bounds__(64 * NW, D == 64 ? 4 : D == 128 ? 3 : 1) void kv8_d
       v1 += v.y * e;
     }
     if (parts == 1) {
-      finish(r, d, v0, v1, m, l);
+      const int64_t at = (int64_t)(t0 + i0 + r / G) * (c.heads * a.G) + head * a.G + h0 + r % G;
+      const Share sh = share<T>(v0, v1, l);
+      *reinterpret_cast<uint32_t*>(a.out + at * D + d) = sh.pair;
+      if (d == 0 && a.lse) a.lse[at] = sh.any ? fmaf(m, kLn2, logf(l)) : -__builtin_inff();
     } else {
-      float* mine = part + split * kPart;
-      put2(mine + 32 + r * D + d, v0, v1);
-      if (d == 0) put2(mine + 2 * r, m, l);
+      *reinterpret_cast<float2*>(part + 32 + r * D + d) = make_float2(v0, v1);
+      if (d == 0) *reinterpret_cast<float2*>(part + 2 * r) = make_float2(m, l);
     }
   }
-  if (parts == 1) return;
-  // several workgroups share the rows: the last to arrive joins their parts,
-  // in order. Relaxed agent-scope accesses are coherent across the XCDs' L2
-  // caches; the stores have completed before the counter is touched, and the
-  // wrapping increment leaves it at zero.
-  __shared__ unsigned is_last;
-  __builtin_amdgcn_s_waitcnt(0);
+}
+
+// Joins the parts of one query row (blockIdx.y of the rows of item
+// blockIdx.x / columns): a thread per two of its D values and 1/kSub of the
+// parts. All loads are asked for at once, before anything is known of the
+// sequence: the scratch buffer was written from all over the chip, so each of
+// them takes as long as memory does, and what lies past the sequence's parts
+// is not used. A kernel of its own: its launch costs less than a counter that
+// every workgroup waits for.
+template <class T, int D, int BT>
+__global__ __launch_bounds__(256) void kv8_join_kernel(AttnArgs a) {
+  constexpr int kSub = 512 / D, kEach = kMaxSplits / kSub;
+  __shared__ float fac[kMaxSplits], half[256][2];
+  const int tid = threadIdx.x, lane = tid % 64;
+  const int sub = tid / (D / 2), d = tid % (D / 2) * 2;
+  const int blocks = (a.G + 15) / 16, columns = a.c.heads * blocks;
+  const int index = blockIdx.x / columns, column = blockIdx.x % columns, r = blockIdx.y;
+  const float* part = a.ws + (int64_t)blockIdx.x * a.splits * kPart<D>;
+  float2 v[kEach], ml[kMaxSplits / 64];
+#pragma unroll
+  for (int k = 0; k < kMaxSplits / 64; k++)
+    if (k * 64 + lane < a.splits)
+      ml[k] = *reinterpret_cast<const float2*>(part + (k * 64 + lane) * kPart<D> + 2 * r);
+#pragma unroll
+  for (int k = 0; k < kEach; k++)
+    if (k * kSub + sub < a.splits)
+      v[k] = *reinterpret_cast<const float2*>(part + (k * kSub + sub) * kPart<D> + 32 + r * D + d);
+  const int head = column / blocks, h0 = column % blocks * 16, G = min(16, a.G - h0);
+  const SeqAt q = locate(a.q, index, a.unit, a.extra, BT);
+  const int i0 = q.item * a.unit;
+  if (q.item < 0 || i0 >= q.count || (int64_t)q.count * a.G > a.many) return;
+  const int ntok = min(q.count - i0, a.unit);
+  if (r >= ntok * G) return;
+  const int most = q.len - q.count + i0 + ntok;
+  const int tiles = most > 0 ? (most + kTile - 1) / kTile : 0;
+  const int parts = (tiles + a.per - 1) / a.per;
+  if (parts <= 1) return;   // written already
+  // the parts' factors exp2(m - max) and the sum, by every wavefront
+  float m = -__builtin_inff(), l = 0.0f;
+#pragma unroll
+  for (int k = 0; k < kMaxSplits / 64; k++)
+    if (k * 64 + lane < parts) m = fmaxf(m, ml[k].x);
+#pragma unroll
+  for (int x = 32; x >= 1; x >>= 1) m = fmaxf(m, __shfl_xor(m, x));
+  const float mu = m == -__builtin_inff() ? 0.0f : m;
+#pragma unroll
+  for (int k = 0; k < kMaxSplits / 64; k++)
+    if (k * 64 + lane < parts) {
+      const float e = __builtin_amdgcn_exp2f(ml[k].x - mu);
+      l += ml[k].y * e;
+      if (tid < 64) fac[k * 64 + lane] = e;
+    }
+#pragma unroll
+  for (int x = 32; x >= 1; x >>= 1) l += __shfl_xor(l, x);
   __syncthreads();
-  if (tid == 0)
-    is_last = __builtin_amdgcn_atomic_inc32(a.cnt + unit, (unsigned)(parts - 1), __ATOMIC_RELAXED,
-                                            "agent") == (unsigned)(parts - 1);
-  __syncthreads();
-  if (!is_last) return;
-  // every part's factor exp2(m - max) per row, and the rows' sums
-  float* fac = jo;                       // [parts][16]; parts <= kMaxSplits
-  for (int i = tid; i < parts * rows; i += 64 * NW) {
-    const float2 ml = get2(part + i / rows * kPart + 2 * (i % rows));
-    fac[i / rows * 16 + i % rows] = ml.x;
-    fac[(kMaxSplits + i / rows) * 16 + i % rows] = ml.y;
+  float v0 = 0.0f, v1 = 0.0f;
+#pragma unroll
+  for (int k = 0; k < kEach; k++) {
+    const int w = k * kSub + sub;
+    if (w < parts) {
+      v0 = fmaf(v[k].x, fac[w], v0);
+      v1 = fmaf(v[k].y, fac[w], v1);
+    }
   }
+  half[tid][0] = v0;
+  half[tid][1] = v1;
   __syncthreads();
-  for (int r = wave; r < rows; r += NW) {   // a wavefront per row
-    float m = -__builtin_inff();
-    for (int w = lane; w < parts; w += 64) m = fmaxf(m, fac[w * 16 + r]);
+  if (sub > 0) return;
 #pragma unroll
-    for (int x = 32; x >= 1; x >>= 1) m = fmaxf(m, __shfl_xor(m, x));
-    const float mu = m == -__builtin_inff() ? 0.0f : m;
-    float l = 0.0f;
-    for (int w = lane; w < parts; w += 64) {
-      const float e = __builtin_amdgcn_exp2f(fac[w * 16 + r] - mu);
-      fac[w * 16 + r] = e;
-      l += fac[(kMaxSplits + w) * 16 + r] * e;
-    }
-#pragma unroll
-    for (int x = 32; x >= 1; x >>= 1) l += __shfl_xor(l, x);
-    if (lane == 0) {
-      jm[0][r] = m;
-      jl[0][r] = l;
-    }
+  for (int k = 1; k < kSub; k++) {
+    v0 += half[tid + k * (D / 2)][0];
+    v1 += half[tid + k * (D / 2)][1];
   }
-  __syncthreads();
-  for (int i = tid; i < rows * (D / 2); i += 64 * NW) {
-    const int r = i / (D / 2), d = i % (D / 2) * 2;
-    float v0 = 0.0f, v1 = 0.0f;
-    const float* p = part + 32 + r * D + d;
-    int w = 0;
-    for (; w + 8 <= parts; w += 8) {   // eight loads in flight
-      float2 v[8];
-#pragma unroll
-      for (int x = 0; x < 8; x++) v[x] = get2(p + (w + x) * kPart);
-#pragma unroll
-      for (int x = 0; x < 8; x++) {
-        const float e = fac[(w + x) * 16 + r];
-        v0 = fmaf(v[x].x, e, v0);
-        v1 = fmaf(v[x].y, e, v1);
-      }
-    }
-    for (; w < parts; w++) {
-      const float2 v = get2(p + w * kPart);
-      const float e = fac[w * 16 + r];
-      v0 = fmaf(v.x, e, v0);
-      v1 = fmaf(v.y, e, v1);
-    }
-    finish(r, d, v0, v1, jm[0][r], jl[0][r]);
-  }
+  const int64_t at = (int64_t)(q.first + i0 + r / G) * (a.c.heads * a.G) + head * a.G + h0 + r % G;
+  const Share sh = share<T>(v0, v1, l);
+  *reinterpret_cast<uint32_t*>(a.out + at * D + d) = sh.pair;
+  if (d == 0 && a.lse) a.lse[at] = sh.any ? fmaf(m, kLn2, logf(l)) : -__builtin_inff();
 }
 
 // ------------------------------------------------------------------ prompts
@@ -453,15 +474,15 @@ __global__ __launch_bounds__(64 * NW) void kv8_prompt_kernel(AttnArgs a) {
   auto key_piece = [](int r, int p) QMM_INLINE {
     return (p ^ (D == 64 ? r >> 1 : r)) & (D / 8 - 1);
   };
-  const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
+  const int tid = threadIdx.x, lane = tid % 64;
+  const int wave = __builtin_amdgcn_readfirstlane(tid / 64);   // uniform: scalar
   const int col = lane % 32, h = lane / 32;
   const int head = blockIdx.y;
   const Kv8& c = a.c;
   // long sequences' last items have most to do: they come first
   const int index = gridDim.x - 1 - blockIdx.x;
-  const int s = find_seq(a.q, index, a.unit, a.extra);
-  const int t0 = a.q.first(s), n = a.q.count(s), len = a.q.length(s, c.bt_log2);
-  const int item = index - first_item(a.q, s, a.unit, a.extra);
+  const SeqAt seq = locate(a.q, index, a.unit, a.extra, c.bt_log2);
+  const int s = seq.s, t0 = seq.first, n = seq.count, len = seq.len, item = seq.item;
   const int i0 = item * a.unit;
   if (item < 0 || i0 >= n || (int64_t)n * a.G <= a.many) return;
   const int ntok = min(n - i0, a.unit);
@@ -693,7 +714,7 @@ __global__ __launch_bounds__(64 * NW) void kv8_prompt_kernel(AttnArgs a) {
 constexpr int kFewRows = 64;
 
 struct Plan {
-  int unit, extra, splits, per, nw, many;
+  int unit, extra, splits, per, nw, many, most_rows;
   int64_t items, columns;   // grid: items x heads and blocks of a group's heads
   bool prompts;
   int p_unit;
@@ -712,18 +733,29 @@ Plan plan(const Kv8& c, int64_t T, int64_t Hq, int64_t S, int64_t W) {
   p.extra = p.unit > 1 ? 1 : 0;
   p.items = T / p.unit + p.extra * S;
   p.columns = c.heads * ((G + 15) / 16);
+  p.most_rows = (int)(p.unit * (G < 16 ? G : 16));
   p.p_unit = (int)(prompt_rows / (G < prompt_rows ? G : prompt_rows));
   p.p_items = T / p.p_unit + S;
-  p.nw = kDecodeWaves;
   const int64_t units = (T < p.items ? T : p.items) * p.columns;
   const int64_t tiles = ((W << c.bt_log2) + kTile - 1) / kTile;
-  // Every workgroup takes the same number of tiles (a multiple of the
-  // wavefronts), so that ragged sequences load the chip evenly: as many as
-  // make about 2048 workgroups of sequences that fill their table rows, and
-  // no sequence is cut into more parts than one workgroup joins.
+  // Every workgroup takes the same number of tiles, so that ragged sequences
+  // load the chip evenly: as many as make 2048 workgroups of sequences that
+  // fill their table rows, and no more than kMaxSplits parts of a sequence.
+  // Contexts of up to 24 tiles are not cut: eight wavefronts walk them in
+  // three steps, which costs less than the second launch that joins parts.
+  // (48 contexts to 8192 tokens, 8 heads: 111 us with parts of 24 tiles and 4
+  // wavefronts, 134 us with 8, 119 us with 10 tiles and 1; one context of
+  // 131071 tokens, 2 heads: 23.8 us with 128 parts, 26.7 with 64, 37 with 1
+  // wavefront.)
+  const int64_t cut = (tiles + kMaxSplits - 1) / kMaxSplits;
   int64_t per = (units * tiles + 2047) / 2048;
-  per = per > (tiles + kMaxSplits - 1) / kMaxSplits ? per : (tiles + kMaxSplits - 1) / kMaxSplits;
-  if (p.items * p.columns > kScratchCounters) per = tiles;
+  per = per > cut ? per : cut;
+  p.nw = 4;
+  if (tiles <= 24) {
+    p.nw = c.dim == 256 ? 4 : 8;
+    per = tiles;
+  }
+  if (p.items * p.columns * cut > (1 << 20)) per = tiles;
   per = (per + p.nw - 1) / p.nw * p.nw;
   p.per = (int)per;
   const int64_t sp = (tiles + per - 1) / per;
@@ -741,17 +773,24 @@ int64_t kv8_attention_work(const Kv8& c, int64_t T, int64_t Hq, int64_t S, int64
 hipError_t launch_kv8_attention(const Kv8& c, int dt, const void* q, int64_t ldq, int64_t T,
                                 int64_t Hq, const int32_t* table, const int32_t* lens,
                                 const int32_t* cu, int64_t S, int64_t W, float scale, void* out,
-                                float* lse, unsigned* cnt, float* ws, hipStream_t st) {
+                                float* lse, float* ws, hipStream_t st) {
   const Plan p = plan(c, T, Hq, S, W);
   AttnArgs a{c, {table, lens, cu, (int)S, (int)W, (int)T}, static_cast<const uint16_t*>(q), ldq,
              (int)(Hq / c.heads), p.unit, p.extra, p.many, fabsf(scale) * kLog2e,
-             scale < 0 ? 0x80008000u : 0u, static_cast<uint16_t*>(out), lse, p.splits, p.per, ws, cnt};
+             scale < 0 ? 0x80008000u : 0u, static_cast<uint16_t*>(out), lse, p.splits, p.per, ws};
   const dim3 grid((unsigned)p.items, (unsigned)p.columns, (unsigned)p.splits);
   auto go = [&]<class T_, int D>() {
-    constexpr int NW = kDecodeWaves;
-    const size_t lds = (size_t)NW * 16 * D * 4;
     auto decode = [&]<int BT>() {
-      hipLaunchKernelGGL((kv8_decode_kernel<T_, D, BT, NW>), grid, dim3(64 * NW), lds, st, a);
+      auto waves = [&]<int NW>() {
+        hipLaunchKernelGGL((kv8_decode_kernel<T_, D, BT, NW>), grid, dim3(64 * NW), NW * 16 * D * 4,
+                           st, a);
+      };
+      if (p.nw == 4) waves.template operator()<4>();
+      else waves.template operator()<D == 256 ? 4 : 8>();
+      if (p.splits > 1)
+        hipLaunchKernelGGL((kv8_join_kernel<T_, D, BT>),
+                           dim3((unsigned)(p.items * p.columns), (unsigned)p.most_rows),
+                           dim3(256), 0, st, a);
     };
     if (c.bt_log2 == 4) decode.template operator()<4>();
     else if (c.bt_log2 == 5) decode.template operator()<5>();

@@ -28,37 +28,46 @@ struct Kv8Seqs {
   const int32_t* lens;    // [S]
   const int32_t* cu;      // [S + 1]
   int S, W, T;            // T <= 2^24
-  // (values of one sequence are the same in every lane: they belong in scalar
-  // registers, which the compiler does not see through the loads)
-  __device__ int first(int s) const {
-    const int c = __builtin_amdgcn_readfirstlane(cu[s]);
-    return c < 0 ? 0 : c > T ? T : c;
-  }
-  __device__ int count(int s) const {
-    const int n = first(s + 1) - first(s);
-    return n < 0 ? 0 : n;
-  }
-  __device__ int length(int s, int bt_log2) const {
-    const int64_t most = (int64_t)W << bt_log2;
-    const int n = __builtin_amdgcn_readfirstlane(lens[s]);
-    return n < 0 ? 0 : n > most ? (int)most : n;
-  }
+  __device__ int clip_row(int c) const { return c < 0 ? 0 : c > T ? T : c; }
 };
 
 // Work items of a ragged batch, `unit` new tokens each: sequence s owns items
 // cu[s] / unit + extra * s .. cu[s+1] / unit + extra * (s+1), at least count /
-// unit + extra of them. Returns the sequence that owns item i (binary search).
-__device__ __forceinline__ int first_item(const Kv8Seqs& q, int s, int unit, int extra) {
-  return (uint32_t)q.first(s) / (uint32_t)unit + extra * s;
-}
-__device__ __forceinline__ int find_seq(const Kv8Seqs& q, int i, int unit, int extra) {
-  int lo = 0, hi = q.S;   // the item belongs to a sequence in [lo, hi)
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (first_item(q, mid, unit, extra) <= i) lo = mid;
-    else hi = mid;
+// unit + extra of them. locate() finds the sequence that owns item i (the last
+// one whose items start at or before i) and what a workgroup needs to know
+// of it. It is the first link of a chain of dependent loads (sequence, pages,
+// codes), so the lanes look at 63 boundaries at once: one round trip up to 63
+// sequences, two up to 4000.
+struct SeqAt {
+  int s, first, count, len;   // new tokens are rows first .. first + count
+  int item;                   // index of the work item in the sequence
+};
+__device__ __forceinline__ SeqAt locate(const Kv8Seqs& q, int i, int unit, int extra, int bt_log2) {
+  const int lane = threadIdx.x % 64;
+  auto starts = [&](int c, int j) QMM_INLINE {
+    return (int)((uint32_t)q.clip_row(c) / (uint32_t)unit) + extra * j <= i;
+  };
+  int lo = 0, n = q.S;   // the sequence is one of lo .. lo + n
+  while (n > 63) {
+    const int step = (n + 62) / 63, j = lo + lane * step;
+    const bool at = lane < 63 && j < lo + n && starts(q.cu[j < q.S ? j : q.S], j);
+    const int c = max(__builtin_popcountll(__ballot(at)), 1) - 1;
+    n = min(step, n - c * step);
+    lo += c * step;
   }
-  return lo;
+  const int j = min(lo + lane, q.S);
+  const int c = q.cu[j], l = q.lens[min(j, q.S - 1)];
+  const int k = max(__builtin_popcountll(__ballot(lane < n && starts(c, j))), 1) - 1;
+  // (the same in every lane: scalar registers)
+  SeqAt r;
+  r.s = __builtin_amdgcn_readfirstlane(lo + k);
+  r.first = q.clip_row(__builtin_amdgcn_readlane(c, k));
+  r.count = max(q.clip_row(__builtin_amdgcn_readlane(c, k + 1)) - r.first, 0);
+  const int64_t most = (int64_t)q.W << bt_log2;
+  const int len = max(__builtin_amdgcn_readlane(l, k), 0);
+  r.len = len > most ? (int)most : len;
+  r.item = i - ((int)((uint32_t)r.first / (uint32_t)unit) + extra * r.s);
+  return r;
 }
 
 // Copies part `part` of `parts` of a page (codes, and with part 0 the scales)

@@ -128,7 +128,7 @@ int64_t qmm_i8_t_work(int64_t M, int64_t N, int64_t K) {
 }
 
 int64_t qmm_i8_linear_work(int64_t M, int64_t N, int64_t K) {
-  if (M < 1 || N < 1 || K < 16) return 0;
+  if (M < 1 || N < 1 || K < 16 || qmm::i8_fused(M, K)) return 0;
   return kCounterBytes + up16(M * K) + up16(4 * M) + qmm::i8_plan(M, N, K).ws_bytes;
 }
 
@@ -168,6 +168,10 @@ qmm_status qmm_i8_linear(const void* x, int64_t ldx, const int8_t* wq, const flo
   if (qmm_status s = i8_common(tag, wq, sw, bias, dt, M, N, K, y)) return s;
   if (qmm_status s = check_i8_rows(tag, x, ldx, K)) return s;
   if (qmm_status s = check_work(tag, work, work_bytes, qmm_i8_linear_work(M, N, K))) return s;
+  if (qmm::i8_fused(M, K))
+    return launched(qmm::launch_i8_fused((int)dt, x, ldx, wq, sw, bias, M, N, K, y,
+                                         (hipStream_t)stream),
+                    tag);
   char* p = past_counters(work);
   int8_t* xq = reinterpret_cast<int8_t*>(p);
   float* sx = reinterpret_cast<float*>(p + up16(M * K));

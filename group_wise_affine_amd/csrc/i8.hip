@@ -41,11 +41,12 @@ __global__ __launch_bounds__(256) void i8_quantize_kernel(const uint16_t* __rest
     }
   uint32_t top = wave_umax(amax_halves(m));
   if constexpr (NT > 64) {
-    __shared__ uint32_t part[NT / 64];
-    if (t % 64 == 0) part[t / 64] = top;
+    __shared__ uint32_t part[4];   // of the row's NT / 64 wavefronts
+    const int wave = threadIdx.x / 64, w0 = wave - t / 64;
+    if (t % 64 == 0) part[wave] = top;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < NT / 64; i++) top = part[i] > top ? part[i] : top;
+    for (int i = 0; i < NT / 64; i++) top = part[w0 + i] > top ? part[w0 + i] : top;
   }
   if (!live) return;
   const float s = amax_scale<T>(top);
@@ -75,7 +76,6 @@ __global__ __launch_bounds__(256) void i8_quantize_kernel(const uint16_t* __rest
 // lane%16, both k = 16 * (lane/16) .. +16; D column lane%16, rows
 // 4 * (lane/16) .. +4.
 constexpr int kGvWaves = 8;
-constexpr int kGvHold = 4;   // pieces in flight per wavefront
 
 template <class T>
 __device__ __forceinline__ uint16_t i8_out(int acc, float sx, float sw, const uint16_t* bias,
@@ -85,33 +85,89 @@ __device__ __forceinline__ uint16_t i8_out(int acc, float sx, float sw, const ui
   return from_f32(T{}, v);
 }
 
-template <class T, int MT>
+// FUSED: x itself (at most kGvChunks * 512 pieces of 8, at most 16 rows) comes
+// in, and every workgroup quantizes it into LDS while its first pieces of W
+// are on their way; otherwise codes and scales come in.
+// (13 x 2048: 14.2 us fused, 10.6 us in two launches; 1 x 4096: 5.7 and 10.0.)
+constexpr int kGvChunks = 2;
+
+template <class T, int MT, bool FUSED>
 __global__ __launch_bounds__(64 * kGvWaves) void i8_gemv_kernel(
-    const int8_t* __restrict__ xq, const float* __restrict__ sx, const int8_t* __restrict__ wq,
-    const float* __restrict__ sw, const uint16_t* __restrict__ bias, uint16_t* __restrict__ y,
-    int M, int N, int K) {
+    const uint16_t* __restrict__ x, int64_t ldx, const int8_t* __restrict__ xq,
+    const float* __restrict__ sx, const int8_t* __restrict__ wq, const float* __restrict__ sw,
+    const uint16_t* __restrict__ bias, uint16_t* __restrict__ y, int M, int N, int K) {
+  constexpr int kThreads = 64 * kGvWaves;
+  constexpr int kGvHold = MT <= 2 ? 4 : 2;   // pieces in flight per wavefront
   __shared__ int part[kGvWaves][MT * 256];
-  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+  __shared__ uint32_t top[16];
+  extern __shared__ __attribute__((aligned(16))) uint8_t codes[];   // FUSED: [M][K + 16]
+  const int tid = threadIdx.x, lane = tid % 64;
+  const int wave = __builtin_amdgcn_readfirstlane(tid / 64);
   const int r = lane % 16, g = lane / 16;
   const int64_t n0 = (int64_t)blockIdx.x * 16, m0 = (int64_t)blockIdx.y * 16 * MT;
   const int wrows = (int)(N - n0 < 16 ? N - n0 : 16);
   const int xrows = (int)(M - m0 < 16 * MT ? M - m0 : 16 * MT);
   const __amdgpu_buffer_rsrc_t rw = make_rsrc(wq + n0 * K, (uint32_t)wrows * (uint32_t)K);
-  const __amdgpu_buffer_rsrc_t rx = make_rsrc(xq + m0 * K, (uint32_t)xrows * (uint32_t)K);
+  const __amdgpu_buffer_rsrc_t rx = make_rsrc(xq + m0 * K, FUSED ? 0u : (uint32_t)xrows * (uint32_t)K);
   int4_t acc[MT];
 #pragma unroll
   for (int i = 0; i < MT; i++) acc[i] = int4_t{0, 0, 0, 0};
   const uint32_t row = (uint32_t)r * (uint32_t)K;
   // out-of-range pieces and rows load zeros
-  auto at = [&](uint32_t base, int k) QMM_INLINE { return k < K ? base + (uint32_t)k : kOob; };
-  for (int k0 = wave * 128; k0 < K; k0 += kGvWaves * 128 * kGvHold) {
-    u32x4_t w[kGvHold][2];
+  auto at = [&](uint32_t base, int k) QMM_INLINE { return base + (k < K ? (uint32_t)k : kOob); };
+  u32x4_t w[kGvHold][2];
+  auto fetch = [&](int k0) QMM_INLINE {
 #pragma unroll
     for (int i = 0; i < kGvHold; i++)
 #pragma unroll
       for (int h = 0; h < 2; h++)
         w[i][h] = __builtin_amdgcn_raw_buffer_load_b128(
             rw, (int)at(row, k0 + i * kGvWaves * 128 + h * 64 + g * 16), 0, 0);
+  };
+  fetch(wave * 128);
+  const int ldc = K + 16;   // (16 rows' pieces fall on different banks)
+  if constexpr (FUSED) {
+    const int per = K / 8, pieces = M * per;
+    uint4 u[kGvChunks];
+    if (tid < 16) top[tid] = 0;
+#pragma unroll
+    for (int i = 0; i < kGvChunks; i++) {
+      const int c = i * kThreads + tid, m = c / per;
+      if (c < pieces) u[i] = *reinterpret_cast<const uint4*>(x + m * ldx + (c - m * per) * 8);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kGvChunks; i++) {
+      const int c = i * kThreads + tid;
+      if (i * kThreads + wave * 64 >= pieces) break;
+      const int m = min(c, pieces - 1) / per;
+      const uint32_t v = c < pieces ? amax_halves(amax_pair(amax_pair(amax_pair(amax_pair(0, u[i].x), u[i].y), u[i].z), u[i].w)) : 0;
+      if (__all(m == __builtin_amdgcn_readfirstlane(m))) {   // one row: one update
+        const uint32_t a = wave_umax(v);
+        if (lane == 0) atomicMax(&top[m], a);
+      } else if (c < pieces) {
+        atomicMax(&top[m], v);
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kGvChunks; i++) {
+      const int c = i * kThreads + tid, m = c / per;
+      if (c < pieces) {
+        const Divisor d = divisor(amax_scale<T>(top[m]));
+        float f[8], q[8];
+        unpack8(T{}, u[i], f);
+        divide_round<8>(f, d, q);
+        *reinterpret_cast<uint2*>(codes + m * ldc + (c - m * per) * 8) =
+            make_uint2(pack_codes(q[0], q[1], q[2], q[3]), pack_codes(q[4], q[5], q[6], q[7]));
+      }
+    }
+    __syncthreads();
+  }
+  for (int k0 = wave * 128; k0 < K; k0 += kGvWaves * 128 * kGvHold) {
+    if (k0 > wave * 128) fetch(k0);
+    // x comes from the L2 (or LDS); all of it is asked for before its first use
+    u32x4_t xv[MT][kGvHold][2];
 #pragma unroll
     for (int i = 0; i < kGvHold; i++)
 #pragma unroll
@@ -119,36 +175,48 @@ __global__ __launch_bounds__(64 * kGvWaves) void i8_gemv_kernel(
         const int k = k0 + i * kGvWaves * 128 + h * 64 + g * 16;
 #pragma unroll
         for (int t = 0; t < MT; t++) {
-          const u32x4_t xv = __builtin_amdgcn_raw_buffer_load_b128(
-              rx, (int)at(row + (uint32_t)(t * 16) * (uint32_t)K, k), 0, 0);
-          acc[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(int4_t, w[i][h]),
-                                                         __builtin_bit_cast(int4_t, xv), acc[t],
-                                                         0, 0, 0);
+          if constexpr (FUSED)   // (past K: the last piece again, W is zero there)
+            xv[t][i][h] = *reinterpret_cast<const u32x4_t*>(codes + min(r, M - 1) * ldc + min(k, K - 16));
+          else
+            xv[t][i][h] = __builtin_amdgcn_raw_buffer_load_b128(
+                rx, (int)at(row + (uint32_t)(t * 16) * (uint32_t)K, k), 0, 0);
         }
       }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < kGvHold; i++)
+#pragma unroll
+      for (int h = 0; h < 2; h++)
+#pragma unroll
+        for (int t = 0; t < MT; t++)
+          acc[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(
+              __builtin_bit_cast(int4_t, w[i][h]), __builtin_bit_cast(int4_t, xv[t][i][h]), acc[t],
+              0, 0, 0);
   }
 #pragma unroll
   for (int t = 0; t < MT; t++)
 #pragma unroll
     for (int e = 0; e < 4; e++) part[wave][t * 256 + r * 16 + g * 4 + e] = acc[t][e];
   __syncthreads();
-  for (int i = threadIdx.x; i < MT * 256; i += 64 * kGvWaves) {
+  for (int i = tid; i < MT * 256; i += kThreads) {
     const int64_t m = m0 + i / 16, n = n0 + i % 16;
     if (m >= M || n >= N) continue;
     int s = 0;
 #pragma unroll
     for (int v = 0; v < kGvWaves; v++) s += part[v][i];
-    y[m * N + n] = i8_out<T>(s, sx[m], sw[n], bias, n);
+    const float sm = FUSED ? amax_scale<T>(top[i / 16]) : sx[m];
+    y[m * N + n] = i8_out<T>(s, sm, sw[n], bias, n);
   }
 }
 
 // ---------------------------------------------------------------- tile GEMM
 // BM rows of x by BN rows of W per workgroup, WM x WN wavefronts. K advances
-// in steps of 128 bytes through two LDS slots filled by direct
-// global-to-LDS copies; inside a slot row r's 16-byte piece c sits at
-// position c ^ (r / 2 & 7), so the 16 rows that are read together touch all
-// banks. W is the A operand, so a lane ends up with runs of four consecutive
-// n of one row of y.
+// in steps of 128 bytes (whole cache lines of every row: steps of 64 in twice
+// as many slots cost 52 instead of 42 us at 2048 x 4096 x 4096) through a ring of
+// NS LDS slots filled by direct global-to-LDS copies, NS - 1 steps ahead. Inside
+// a slot row r's 16-byte piece c sits at position c ^ (r / 2 & 7), so the 16
+// rows that are read together touch all banks. W is the A operand, so a lane
+// ends up with runs of four consecutive n of one row of y.
 struct I8Args {
   const int8_t* xq;
   const float* sx;
@@ -244,14 +312,15 @@ __device__ __forceinline__ void settle(int16v_t (&c)[R][R]) {
 #undef QMM_LD
 #undef QMM_MM
 
-template <class T, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(64 * WM * WN, BM * BN == 65536 ? 1 : 2) void i8_tile_kernel(I8Args a) {
+template <class T, int BM, int BN, int WM, int WN, int NS>
+__global__ __launch_bounds__(64 * WM * WN, BM * BN == 65536 || NS > 2 ? 1 : 2) void i8_tile_kernel(I8Args a) {
   constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
   constexpr int TM = BM / WM / 32, TN = BN / WN / 32;   // 32x32 tiles per wavefront
   constexpr int kRows = BM + BN;
   constexpr int kLoads = kRows * 8 / kThreads;          // 16-byte pieces per thread and step
+  constexpr int kSlot = kRows * 128;
   static_assert(BM * 8 % kThreads == 0 && BN * 8 % kThreads == 0 && TM == TN, "shape");
-  __shared__ __attribute__((aligned(128))) uint8_t lds[2][kRows * 128];
+  __shared__ __attribute__((aligned(128))) uint8_t lds[NS * kSlot];
   const int tid = threadIdx.x, lane = tid % 64;
   const int wave = __builtin_amdgcn_readfirstlane(tid / 64);   // uniform: scalar
   const int tiles_n = (a.N + BN - 1) / BN, tiles_m = (a.M + BM - 1) / BM;
@@ -281,8 +350,7 @@ __global__ __launch_bounds__(64 * WM * WN, BM * BN == 65536 ? 1 : 2) void i8_til
   // piece i of this thread: row (i * kThreads + tid) / 8 of [x rows | W rows];
   // pieces past K are out of every row's range and become zeros
   const int c = (tid % 8) ^ (tid / 16 % 8);
-  auto copy = [&](int step) QMM_INLINE {
-    uint8_t* slot = lds[step % 2];
+  auto copy = [&](int step, int at) QMM_INLINE {
     const uint32_t k = (uint32_t)(k_begin + step * 128 + c * 16);
     const uint32_t off = (tid / 8) * (uint32_t)a.K + (k < (uint32_t)a.K ? k : kOob);
 #pragma unroll
@@ -290,7 +358,7 @@ __global__ __launch_bounds__(64 * WM * WN, BM * BN == 65536 ? 1 : 2) void i8_til
       constexpr int kX = BM * 8 / kThreads;
       const int row = (i < kX ? i : i - kX) * (kThreads / 8);
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          i < kX ? rx : rw, (lds_ptr_t*)(slot + (i * kThreads + wave * 64) * 16), 16,
+          i < kX ? rx : rw, (lds_ptr_t*)(lds + at + (i * kThreads + wave * 64) * 16), 16,
           (int)(off + (uint32_t)row * (uint32_t)a.K), 0, 0, 0);
     }
   };
@@ -306,27 +374,30 @@ __global__ __launch_bounds__(64 * WM * WN, BM * BN == 65536 ? 1 : 2) void i8_til
   // LDS byte addresses of this lane's operand rows; the permuted position of
   // a K piece depends on the row's low bits only, which are the same for all
   // of a wavefront's tiles
-  const uint32_t base = (uint32_t)(uintptr_t)(lds_ptr_t*)&lds[0][0];
+  const uint32_t base = (uint32_t)(uintptr_t)(lds_ptr_t*)&lds[0];
   const uint32_t at_x = base + (uint32_t)(wm * TM * 32 + lr) * 128;
   const uint32_t at_w = base + (uint32_t)(BM + wn * TN * 32 + lr) * 128;
-  auto piece = [&](int step, int ks) QMM_INLINE {
-    return (uint32_t)(step % 2) * (kRows * 128) + (uint32_t)(((ks * 2 + lh) ^ (lr >> 1)) & 7) * 16;
-  };
+  auto piece = [&](int ks) QMM_INLINE { return (uint32_t)(((ks * 2 + lh) ^ (lr >> 1)) & 7) * 16; };
+  // copies past the last step bring zeros, or the next split's data, unused
+#pragma unroll
+  for (int s = 0; s < NS - 1; s++) copy(s, s * kSlot);
+  ring_wait<(NS - 2) * kLoads>();
+  copy(NS - 1, (NS - 1) * kSlot);
   Operands<TN> u[2];
-  copy(0);
-  ring_wait<0>();
-  copy(1);   // past the last step: zeros, or the next split's, and unused
-  read_operands(at_w + piece(0, 0), at_x + piece(0, 0), u[0]);
+  read_operands(at_w + piece(0), at_x + piece(0), u[0]);
+  int slot = 0;
   for (int step = 0; step < steps; step++) {
 #pragma unroll
     for (int ks = 0; ks < 4; ks++) {
+      const int from = slot;
       if (ks == 3) {
-        // every wavefront has read the last piece of this step's slot, and the
-        // copies of the next step, issued one step ago, have landed
-        ring_wait<0>();
-        copy(step + 2);
+        // every wavefront has read the last piece of this step's slot, and this
+        // wavefront's copies of the next step have landed
+        ring_wait<(NS - 2) * kLoads>();
+        copy(step + NS, from);
+        slot = from + kSlot < NS * kSlot ? from + kSlot : 0;
       }
-      const uint32_t p = ks < 3 ? piece(step, ks + 1) : piece(step + 1, 0);
+      const uint32_t p = (uint32_t)slot + piece((ks + 1) % 4);
       multiply_read(acc, u[ks % 2], at_w + p, at_x + p, u[(ks + 1) % 2]);
     }
   }
@@ -376,7 +447,7 @@ __global__ __launch_bounds__(64 * WM * WN, BM * BN == 65536 ? 1 : 2) void i8_til
   // whole rows: 16-byte piece p of row r sits at p ^ r modulo the row's pieces.
   constexpr int kRow = TN * 64, kPieces = kRow / 16;   // bytes, pieces of a row
   __syncthreads();
-  uint8_t* mine = &lds[0][0] + wave * (TM * 32 * kRow);
+  uint8_t* mine = &lds[0] + wave * (TM * 32 * kRow);
   auto at = [&](int r, int p) QMM_INLINE {
     return mine + r * kRow + ((p ^ (kPieces == 8 ? r >> 1 : r)) & (kPieces - 1)) * 16;
   };
@@ -442,12 +513,32 @@ hipError_t launch_i8_quantize(int dt, const void* x, int64_t ldx, int64_t rows, 
                               int8_t* xq, float* sx, hipStream_t st) {
   auto go = [&]<class T>() {
     const uint16_t* p = static_cast<const uint16_t*>(x);
-    if (K <= 2048)   // a wavefront holds the whole row
-      hipLaunchKernelGGL((i8_quantize_kernel<T, 64>), dim3((unsigned)((rows + 3) / 4)), dim3(256),
-                         0, st, p, ldx, rows, (int)K, xq, sx);
-    else
-      hipLaunchKernelGGL((i8_quantize_kernel<T, 256>), dim3((unsigned)rows), dim3(256), 0, st, p,
-                         ldx, rows, (int)K, xq, sx);
+    auto threads = [&]<int NT>() {   // per row: they hold 32 * NT elements
+      hipLaunchKernelGGL((i8_quantize_kernel<T, NT>), dim3((unsigned)((rows + 256 / NT - 1) / (256 / NT))),
+                         dim3(256), 0, st, p, ldx, rows, (int)K, xq, sx);
+    };
+    if (K <= 2048) threads.template operator()<64>();
+    else if (K <= 4096) threads.template operator()<128>();
+    else threads.template operator()<256>();
+  };
+  if (dt == 0) go.template operator()<F16>();
+  else go.template operator()<BF16>();
+  return hipGetLastError();
+}
+
+bool i8_fused(int64_t M, int64_t K) {
+  return M <= 16 && M * K <= kGvChunks * 64 * kGvWaves * 8;
+}
+
+hipError_t launch_i8_fused(int dt, const void* x, int64_t ldx, const int8_t* wq, const float* sw,
+                           const void* bias, int64_t M, int64_t N, int64_t K, void* y,
+                           hipStream_t st) {
+  auto go = [&]<class T>() {
+    hipLaunchKernelGGL((i8_gemv_kernel<T, 1, true>), dim3((unsigned)((N + 15) / 16)),
+                       dim3(64 * kGvWaves), (size_t)(M * (K + 16)), st,
+                       static_cast<const uint16_t*>(x), ldx, nullptr, nullptr, wq, sw,
+                       static_cast<const uint16_t*>(bias), static_cast<uint16_t*>(y), (int)M,
+                       (int)N, (int)K);
   };
   if (dt == 0) go.template operator()<F16>();
   else go.template operator()<BF16>();
@@ -461,13 +552,20 @@ I8Plan i8_plan(int64_t M, int64_t N, int64_t K) {
     p.ks = 1;
     return p;
   }
-  p.bm = p.bn = M > 1024 && N >= 256 ? 256 : 128;
+  // A round of 256 large tiles takes 1.8 times as long as one of 512 small ones
+  // (4096 x 4096 x 4096: 75 against 41 us per round), and small tiles end in
+  // smaller steps: the large ones run where their rounds are full enough.
+  auto tiles = [&](int64_t b) { return ((M + b - 1) / b) * ((N + b - 1) / b); };
+  p.bm = p.bn = (tiles(256) + 255) / 256 * 9 * 512 <= tiles(128) * 5 ? 256 : 128;
   p.ks = 1;
-  p.tiles = ((M + p.bm - 1) / p.bm) * ((N + p.bn - 1) / p.bn);
+  p.tiles = tiles(p.bm);
   const int64_t steps = (K + 127) / 128;
-  if (p.bm == 128)   // a few tiles: K over several workgroups, at least 8 steps each
-    while (p.tiles * p.ks * 2 <= 512 && steps / (p.ks * 2) >= 8 && p.ks < 16 &&
-           p.tiles <= kScratchCounters)
+  // A few tiles: K over up to 4 workgroups, at least 8 steps each, while they
+  // fit the chip once. (512 x 4096 x 4096: 24.3 / 21.0 / 25.7 us for 1 / 2 / 4
+  // parts, 128 tiles; 128 x 4096 x 4096: 23.3 / 17.6 / 16.2 / 20.2 for 1 / 2 / 4
+  // / 8, 32 tiles.)
+  if (p.bm == 128)
+    while (p.tiles * p.ks * 2 <= 256 && steps / (p.ks * 2) >= 8 && p.ks < (p.tiles <= 32 ? 4 : 2))
       p.ks *= 2;
   p.steps = (steps + p.ks - 1) / p.ks;
   p.ks = (steps + p.steps - 1) / p.steps;
@@ -485,19 +583,23 @@ hipError_t launch_i8_t(int dt, const int8_t* xq, const float* sx, const int8_t* 
     if (p.gemv) {
       const unsigned nb = (unsigned)((N + 15) / 16);
       auto mv = [&]<int MT>() {
-        hipLaunchKernelGGL((i8_gemv_kernel<T, MT>), dim3(nb, (unsigned)((M + 16 * MT - 1) / (16 * MT))),
-                           dim3(64 * kGvWaves), 0, st, xq, sx, wq, sw, b, yo, (int)M, (int)N, (int)K);
+        hipLaunchKernelGGL((i8_gemv_kernel<T, MT, false>),
+                           dim3(nb, (unsigned)((M + 16 * MT - 1) / (16 * MT))), dim3(64 * kGvWaves),
+                           0, st, nullptr, 0, xq, sx, wq, sw, b, yo, (int)M, (int)N, (int)K);
       };
       if (M <= 16) mv.template operator()<1>();
-      else mv.template operator()<2>();
+      else if (M <= 32) mv.template operator()<2>();
+      else mv.template operator()<4>();
       return;
     }
     I8Args a{xq, sx, wq, sw, b, yo, (int)M, (int)N, (int)K, (int)p.ks, (int)p.steps, ws, cnt};
     const dim3 grid((unsigned)p.tiles, (unsigned)p.ks);
     if (p.bm == 256)
-      hipLaunchKernelGGL((i8_tile_kernel<T, 256, 256, 2, 2>), grid, dim3(256), 0, st, a);
+      hipLaunchKernelGGL((i8_tile_kernel<T, 256, 256, 2, 2, 2>), grid, dim3(256), 0, st, a);
+    else if (p.tiles * p.ks <= 256)   // one workgroup per CU: the LDS is its own
+      hipLaunchKernelGGL((i8_tile_kernel<T, 128, 128, 2, 2, 4>), grid, dim3(256), 0, st, a);
     else
-      hipLaunchKernelGGL((i8_tile_kernel<T, 128, 128, 2, 2>), grid, dim3(256), 0, st, a);
+      hipLaunchKernelGGL((i8_tile_kernel<T, 128, 128, 2, 2, 2>), grid, dim3(256), 0, st, a);
   };
   if (dt == 0) go.template operator()<F16>();
   else go.template operator()<BF16>();

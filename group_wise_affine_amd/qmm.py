@@ -9,7 +9,6 @@ status and RuntimeError if the library has not been built.
 """
 import ctypes
 import os
-import threading
 
 import torch
 
@@ -564,127 +563,92 @@ def force_kernel(kernel):
 
 # ------------------------------------------------------------ serving in 8 bits
 # int8 products and the paged 8-bit cache (the second part of libqmm.h). These
-# calls are short, so their checks are written to cost little.
+# calls are short, so the tensors' checks, the outputs and the scratch buffer
+# are handled by the native part of the binding (csrc/binding.cpp); the
+# functions here are its public face. Checks raise ValueError, the library's
+# refusals QmmError.
 
 WORK_COUNTERS = 65536
-_local = threading.local()
+BINDING_PATH = os.path.join(_HERE, "_serving.so")
+_native = None
+_have_gpu = False
 
 
-def _where(stream, *named):
-    """Checks that the tensors are on the current ROCm device; (device, stream
-    handle)."""
-    dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
-    for name, t in named:
-        if t is not None and (t.get_device() != dev or dev < 0):
-            _check_device((name, t))
-            raise ValueError(f"{name} must be on the current ROCm device, got {t.device}")
-    if stream is None:
-        return dev, torch.cuda.current_stream(dev).cuda_stream
-    return dev, _stream(stream).value or 0
+def _raise(status, msg):
+    raise QmmError(status, msg)
 
 
-def _work(nbytes, dev, handle):
-    """Scratch of at least nbytes for calls on one stream from this thread (kept
-    and reused, as a program's workspace is); (address, bytes)."""
-    if nbytes == 0:
-        return None, 0
-    if torch.cuda.is_current_stream_capturing():   # memory of the graph, cleared in it
-        t = torch.empty(nbytes, dtype=torch.uint8, device=f"cuda:{dev}")
+def _grow(nbytes, dev, handle, capturing):
+    """Scratch for calls on one stream, its counters zero; under capture memory
+    of the graph, cleared in it."""
+    def make(n):
+        t = torch.empty(n, dtype=torch.uint8, device=f"cuda:{dev}")
         t[:WORK_COUNTERS].zero_()
-        return t.data_ptr(), nbytes
-    held = _local.__dict__.setdefault("work", {})
-    t = held.get((dev, handle))
-    if t is None or t.numel() < nbytes:
-        with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=dev)):
-            t = torch.empty(max(nbytes, 1 << 20), dtype=torch.uint8, device=f"cuda:{dev}")
-            t[:WORK_COUNTERS].zero_()
-        held[dev, handle] = t
-    return t.data_ptr(), t.numel()
+        return t
+    if capturing:
+        return make(nbytes)
+    with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=dev)):
+        return make(max(nbytes, 1 << 20))
 
 
-def _rows(t, name):
-    """Stride of the first dimension of a tensor whose other dimensions are
-    packed (a slice of a fused projection's columns)."""
-    width = 1
-    for n, st in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
-        if n != 1 and st != width:
-            raise ValueError(f"{name}: all dimensions but the first must be packed")
-        width *= n
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), width)
+def _serving():
+    """The native part of the binding (raises if it has not been built)."""
+    global _native
+    if _native is None:
+        if not os.path.exists(BINDING_PATH):
+            raise RuntimeError(f"{BINDING_PATH} is missing: build it with `python -c 'import "
+                               f"__graft_entry__ as g; g.build()'` (or group_wise_affine_amd/build.py)")
+        lib()
+        import importlib.util
+        spec = importlib.util.spec_from_file_location("_serving", BINDING_PATH)
+        m = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(m)
+        m.set_hooks(_raise, _grow)
+        _native = m
+    return _native
 
 
-def _is(t, name, shape, dtype):
-    if not isinstance(t, torch.Tensor):
-        raise ValueError(f"{name} must be a torch.Tensor")
-    if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
-        _check_tensor(t, name, shape, dtype)
+def _on(stream):
+    """Handle of the stream to launch on (0 where there is no GPU: the checks of
+    the tensors' device refuse the call)."""
+    if stream is not None:
+        return _stream(stream).value or 0
+    global _have_gpu
+    if not _have_gpu:
+        _have_gpu = torch.cuda.is_available()
+        if not _have_gpu:
+            return 0
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+
+
+def _bf16(dtype):
+    if dtype not in (torch.float16, torch.bfloat16):
+        raise QmmError(QMM_E_DTYPE, f"unsupported dtype {dtype}")
+    return dtype == torch.bfloat16
+
+
+def _cache(cache, name="cache"):
+    if not isinstance(cache, Kv8Cache):
+        raise ValueError(f"{name} must be a Kv8Cache")
+    return cache._at
 
 
 def i8_quantize(x, out=None, stream=None):
     """Rows of x [M, K] (f16 or bf16, rows may be strided) -> (codes int8 [M, K],
     scales fp32 [M]): per-token activations, or a weight [N, K] per channel."""
-    if not isinstance(x, torch.Tensor) or x.dim() != 2:
-        raise ValueError("x must be a tensor of 2 dimensions")
-    M, K = x.shape
-    ld = _rows(x, "x")
-    if out is None:
-        out = (torch.empty((M, K), dtype=torch.int8, device=x.device),
-               torch.empty((M,), dtype=torch.float32, device=x.device))
-    _is(out[0], "codes", (M, K), torch.int8)
-    _is(out[1], "scales", (M,), torch.float32)
-    _, st = _where(stream, ("x", x), ("codes", out[0]), ("scales", out[1]))
-    _check(lib().qmm_i8_quantize(x.data_ptr(), ld, _dt(x.dtype), M, K, out[0].data_ptr(),
-                                 out[1].data_ptr(), st))
-    return out
+    return _serving().i8_quantize(x, out, _on(stream))
 
 
 def i8_t(xq, sx, wq, sw, bias=None, dtype=torch.bfloat16, out=None, stream=None):
     """y [M, N] = (sx[m] sw[n]) (xq . wq^T) + bias in dtype, from codes xq [M, K], wq
     [N, K] and fp32 scales sx [M], sw [N]."""
-    if not isinstance(xq, torch.Tensor) or xq.dim() != 2 or not isinstance(wq, torch.Tensor) or wq.dim() != 2:
-        raise ValueError("xq and wq must be tensors of 2 dimensions")
-    (M, K), N = xq.shape, wq.shape[0]
-    dt = _dt(dtype)
-    if out is None:
-        out = torch.empty((M, N), dtype=dtype, device=xq.device)
-    _is(xq, "xq", (M, K), torch.int8)
-    _is(sx, "sx", (M,), torch.float32)
-    _is(wq, "wq", (N, K), torch.int8)
-    _is(sw, "sw", (N,), torch.float32)
-    _is(out, "out", (M, N), dtype)
-    if bias is not None:
-        _is(bias, "bias", (N,), dtype)
-    dev, st = _where(stream, ("xq", xq), ("sx", sx), ("wq", wq), ("sw", sw), ("bias", bias), ("out", out))
-    L = lib()
-    work, nbytes = _work(L.qmm_i8_t_work(M, N, K), dev, st)
-    _check(L.qmm_i8_t(xq.data_ptr(), sx.data_ptr(), wq.data_ptr(), sw.data_ptr(),
-                      None if bias is None else bias.data_ptr(), dt, M, N, K, out.data_ptr(),
-                      work, nbytes, st))
-    return out
+    return _serving().i8_t(xq, sx, wq, sw, bias, _bf16(dtype), out, _on(stream))
 
 
 def i8_linear(x, wq, sw, bias=None, out=None, stream=None):
     """y [M, N] = x . (sw wq)^T + bias on 8-bit integers: x [M, K] (f16 or bf16, rows
     may be strided) is quantized per row on the way (i8_quantize, then i8_t)."""
-    if not isinstance(x, torch.Tensor) or x.dim() != 2 or not isinstance(wq, torch.Tensor) or wq.dim() != 2:
-        raise ValueError("x and wq must be tensors of 2 dimensions")
-    (M, K), N = x.shape, wq.shape[0]
-    ld = _rows(x, "x")
-    dt = _dt(x.dtype)
-    if out is None:
-        out = torch.empty((M, N), dtype=x.dtype, device=x.device)
-    _is(wq, "wq", (N, K), torch.int8)
-    _is(sw, "sw", (N,), torch.float32)
-    _is(out, "out", (M, N), x.dtype)
-    if bias is not None:
-        _is(bias, "bias", (N,), x.dtype)
-    dev, st = _where(stream, ("x", x), ("wq", wq), ("sw", sw), ("bias", bias), ("out", out))
-    L = lib()
-    work, nbytes = _work(L.qmm_i8_linear_work(M, N, K), dev, st)
-    _check(L.qmm_i8_linear(x.data_ptr(), ld, wq.data_ptr(), sw.data_ptr(),
-                           None if bias is None else bias.data_ptr(), dt, M, N, K,
-                           out.data_ptr(), work, nbytes, st))
-    return out
+    return _serving().i8_linear(x, wq, sw, bias, out, _on(stream))
 
 
 class _Kv8(ctypes.Structure):
@@ -726,57 +690,19 @@ class Kv8Cache:
         self._at = ctypes.addressof(self._c)
 
 
-def _kv8_batch(cache, table, lens, cu):
-    if not isinstance(cache, Kv8Cache):
-        raise ValueError("cache must be a Kv8Cache")
-    if not isinstance(table, torch.Tensor) or table.dim() != 2:
-        raise ValueError("table must be a tensor of 2 dimensions")
-    S, W = table.shape
-    _is(table, "table", (S, W), torch.int32)
-    _is(lens, "lens", (S,), torch.int32)
-    if cu is not None:
-        _is(cu, "cu", (S + 1,), torch.int32)
-    return S, W
-
-
-def _kv8_new(cache, t, name, heads):
-    if not isinstance(t, torch.Tensor) or t.dim() != 3 or t.shape[2] != cache.head_dim or (
-            heads is not None and t.shape[1] != heads):
-        raise ValueError(f"{name} must be a tensor [tokens, {'heads' if heads is None else heads}, "
-                         f"{cache.head_dim}]")
-    return _rows(t, name)
-
-
 def kv8_append(cache, k, v, table, lens, cu, stream=None):
     """Write the new tokens' k and v [T, heads, head_dim] into the cache: sequence s
     owns rows cu[s] .. cu[s+1], its last places; lens [S] counts its tokens with
     them, table [S, W] (int32) names its pages."""
-    S, W = _kv8_batch(cache, table, lens, cu)
-    ldk, ldv = _kv8_new(cache, k, "k", cache.heads), _kv8_new(cache, v, "v", cache.heads)
-    if v.shape != k.shape or v.dtype != k.dtype:
-        raise ValueError("k and v must have one shape and dtype")
-    _, st = _where(stream, ("cache", cache.k), ("k", k), ("v", v), ("table", table),
-                   ("lens", lens), ("cu", cu))
-    _check(lib().qmm_kv8_append(cache._at, k.data_ptr(), ldk, v.data_ptr(), ldv, _dt(k.dtype),
-                                k.shape[0], table.data_ptr(), lens.data_ptr(), cu.data_ptr(), S, W,
-                                st))
+    at = _cache(cache)
+    _serving().kv8_append(at, cache.k, k, v, table, lens, cu, _on(stream))
 
 
 def kv8_read(cache, pages, dtype=torch.bfloat16, stream=None):
     """Pages as values: (k, v), both [n, heads, page_tokens, head_dim] in dtype, for
     int32 page numbers pages [n]."""
-    if not isinstance(cache, Kv8Cache):
-        raise ValueError("cache must be a Kv8Cache")
-    if not isinstance(pages, torch.Tensor) or pages.dim() != 1:
-        raise ValueError("pages must be a tensor of 1 dimension")
-    _is(pages, "pages", pages.shape, torch.int32)
-    shape = (pages.shape[0], cache.heads, cache.page_tokens, cache.head_dim)
-    k = torch.empty(shape, dtype=dtype, device=pages.device)
-    v = torch.empty(shape, dtype=dtype, device=pages.device)
-    _, st = _where(stream, ("cache", cache.k), ("pages", pages))
-    _check(lib().qmm_kv8_read(cache._at, pages.data_ptr(), shape[0], _dt(dtype), k.data_ptr(),
-                              v.data_ptr(), st))
-    return k, v
+    at = _cache(cache)
+    return _serving().kv8_read(at, cache.k, pages, _bf16(dtype), _on(stream))
 
 
 def kv8_attention(cache, q, table, lens, cu, scale=None, out=None, return_lse=False, stream=None):
@@ -784,22 +710,8 @@ def kv8_attention(cache, q, table, lens, cu, scale=None, out=None, return_lse=Fa
     their sequences in the cache (which hold the new tokens already). scale
     defaults to head_dim ** -0.5. Returns out [T, q_heads, head_dim], with
     return_lse (out, lse fp32 [T, q_heads])."""
-    S, W = _kv8_batch(cache, table, lens, cu)
-    ld = _kv8_new(cache, q, "q", None)
-    T, Hq, D = q.shape
-    if out is None:
-        out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
-    _is(out, "out", (T, Hq, D), q.dtype)
-    lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device) if return_lse else None
-    dev, st = _where(stream, ("cache", cache.k), ("q", q), ("table", table), ("lens", lens),
-                     ("cu", cu), ("out", out))
-    L = lib()
-    work, nbytes = _work(L.qmm_kv8_attention_work(cache._at, T, Hq, S, W), dev, st)
-    _check(L.qmm_kv8_attention(cache._at, q.data_ptr(), ld, _dt(q.dtype), T, Hq, table.data_ptr(),
-                               lens.data_ptr(), cu.data_ptr(), S, W,
-                               D ** -0.5 if scale is None else scale, out.data_ptr(),
-                               None if lse is None else lse.data_ptr(), work, nbytes, st))
-    return (out, lse) if return_lse else out
+    at = _cache(cache)
+    return _serving().kv8_attention(at, cache.k, q, table, lens, cu, scale, out, return_lse, _on(stream))
 
 
 def kv8_update(cache, ref, table, lens, parent, new_lens, stream=None):
@@ -807,52 +719,20 @@ def kv8_update(cache, ref, table, lens, parent, new_lens, stream=None):
     parent[s] and gets pages for new_lens[s] tokens. Returns (ref, table,
     shortage), new tensors; shortage int32 [1] counts pages that were wanted
     and not there."""
-    S, W = _kv8_batch(cache, table, lens, None)
-    _is(ref, "ref", (cache.pages,), torch.int32)
-    _is(parent, "parent", (S,), torch.int32)
-    _is(new_lens, "new_lens", (S,), torch.int32)
-    ref_out, table_out = torch.empty_like(ref), torch.empty_like(table)
-    short = torch.empty((1,), dtype=torch.int32, device=ref.device)
-    dev, st = _where(stream, ("cache", cache.k), ("ref", ref), ("table", table), ("lens", lens),
-                     ("parent", parent), ("new_lens", new_lens))
-    L = lib()
-    work, nbytes = _work(L.qmm_kv8_pages_work(cache.pages), dev, st)
-    _check(L.qmm_kv8_update(cache._at, ref.data_ptr(), table.data_ptr(), lens.data_ptr(),
-                            parent.data_ptr(), new_lens.data_ptr(), S, W, ref_out.data_ptr(),
-                            table_out.data_ptr(), short.data_ptr(), work, nbytes, st))
-    return ref_out, table_out, short
+    at = _cache(cache)
+    return _serving().kv8_update(at, cache.k, ref, table, lens, parent, new_lens, _on(stream))
 
 
 def kv8_compact(cache, ref, table, stream=None):
     """Pack the pages in use to the front of the cache (libqmm.h, qmm_kv8_compact).
     Returns (ref, table, remap, used): the new counts and table, each page's new
     number, and int32 [1] the number of pages in use."""
-    if not isinstance(cache, Kv8Cache):
-        raise ValueError("cache must be a Kv8Cache")
-    if not isinstance(table, torch.Tensor) or table.dim() != 2:
-        raise ValueError("table must be a tensor of 2 dimensions")
-    S, W = table.shape
-    _is(table, "table", (S, W), torch.int32)
-    _is(ref, "ref", (cache.pages,), torch.int32)
-    ref_out, table_out, remap = torch.empty_like(ref), torch.empty_like(table), torch.empty_like(ref)
-    used = torch.empty((1,), dtype=torch.int32, device=ref.device)
-    dev, st = _where(stream, ("cache", cache.k), ("ref", ref), ("table", table))
-    L = lib()
-    work, nbytes = _work(L.qmm_kv8_pages_work(cache.pages), dev, st)
-    _check(L.qmm_kv8_compact(cache._at, ref.data_ptr(), table.data_ptr(), S, W, ref_out.data_ptr(),
-                             table_out.data_ptr(), remap.data_ptr(), used.data_ptr(), work, nbytes,
-                             st))
-    return ref_out, table_out, remap, used
+    at = _cache(cache)
+    return _serving().kv8_compact(at, cache.k, ref, table, _on(stream))
 
 
 def kv8_copy(to, dst, source, src, stream=None):
     """Copy pages src [n] of the cache `source` to pages dst [n] of the cache `to`
     (int32 tensors; the dst distinct, none of them also a src of one cache)."""
-    if not isinstance(to, Kv8Cache) or not isinstance(source, Kv8Cache):
-        raise ValueError("to and source must be Kv8Caches")
-    if not isinstance(dst, torch.Tensor) or dst.dim() != 1:
-        raise ValueError("dst must be a tensor of 1 dimension")
-    _is(dst, "dst", dst.shape, torch.int32)
-    _is(src, "src", dst.shape, torch.int32)
-    _, st = _where(stream, ("to", to.k), ("source", source.k), ("dst", dst), ("src", src))
-    _check(lib().qmm_kv8_copy(to._at, dst.data_ptr(), source._at, src.data_ptr(), dst.shape[0], st))
+    a, b = _cache(to, "to"), _cache(source, "source")
+    _serving().kv8_copy(a, to.k, dst, b, source.k, src, _on(stream))

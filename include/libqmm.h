@@ -472,7 +472,7 @@ qmm_status qmm_i8_quantize(const void* x, int64_t ldx, qmm_dtype dt, int64_t row
  * with codes xq [M, K], wq [N, K], fp32 scales sx [M] (tokens), sw [N]
  * (channels) and an optional bias [N] in dt (NULL: none). The integer sum is
  * exact; scales, bias and the one rounding to dt follow in fp32. A GEMV up to
- * 32 rows, an MFMA tile kernel beyond. xq, wq and y 16-byte aligned.
+ * 64 rows, an MFMA tile kernel beyond. xq, wq and y 16-byte aligned.
  */
 int64_t qmm_i8_t_work(int64_t M, int64_t N, int64_t K);
 qmm_status qmm_i8_t(const int8_t* xq, const float* sx, const int8_t* wq, const float* sw,

@@ -59,7 +59,7 @@ def test_null_pointers(L):
         if "c" in args:
             refused(L, fn, Q.QMM_E_NULL, c=None)
             refused(L, fn, Q.QMM_E_NULL, c=cache(v_scales=0))
-    refused(L, "qmm_i8_linear", Q.QMM_E_NULL, work=None)
+    refused(L, "qmm_i8_linear", Q.QMM_E_NULL, work=None, M=400)
     refused(L, "qmm_kv8_update", Q.QMM_E_NULL, work=None)
     refused(L, "qmm_kv8_compact", Q.QMM_E_NULL, work=None)
     refused(L, "qmm_kv8_copy", Q.QMM_E_NULL, source=None)
@@ -128,10 +128,10 @@ def test_alignment(L):
 
 
 def test_scratch_and_aliases(L):
-    refused(L, "qmm_i8_linear", Q.QMM_E_ARG, nb=100)
-    need = L.qmm_i8_linear_work(4, 4, 64)
-    assert need >= 65536 + 4 * 64 + 16
-    refused(L, "qmm_i8_linear", Q.QMM_E_ARG, nb=need - 1)
+    refused(L, "qmm_i8_linear", Q.QMM_E_ARG, nb=100, M=400)
+    need = L.qmm_i8_linear_work(400, 4, 64)
+    assert need >= 65536 + 400 * 64 + 1600
+    refused(L, "qmm_i8_linear", Q.QMM_E_ARG, nb=need - 1, M=400)
     refused(L, "qmm_kv8_update", Q.QMM_E_ARG, nb=L.qmm_kv8_pages_work(8) - 1)
     refused(L, "qmm_kv8_compact", Q.QMM_E_ARG, nb=0)
     refused(L, "qmm_kv8_attention", Q.QMM_E_ARG, W=4096, T=1, S=1, nb=64)

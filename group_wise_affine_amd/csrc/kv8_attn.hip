@@ -94,10 +94,11 @@ __device__ __forceinline__ Share share(float v0, float v1, float l) {
            (uint32_t)from_f32(T{}, s.any ? v1 * back : 0.0f) << 16;
   return s;
 }
-// floats of a part in the scratch buffer: per row the maximum and the sum,
-// then the rows
-template <int D>
-constexpr int kPart = 16 * (D + 2);
+// A part in the scratch buffer: R rows' maxima and sums, then the rows. R is 16
+// for the decode kernel and kPromptRows for the prompt kernel.
+constexpr int kPromptRows = 128;
+template <int D, int R>
+constexpr int kPart = R * (D + 2);
 
 // ------------------------------------------------------------------- decode
 // Up to 16 query rows (tokens x heads of one group) per workgroup, NW
@@ -341,7 +342,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : D == 128 ? 2 : 3) void kv8_
   for (int i = 0; i < VD; i++)
     *reinterpret_cast<float4_t*>(jo + ((wave * 16 + col) * D + i * 16 + g * 4)) = o[i] * vref;
   __syncthreads();
-  float* part = a.ws + (((int64_t)blockIdx.x * gridDim.y + blockIdx.y) * a.splits + split) * kPart<D>;
+  float* part = a.ws + (((int64_t)blockIdx.x * gridDim.y + blockIdx.y) * a.splits + split) * kPart<D, 16>;
   for (int i = tid; i < rows * (D / 2); i += 64 * NW) {
     const int r = i / (D / 2), d = i % (D / 2) * 2;
     float m = -__builtin_inff();
@@ -376,28 +377,31 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : D == 128 ? 2 : 3) void kv8_
 // them takes as long as memory does, and what lies past the sequence's parts
 // is not used. A kernel of its own: its launch costs less than a counter that
 // every workgroup waits for.
-template <class T, int D, int BT>
+template <class T, int D, int R>
 __global__ __launch_bounds__(256) void kv8_join_kernel(AttnArgs a) {
+  constexpr bool kPrompt = R == kPromptRows;
+  constexpr int kFloats = kPart<D, R>;
   constexpr int kSub = 512 / D, kEach = kMaxSplits / kSub;
   __shared__ float fac[kMaxSplits], half[256][2];
   const int tid = threadIdx.x, lane = tid % 64;
   const int sub = tid / (D / 2), d = tid % (D / 2) * 2;
-  const int blocks = (a.G + 15) / 16, columns = a.c.heads * blocks;
+  const int blocks = kPrompt ? 1 : (a.G + 15) / 16, columns = a.c.heads * blocks;
   const int index = blockIdx.x / columns, column = blockIdx.x % columns, r = blockIdx.y;
-  const float* part = a.ws + (int64_t)blockIdx.x * a.splits * kPart<D>;
+  const float* part = a.ws + (int64_t)blockIdx.x * a.splits * kFloats;
   float2 v[kEach], ml[kMaxSplits / 64];
 #pragma unroll
   for (int k = 0; k < kMaxSplits / 64; k++)
     if (k * 64 + lane < a.splits)
-      ml[k] = *reinterpret_cast<const float2*>(part + (k * 64 + lane) * kPart<D> + 2 * r);
+      ml[k] = *reinterpret_cast<const float2*>(part + (k * 64 + lane) * kFloats + 2 * r);
 #pragma unroll
   for (int k = 0; k < kEach; k++)
     if (k * kSub + sub < a.splits)
-      v[k] = *reinterpret_cast<const float2*>(part + (k * kSub + sub) * kPart<D> + 32 + r * D + d);
-  const int head = column / blocks, h0 = column % blocks * 16, G = min(16, a.G - h0);
-  const SeqAt q = locate(a.q, index, a.unit, a.extra, BT);
+      v[k] = *reinterpret_cast<const float2*>(part + (k * kSub + sub) * kFloats + 2 * R + r * D + d);
+  const int head = column / blocks, h0 = column % blocks * 16;
+  const int G = kPrompt ? a.G : min(16, a.G - h0);
+  const SeqAt q = locate(a.q, index, a.unit, a.extra, a.c.bt_log2);
   const int i0 = q.item * a.unit;
-  if (q.item < 0 || i0 >= q.count || (int64_t)q.count * a.G > a.many) return;
+  if (q.item < 0 || i0 >= q.count || ((int64_t)q.count * a.G > a.many) != kPrompt) return;
   const int ntok = min(q.count - i0, a.unit);
   if (r >= ntok * G) return;
   const int most = q.len - q.count + i0 + ntok;
@@ -447,7 +451,43 @@ __global__ __launch_bounds__(256) void kv8_join_kernel(AttnArgs a) {
 }
 
 // ------------------------------------------------------------------ prompts
-// 32 query rows per wavefront, NW wavefronts, tiles of 64 tokens through two
+// The work items of a prompt batch differ in length by as much as the contexts
+// do, and there are only a few of them per CU: the longest come first. Returns
+// the item of rank `rank` (every workgroup finds the ranks by itself: a few
+// hundred comparisons per thread). Batches of more items or sequences than a
+// workgroup has threads go from the last item of the last sequence to the first.
+template <int N>
+__device__ __forceinline__ int longest_first(const AttnArgs& a, int rank, int items) {
+  __shared__ int cu[N + 1], begin[N], len[N], most[N], found;
+  const int tid = threadIdx.x, S = a.q.S;
+  if (items > N || S >= N) return items - 1 - rank;
+  if (tid <= S) cu[tid] = a.q.clip_row(a.q.cu[tid]);
+  if (tid < S) {
+    begin[tid] = (int)((uint32_t)a.q.clip_row(a.q.cu[tid]) / (uint32_t)a.unit) + a.extra * tid;
+    len[tid] = a.q.lens[tid];
+  }
+  if (tid == 0) found = 0;
+  __syncthreads();
+  if (tid < items) {
+    int s = 0;
+    for (int j = 1; j < S; j++)
+      if (begin[j] <= tid) s = j;
+    const int n = cu[s + 1] - cu[s], i0 = (tid - begin[s]) * a.unit;
+    // (a length past the table is cut later: it only costs order here)
+    most[tid] = i0 < 0 || i0 >= n ? -1 : len[s] - n + min(i0 + a.unit, n);
+  }
+  __syncthreads();
+  if (tid < items) {
+    const int mine = most[tid];
+    int before = 0;
+    for (int j = 0; j < items; j++) before += most[j] > mine || (most[j] == mine && j < tid);
+    if (before == rank) found = tid;
+  }
+  __syncthreads();
+  return __builtin_amdgcn_readfirstlane(found);
+}
+
+// 32 query rows per wavefront, four wavefronts, tiles of 64 tokens through two
 // LDS buffers. The codes are turned into f16 once per workgroup on their way
 // into LDS (keys [64][D], rows in the order in which the products want them;
 // values [D][64]); the 16-byte pieces of a row are permuted by an exclusive-or
@@ -460,8 +500,9 @@ __global__ __launch_bounds__(256) void kv8_join_kernel(AttnArgs a) {
 // over groups of 16 tokens, hence scalars. The running maximum is only raised
 // when it grows by more than 2^8: until then weights reach 256, which f16 and
 // the fp32 sums hold as well, and nothing is rescaled.
-template <class T, int D, int NW>
-__global__ __launch_bounds__(64 * NW) void kv8_prompt_kernel(AttnArgs a) {
+template <class T, int D>
+__global__ __launch_bounds__(2 * kPromptRows, D == 256 ? 1 : 2) void kv8_prompt_kernel(AttnArgs a) {
+  constexpr int NW = kPromptRows / 32;
   constexpr int KS = D / 16, VD = D / 32, kThreads = 64 * NW;
   constexpr int kUnits = kTile * D / 16 / kThreads;   // 16 codes per unit
   // f16 results: the weights go in as two f16 terms, since 11 bits of them would
@@ -477,10 +518,9 @@ __global__ __launch_bounds__(64 * NW) void kv8_prompt_kernel(AttnArgs a) {
   const int tid = threadIdx.x, lane = tid % 64;
   const int wave = __builtin_amdgcn_readfirstlane(tid / 64);   // uniform: scalar
   const int col = lane % 32, h = lane / 32;
-  const int head = blockIdx.y;
   const Kv8& c = a.c;
-  // long sequences' last items have most to do: they come first
-  const int index = gridDim.x - 1 - blockIdx.x;
+  const int head = blockIdx.x % c.heads, items = gridDim.x / c.heads, split = blockIdx.y;
+  const int index = longest_first<kThreads>(a, blockIdx.x / c.heads, items);
   const SeqAt seq = locate(a.q, index, a.unit, a.extra, c.bt_log2);
   const int s = seq.s, t0 = seq.first, n = seq.count, len = seq.len, item = seq.item;
   const int i0 = item * a.unit;
@@ -489,6 +529,9 @@ __global__ __launch_bounds__(64 * NW) void kv8_prompt_kernel(AttnArgs a) {
   const int rows = ntok * a.G;
   const int most = len - n + i0 + ntok;
   const int tiles = most > 0 ? (most + kTile - 1) / kTile : 0;
+  const int parts = tiles > 0 ? (tiles + a.per - 1) / a.per : 1;
+  if (split >= parts) return;
+  const int first = split * a.per, last = min(first + a.per, tiles);
 
   // this lane's query row; rows past the last repeat it, and nothing reads them
   const int rr = min(wave * 32 + col, rows - 1);
@@ -643,16 +686,16 @@ __global__ __launch_bounds__(64 * NW) void kv8_prompt_kernel(AttnArgs a) {
       }
     }
   };
-  if (tiles > 0) {
-    look_up(0);
+  if (first < last) {
+    look_up(first);
     fetch();
-    look_up(1);
-    put(0);
+    look_up(first + 1);
+    put(first & 1);
   }
-  for (int tile = 0; tile < tiles; tile++) {
+  for (int tile = first; tile < last; tile++) {
     const int buf = tile & 1;
     __syncthreads();
-    if (tile + 1 < tiles) {
+    if (tile + 1 < last) {
       fetch();
       look_up(tile + 2);
     }
@@ -690,10 +733,24 @@ __global__ __launch_bounds__(64 * NW) void kv8_prompt_kernel(AttnArgs a) {
       else
         weigh.template operator()<true>(sc, f, vs, ve, left, missing, buf);
     }
-    if (tile + 1 < tiles) put(buf ^ 1);
+    if (tile + 1 < last) put(buf ^ 1);
   }
   if (wave * 32 + col >= rows) return;
   l_run += __shfl_xor(l_run, 32);
+  if (parts > 1) {   // kv8_join_kernel adds them up
+    const int64_t unit = (int64_t)index * c.heads + head;
+    float* part = a.ws + (unit * a.splits + split) * kPart<D, kPromptRows>;
+    const float vref = ldexpf(1.0f, v_exp);
+    if (h == 0) *reinterpret_cast<float2*>(part + 2 * (wave * 32 + col)) = make_float2(m_run, l_run);
+    float* mine = part + 2 * kPromptRows + (wave * 32 + col) * D + h * 4;
+#pragma unroll
+    for (int i = 0; i < VD; i++)
+#pragma unroll
+      for (int q = 0; q < 4; q++)
+        *reinterpret_cast<float4_t*>(mine + i * 32 + q * 8) =
+            float4_t{o[i][q * 4], o[i][q * 4 + 1], o[i][q * 4 + 2], o[i][q * 4 + 3]} * vref;
+    return;
+  }
   const bool any = l_run > 0.0f || l_run != l_run;
   const float back = any ? ldexpf(1.0f, v_exp) / l_run : 0.0f;
 #pragma unroll
@@ -717,24 +774,23 @@ struct Plan {
   int unit, extra, splits, per, nw, many, most_rows;
   int64_t items, columns;   // grid: items x heads and blocks of a group's heads
   bool prompts;
-  int p_unit;
+  int p_unit, p_splits, p_per;
   int64_t p_items;
 };
 
 Plan plan(const Kv8& c, int64_t T, int64_t Hq, int64_t S, int64_t W) {
   Plan p{};
   const int64_t G = Hq / c.heads;
-  const int prompt_rows = c.dim == 128 ? 256 : 128;
   // the packed batch says how many new tokens a sequence can have at most
   const int64_t longest = T;
-  p.prompts = longest * G > kFewRows && T > S && G <= prompt_rows;
+  p.prompts = longest * G > kFewRows && T > S && G <= kPromptRows;
   p.many = p.prompts ? kFewRows : INT32_MAX;
   p.unit = T > S && G <= 8 ? (int)(16 / G) : 1;
   p.extra = p.unit > 1 ? 1 : 0;
   p.items = T / p.unit + p.extra * S;
   p.columns = c.heads * ((G + 15) / 16);
   p.most_rows = (int)(p.unit * (G < 16 ? G : 16));
-  p.p_unit = (int)(prompt_rows / (G < prompt_rows ? G : prompt_rows));
+  p.p_unit = (int)(kPromptRows / (G < kPromptRows ? G : kPromptRows));
   p.p_items = T / p.p_unit + S;
   const int64_t units = (T < p.items ? T : p.items) * p.columns;
   const int64_t tiles = ((W << c.bt_log2) + kTile - 1) / kTile;
@@ -760,14 +816,33 @@ Plan plan(const Kv8& c, int64_t T, int64_t Hq, int64_t S, int64_t W) {
   p.per = (int)per;
   const int64_t sp = (tiles + per - 1) / per;
   p.splits = (int)sp;
+  // Prompts: where the items do not fill the chip (two workgroups per CU), the
+  // tiles of each are cut, into parts of at least 16 tiles: a part costs a pass
+  // over its rows in fp32, there and back. (A chunk of 600 tokens behind 29400,
+  // 8 heads of 4: 535 us cut, 949 us whole.)
+  const int64_t work = p.p_items * c.heads;
+  int64_t ps = 512 / (work < 1 ? 1 : work);
+  ps = ps < tiles / 16 ? ps : tiles / 16;
+  ps = ps < 1 ? 1 : ps > 16 ? 16 : ps;
+  p.p_per = (int)((tiles + ps - 1) / ps);
+  p.p_splits = (int)((tiles + p.p_per - 1) / p.p_per);
   return p;
+}
+
+// bytes of the decode kernel's parts, then of the prompt kernel's
+int64_t decode_bytes(const Plan& p, const Kv8& c) {
+  return p.splits > 1 ? p.items * p.columns * p.splits * 16 * (c.dim + 2) * 4 : 0;
+}
+int64_t prompt_bytes(const Plan& p, const Kv8& c) {
+  return p.prompts && p.p_splits > 1
+             ? p.p_items * c.heads * p.p_splits * kPromptRows * (c.dim + 2) * 4 : 0;
 }
 
 }  // namespace
 
 int64_t kv8_attention_work(const Kv8& c, int64_t T, int64_t Hq, int64_t S, int64_t W) {
   const Plan p = plan(c, T, Hq, S, W);
-  return p.splits > 1 ? p.items * p.columns * p.splits * 16 * (c.dim + 2) * 4 : 0;
+  return decode_bytes(p, c) + prompt_bytes(p, c);
 }
 
 hipError_t launch_kv8_attention(const Kv8& c, int dt, const void* q, int64_t ldq, int64_t T,
@@ -788,7 +863,7 @@ hipError_t launch_kv8_attention(const Kv8& c, int dt, const void* q, int64_t ldq
       if (p.nw == 4) waves.template operator()<4>();
       else waves.template operator()<D == 256 ? 4 : 8>();
       if (p.splits > 1)
-        hipLaunchKernelGGL((kv8_join_kernel<T_, D, BT>),
+        hipLaunchKernelGGL((kv8_join_kernel<T_, D, 16>),
                            dim3((unsigned)(p.items * p.columns), (unsigned)p.most_rows),
                            dim3(256), 0, st, a);
     };
@@ -799,9 +874,15 @@ hipError_t launch_kv8_attention(const Kv8& c, int dt, const void* q, int64_t ldq
     AttnArgs b = a;
     b.unit = p.p_unit;
     b.extra = 1;
-    hipLaunchKernelGGL((kv8_prompt_kernel<T_, D, D == 256 ? 4 : D == 128 ? 8 : 4>),
-                       dim3((unsigned)p.p_items, (unsigned)c.heads), dim3(D == 128 ? 512 : 256), 0,
+    b.splits = p.p_splits;
+    b.per = p.p_per;
+    b.ws = ws + decode_bytes(p, c) / 4;
+    const unsigned units = (unsigned)(p.p_items * c.heads);
+    hipLaunchKernelGGL((kv8_prompt_kernel<T_, D>), dim3(units, (unsigned)p.p_splits), dim3(256), 0,
                        st, b);
+    if (p.p_splits > 1)
+      hipLaunchKernelGGL((kv8_join_kernel<T_, D, kPromptRows>), dim3(units, kPromptRows), dim3(256),
+                         0, st, b);
   };
   auto by_dim = [&]<class T_>() {
     if (c.dim == 64) go.template operator()<T_, 64>();

@@ -194,6 +194,30 @@ def test_attention_long_context_is_split(B):
         assert torch.equal(out, again) and torch.equal(lse, l2)
 
 
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("lens,new", [([2500, 100, 0, 1700], [1, 1, 1, 1]), ([3000], [40]), ([2300, 5, 2100], [33, 1, 2]),
+                                      ([2100] + [9] * 70, [60] + [1] * 70)])
+def test_attention_parts_are_joined(lens, new, dt):
+    """Ragged batches whose longer sequences are cut into parts, for the kernels
+    of both few and many query rows; more sequences than one look finds."""
+    B, D, H, G = 32, 128, 1, 4
+    dev, ref = make(230, H, B, D, sum(lens))
+    tab = tables(lens, B, 230, 2)
+    cu = [0] + [int(c) for c in np.cumsum(new)]
+    q = fresh(cu[-1], H * G, D, dt, 3)
+    out, lse = Q.kv8_attention(dev, q.cuda(), i32(tab), i32(lens), i32(cu), return_lse=True)
+    check_attention(out, lse, ref, q, tab, lens, cu, D ** -0.5, dt, f"parts {lens[:4]} {dt}")
+
+
+def test_attention_negative_scale():
+    dev, ref = make(30, 1, 16, 64, 40)
+    lens, new = [130, 60], [30, 1]
+    tab, cu = tables(lens, 16, 30, 41), [0, 30, 31]
+    q = fresh(31, 4, 64, "bf16", 42)
+    out, lse = Q.kv8_attention(dev, q.cuda(), i32(tab), i32(lens), i32(cu), return_lse=True, scale=-0.2)
+    check_attention(out, lse, ref, q, tab, lens, cu, -0.2, "bf16", "negative scale")
+
+
 @pytest.mark.parametrize("new", [1, 40])
 def test_attention_masked_places_may_hold_anything(new):
     """Places behind a sequence's end, pages that later rows alone see and

@@ -10,18 +10,22 @@ namespace {
 // scale is fl32(amax of its new values / 127), and not below the old scale
 // when the page holds earlier tokens; the earlier codes are then brought to
 // the new scale, rint(fl32(fl32(c * old) / new)). Slots behind the last token
-// become zero. Bound by memory: the new values are read once (the second look
-// at them, for the codes, hits the caches), the codes written once.
-template <class T>
+// become zero. Bound by memory: new values are read once, codes written once.
+//
+// A thread's unit is 4 slots by 8 columns of the keys or of the values: four
+// 16-byte loads, held in registers between the maximum and the codes; the key
+// codes go out as 8 bytes per slot, the value codes, transposed by the packing,
+// as a word of four slots per column. The lanes of key units run along the
+// columns, those of value units along the slots, so that both write runs.
+template <class T, int U>   // U units per thread
 __global__ __launch_bounds__(256) void kv8_append_kernel(Kv8 c, Kv8Seqs q,
                                                          const uint16_t* __restrict__ kx,
                                                          int64_t ldk,
                                                          const uint16_t* __restrict__ vx,
                                                          int64_t ldv) {
-  extern __shared__ __attribute__((aligned(16))) uint8_t vt[];   // new value codes, [D][B + 4]
   __shared__ uint32_t top_k[4], top_v[4];
   const int tid = threadIdx.x, head = blockIdx.y;
-  const int B = 1 << c.bt_log2, D = c.dim, D8 = D / 8;
+  const int B = 1 << c.bt_log2, D = c.dim;
   const SeqAt at_seq = locate(q, blockIdx.x, B, 2, c.bt_log2);
   const int s = at_seq.s, t0 = at_seq.first, n = at_seq.count, len = at_seq.len, item = at_seq.item;
   // a sequence whose tokens cannot be placed (fewer places than tokens) gets
@@ -33,28 +37,54 @@ __global__ __launch_bounds__(256) void kv8_append_kernel(Kv8 c, Kv8Seqs q,
   if (page < 0 || page >= c.pages) return;
   const int o0 = begin > pi * B ? begin - pi * B : 0;                     // first new slot
   const int o1 = len - pi * B < B ? len - pi * B : B;                     // end of the tokens
-  const int64_t row0 = t0 + n - len + pi * B;                             // row of slot 0
-  const uint16_t* kr = kx + (int64_t)head * D;
-  const uint16_t* vr = vx + (int64_t)head * D;
-  const int units = (o1 - o0) * D8;
+  const int64_t row0 = (int64_t)t0 + n - len + (int64_t)pi * B;           // row of slot 0
+  const int64_t at = (int64_t)page * c.heads + head;
+  const float old_k = c.ks[at], old_v = c.vs[at];
+  const int half = (B / 4) * (D / 8);   // key units, then as many value units
 
+  struct Unit {
+    bool value, live;
+    int slot, d;   // first of 4 slots, first of 8 columns
+  };
+  auto unit = [&](int i) QMM_INLINE {
+    const int u = i * 256 + tid;
+    Unit x;
+    x.value = u >= half;
+    x.live = u < 2 * half;
+    if (x.value) {
+      x.slot = (u - half) % (B / 4) * 4;
+      x.d = (u - half) / (B / 4) * 8;
+    } else {
+      x.slot = u / (D / 8) * 4;
+      x.d = u % (D / 8) * 8;
+    }
+    return x;
+  };
+  uint4 w[U][4];
   uint32_t mk = 0, mv = 0;
-  for (int u = tid; u < units; u += 256) {
-    const int64_t row = row0 + o0 + u / D8;
-    const int d = (u % D8) * 8;
-    const uint4 a = *reinterpret_cast<const uint4*>(kr + row * ldk + d);
-    const uint4 b = *reinterpret_cast<const uint4*>(vr + row * ldv + d);
-    mk = amax_pair(amax_pair(amax_pair(amax_pair(mk, a.x), a.y), a.z), a.w);
-    mv = amax_pair(amax_pair(amax_pair(amax_pair(mv, b.x), b.y), b.z), b.w);
+#pragma unroll
+  for (int i = 0; i < U; i++) {
+    const Unit x = unit(i);
+    const uint16_t* p = (x.value ? vx : kx) + (int64_t)head * D + x.d;
+    const int64_t ld = x.value ? ldv : ldk;
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+      const bool in = x.live && x.slot + j >= o0 && x.slot + j < o1;
+      w[i][j] = in ? *reinterpret_cast<const uint4*>(p + (row0 + x.slot + j) * ld)
+                   : make_uint4(0, 0, 0, 0);
+      m = amax_pair(amax_pair(amax_pair(amax_pair(m, w[i][j].x), w[i][j].y), w[i][j].z), w[i][j].w);
+    }
+    m = amax_halves(m);
+    mk = !x.value && m > mk ? m : mk;
+    mv = x.value && m > mv ? m : mv;
   }
-  mk = wave_umax(amax_halves(mk));
-  mv = wave_umax(amax_halves(mv));
+  mk = wave_umax(mk);
+  mv = wave_umax(mv);
   if (tid % 64 == 0) {
     top_k[tid / 64] = mk;
     top_v[tid / 64] = mv;
   }
-  const int64_t at = (int64_t)page * c.heads + head;
-  const float old_k = c.ks[at], old_v = c.vs[at];
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < 4; i++) {
@@ -70,63 +100,62 @@ __global__ __launch_bounds__(256) void kv8_append_kernel(Kv8 c, Kv8Seqs q,
     c.ks[at] = dk.s;
     c.vs[at] = dv.s;
   }
-  int8_t* kc = c.k + c.block(page, head);
-  int8_t* vc = c.v + c.block(page, head);
   // four codes of the earlier tokens at the new scale
-  auto again = [&](uint32_t w, float old, const Divisor& d) QMM_INLINE {
+  auto again = [&](uint32_t word, float old, const Divisor& d) QMM_INLINE {
     float f[4], r[4];
 #pragma unroll
-    for (int i = 0; i < 4; i++) f[i] = code_f32(w, i) * old;
+    for (int i = 0; i < 4; i++) f[i] = code_f32(word, i) * old;
     divide_round<4>(f, d, r);
     return pack_codes(r[0], r[1], r[2], r[3]);
   };
-  // keys: 8 codes of one token at a time
-  const bool same_k = old_k == dk.s, same_v = old_v == dv.s;
-  for (int u = tid; u < B * D8; u += 256) {
-    const int slot = u / D8, d = (u % D8) * 8;
-    uint2* p = reinterpret_cast<uint2*>(kc + slot * D + d);
-    if (slot < o0) {
-      if (same_k) continue;
-      const uint2 w = *p;
-      *p = make_uint2(again(w.x, old_k, dk), again(w.y, old_k, dk));
-    } else if (slot < o1) {
-      float f[8], r[8];
-      unpack8(T{}, *reinterpret_cast<const uint4*>(kr + (row0 + slot) * ldk + d), f);
-      divide_round<8>(f, dk, r);
-      *p = make_uint2(pack_codes(r[0], r[1], r[2], r[3]), pack_codes(r[4], r[5], r[6], r[7]));
+#pragma unroll
+  for (int i = 0; i < U; i++) {
+    const Unit x = unit(i);
+    if (!x.live) continue;
+    const float old = x.value ? old_v : old_k;
+    const Divisor d = x.value ? dv : dk;
+    const bool same = old == d.s;
+    if (same && x.slot + 4 <= o0) continue;   // earlier tokens, as they were
+    float r[4][8];
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+#pragma unroll
+      for (int e = 0; e < 8; e++) r[j][e] = 0.0f;
+      if (x.slot + j >= o0 && x.slot + j < o1) {
+        float f[8];
+        unpack8(T{}, w[i][j], f);
+        divide_round<8>(f, d, r[j]);
+      }
+    }
+    if (!x.value) {
+      int8_t* p = c.k + c.block(page, head) + x.slot * D + x.d;
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        uint2* to = reinterpret_cast<uint2*>(p + j * D);
+        uint2 code = make_uint2(pack_codes(r[j][0], r[j][1], r[j][2], r[j][3]),
+                                pack_codes(r[j][4], r[j][5], r[j][6], r[j][7]));
+        if (x.slot + j < o0) {
+          if (same) continue;
+          code = *to;
+          code = make_uint2(again(code.x, old, d), again(code.y, old, d));
+        }
+        *to = code;
+      }
     } else {
-      *p = make_uint2(0, 0);
-    }
-  }
-  // values: codes to LDS by column, then whole words of four tokens
-  const int ldt = B + 4;
-  for (int u = tid; u < units; u += 256) {
-    const int slot = o0 + u / D8, d = (u % D8) * 8;
-    float f[8], r[8];
-    unpack8(T{}, *reinterpret_cast<const uint4*>(vr + (row0 + slot) * ldv + d), f);
-    divide_round<8>(f, dv, r);
+      int8_t* p = c.v + c.block(page, head) + x.d * B + x.slot;
+      const int kept = o0 - x.slot;   // slots of the word with earlier tokens
+      const uint32_t mask = kept <= 0 ? 0u : kept >= 4 ? ~0u : (1u << (8 * kept)) - 1u;
 #pragma unroll
-    for (int i = 0; i < 8; i++) vt[(d + i) * ldt + slot] = (uint8_t)(int)r[i];
-  }
-  __syncthreads();
-  const int B4 = B / 4;
-  for (int u = tid; u < D * B4; u += 256) {
-    const int d = u / B4, slot = (u % B4) * 4;
-    if (same_v && slot + 4 <= o0) continue;
-    uint32_t* p = reinterpret_cast<uint32_t*>(vc + d * B + slot);
-    uint32_t was = 0;
-    if (slot < o0) {
-      was = *p;
-      if (!same_v) was = again(was, old_v, dv);
+      for (int e = 0; e < 8; e++) {
+        uint32_t* to = reinterpret_cast<uint32_t*>(p + e * B);
+        uint32_t code = pack_codes(r[0][e], r[1][e], r[2][e], r[3][e]);
+        if (mask) {
+          const uint32_t was = same ? *to : again(*to, old, d);
+          code = (code & ~mask) | (was & mask);
+        }
+        *to = code;
+      }
     }
-    const uint32_t now = *reinterpret_cast<const uint32_t*>(vt + d * ldt + slot);
-    uint32_t w = 0;
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-      const uint32_t m = 0xffu << (8 * i);
-      w |= slot + i < o0 ? was & m : slot + i < o1 ? now & m : 0u;
-    }
-    *p = w;
   }
 }
 
@@ -191,13 +220,19 @@ hipError_t launch_kv8_append(const Kv8& c, int dt, const void* k, int64_t ldk, c
                              int64_t ldv, int64_t T, const int32_t* table, const int32_t* lens,
                              const int32_t* cu, int64_t S, int64_t W, hipStream_t st) {
   const dim3 grid((unsigned)((T >> c.bt_log2) + 2 * S), (unsigned)c.heads);
-  const size_t lds = (size_t)c.dim * ((1 << c.bt_log2) + 4);
   const Kv8Seqs q = seqs(table, lens, cu, S, W, T);
   const uint16_t *kx = static_cast<const uint16_t*>(k), *vx = static_cast<const uint16_t*>(v);
-  if (dt == 0)
-    hipLaunchKernelGGL(kv8_append_kernel<F16>, grid, dim3(256), lds, st, c, q, kx, ldk, vx, ldv);
-  else
-    hipLaunchKernelGGL(kv8_append_kernel<BF16>, grid, dim3(256), lds, st, c, q, kx, ldk, vx, ldv);
+  const int units = (2 * (c.dim << c.bt_log2) / 32 + 255) / 256;   // per thread: 1, 2 or 4
+  auto go = [&]<class T_>() {
+    auto each = [&]<int U>() {
+      hipLaunchKernelGGL((kv8_append_kernel<T_, U>), grid, dim3(256), 0, st, c, q, kx, ldk, vx, ldv);
+    };
+    if (units == 1) each.template operator()<1>();
+    else if (units == 2) each.template operator()<2>();
+    else each.template operator()<4>();
+  };
+  if (dt == 0) go.template operator()<F16>();
+  else go.template operator()<BF16>();
   return hipGetLastError();
 }
 

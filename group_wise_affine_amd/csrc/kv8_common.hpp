@@ -36,8 +36,8 @@ struct Kv8Seqs {
 // unit + extra of them. locate() finds the sequence that owns item i (the last
 // one whose items start at or before i) and what a workgroup needs to know
 // of it. It is the first link of a chain of dependent loads (sequence, pages,
-// codes), so the lanes look at 63 boundaries at once: one round trip up to 63
-// sequences, two up to 4000.
+// codes), so the lanes look at 64 boundaries at once: one round trip up to 64
+// sequences, two up to 4096.
 struct SeqAt {
   int s, first, count, len;   // new tokens are rows first .. first + count
   int item;                   // index of the work item in the sequence
@@ -48,9 +48,9 @@ __device__ __forceinline__ SeqAt locate(const Kv8Seqs& q, int i, int unit, int e
     return (int)((uint32_t)q.clip_row(c) / (uint32_t)unit) + extra * j <= i;
   };
   int lo = 0, n = q.S;   // the sequence is one of lo .. lo + n
-  while (n > 63) {
-    const int step = (n + 62) / 63, j = lo + lane * step;
-    const bool at = lane < 63 && j < lo + n && starts(q.cu[j < q.S ? j : q.S], j);
+  while (n > 64) {
+    const int step = (n + 63) / 64, j = lo + lane * step;
+    const bool at = j < lo + n && starts(q.cu[min(j, q.S)], j);
     const int c = max(__builtin_popcountll(__ballot(at)), 1) - 1;
     n = min(step, n - c * step);
     lo += c * step;
@@ -58,14 +58,16 @@ __device__ __forceinline__ SeqAt locate(const Kv8Seqs& q, int i, int unit, int e
   const int j = min(lo + lane, q.S);
   const int c = q.cu[j], l = q.lens[min(j, q.S - 1)];
   const int k = max(__builtin_popcountll(__ballot(lane < n && starts(c, j))), 1) - 1;
-  // (the same in every lane: scalar registers)
+  const int next = __shfl(c, (k + 1) & 63), past = q.cu[min(lo + 64, q.S)];
+  const int first = q.clip_row(__shfl(c, k)), len = max(__shfl(l, k), 0);
+  const int64_t most = (int64_t)q.W << bt_log2;
+  // (the same in every lane, which the compiler cannot see: made scalar, or
+  // every loop over the sequence would be one over lanes)
   SeqAt r;
   r.s = __builtin_amdgcn_readfirstlane(lo + k);
-  r.first = q.clip_row(__builtin_amdgcn_readlane(c, k));
-  r.count = max(q.clip_row(__builtin_amdgcn_readlane(c, k + 1)) - r.first, 0);
-  const int64_t most = (int64_t)q.W << bt_log2;
-  const int len = max(__builtin_amdgcn_readlane(l, k), 0);
-  r.len = len > most ? (int)most : len;
+  r.first = __builtin_amdgcn_readfirstlane(first);
+  r.count = __builtin_amdgcn_readfirstlane(max(q.clip_row(k < 63 ? next : past) - first, 0));
+  r.len = __builtin_amdgcn_readfirstlane(len > most ? (int)most : len);
   r.item = i - ((int)((uint32_t)r.first / (uint32_t)unit) + extra * r.s);
   return r;
 }

@@ -246,6 +246,7 @@ qmm_status qmm_kv8_attention(const qmm_kv8_cache* cache, const void* q, int64_t 
   if (q_heads < c.heads || q_heads % c.heads != 0 || q_heads > 65535)
     return fail(QMM_E_SHAPE, "%s: q_heads (%lld) must be a multiple of the cache's heads (%d)", tag,
                 (long long)q_heads, c.heads);
+  if (T * q_heads > kI32) return fail(QMM_E_SHAPE, "%s: problem too large", tag);
   if (qmm_status s = check_rows(tag, "q", q, ldq, q_heads * c.dim)) return s;
   if (!aligned4({table, lens, cu, lse}) || !aligned(out, 16))
     return fail(QMM_E_ALIGN, "%s: out must be 16-byte aligned, table, lens, cu and lse 4-byte", tag);

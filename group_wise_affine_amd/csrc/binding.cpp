@@ -1,6 +1,6 @@
 // Native marshalling of the 8-bit serving calls for Python: the checks that
 // the C ABI cannot make (it sees pointers, not tensors), the outputs, the
-// scratch buffer of the calling thread and stream, and the call. The calls
+// scratch buffer of the stream, and the call. The calls
 // take a few microseconds on the GPU; in Python this part alone took longer
 // (13.5 us for a product that takes 9, 20 us for append and read).
 //
@@ -106,15 +106,18 @@ Place place(PyObject* stream, std::initializer_list<std::pair<const Tensor*, con
   return p;
 }
 
-// Scratch of the calling thread on one stream, kept and reused as a program's
-// workspace is. A graph under capture gets its own, cleared in the graph.
+// Scratch for calls on one stream, kept and reused as a program's workspace
+// is. (The interpreter's lock is held from here until a call's launches are
+// queued, so that calls of two threads on one stream do not mix.) A graph
+// under capture gets its own, cleared in the graph.
 struct Scratch {
   void* p = nullptr;
   int64_t bytes = 0;
 };
 Scratch scratch(int64_t need, const Place& at) {
   if (need <= 0) return {};
-  thread_local std::map<std::pair<int, hipStream_t>, Tensor> held;
+  // never destroyed: the allocator may be gone when the process ends
+  static auto& held = *new std::map<std::pair<int, hipStream_t>, Tensor>;
   hipStreamCaptureStatus cs = hipStreamCaptureStatusNone;
   const bool capturing = hipStreamIsCapturing(at.st, &cs) == hipSuccess && cs != hipStreamCaptureStatusNone;
   Tensor* t = nullptr;

@@ -327,18 +327,20 @@ __global__ __launch_bounds__(64 * WM * WN, BM * BN == 65536 || NS > 2 ? 1 : 2) v
   // The eight XCDs take workgroups in turn: give each a run of consecutive
   // tiles, walked in bands of 8 row tiles, so that the tiles an XCD works on
   // together share rows of x and W in its L2.
-  int tile = blockIdx.x;
+  const int tiles = tiles_m * tiles_n;
+  int tile = blockIdx.x;   // of all splits
   {
-    const int tiles = tiles_m * tiles_n, per = tiles / 8, rem = tiles % 8;
+    const int per = tiles * a.ks / 8, rem = tiles * a.ks % 8;
     const int xcd = tile % 8, i = tile / 8;
     tile = xcd * per + (xcd < rem ? xcd : rem) + i;
   }
+  const int split = tile / tiles;
+  tile %= tiles;
   constexpr int kBand = 8;
   const int band = tile / (kBand * tiles_n), first = band * kBand;
   const int high = tiles_m - first < kBand ? tiles_m - first : kBand;
   const int in = tile - first * tiles_n;
   const int64_t m0 = (int64_t)(first + in % high) * BM, n0 = (int64_t)(in / high) * BN;
-  const int split = blockIdx.y;
   const int xrows = (int)(a.M - m0 < BM ? a.M - m0 : BM);
   const int wrows = (int)(a.N - n0 < BN ? a.N - n0 : BN);
   const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.xq + m0 * a.K, (uint32_t)xrows * (uint32_t)a.K);
@@ -412,7 +414,7 @@ __global__ __launch_bounds__(64 * WM * WN, BM * BN == 65536 || NS > 2 ? 1 : 2) v
     // accesses are coherent across the XCDs' L2 caches; the stores have
     // completed before the counter is touched.
     __shared__ unsigned last;
-    const int64_t t = blockIdx.x;
+    const int64_t t = tile;
     int* mine = a.ws + (t * a.ks + split) * (BM * BN);
 #pragma unroll
     for (int i = 0; i < TN; i++)
@@ -593,7 +595,7 @@ hipError_t launch_i8_t(int dt, const int8_t* xq, const float* sx, const int8_t* 
       return;
     }
     I8Args a{xq, sx, wq, sw, b, yo, (int)M, (int)N, (int)K, (int)p.ks, (int)p.steps, ws, cnt};
-    const dim3 grid((unsigned)p.tiles, (unsigned)p.ks);
+    const dim3 grid((unsigned)(p.tiles * p.ks));
     if (p.bm == 256)
       hipLaunchKernelGGL((i8_tile_kernel<T, 256, 256, 2, 2, 2>), grid, dim3(256), 0, st, a);
     else if (p.tiles * p.ks <= 256)   // one workgroup per CU: the LDS is its own

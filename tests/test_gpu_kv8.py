@@ -209,6 +209,19 @@ def test_attention_parts_are_joined(lens, new, dt):
     check_attention(out, lse, ref, q, tab, lens, cu, D ** -0.5, dt, f"parts {lens[:4]} {dt}")
 
 
+@pytest.mark.parametrize("new", [5, 40])
+def test_attention_more_new_tokens_than_tokens(new):
+    """Lengths that do not hold the new tokens: the rows without a position see
+    nothing, the others what is there."""
+    dev, ref = make(12, 1, 16, 64, 43)
+    lens, news = [3, 20], [new, 1]
+    tab, cu = tables(lens, 16, 12, 44), [0, new, new + 1]
+    q = fresh(new + 1, 4, 64, "f16", 45)
+    out, lse = Q.kv8_attention(dev, q.cuda(), i32(tab), i32(lens), i32(cu), return_lse=True)
+    check_attention(out, lse, ref, q, tab, lens, cu, 64 ** -0.5, "f16", f"{news}")
+    assert int(out[: new - 3].abs().max()) == 0 and bool(torch.isneginf(lse[: new - 3]).all())
+
+
 def test_attention_negative_scale():
     dev, ref = make(30, 1, 16, 64, 40)
     lens, new = [130, 60], [30, 1]

@@ -106,6 +106,7 @@ def test_batches_and_strides(L):
     refused(L, "qmm_kv8_append", Q.QMM_E_SHAPE, ldk=255)
     refused(L, "qmm_kv8_append", Q.QMM_E_SHAPE, ldv=260)
     refused(L, "qmm_kv8_attention", Q.QMM_E_SHAPE, ldq=504)
+    refused(L, "qmm_kv8_attention", Q.QMM_E_SHAPE, T=1 << 24, Hq=512, ldq=512 * 128)
     for Hq in (1, 3, 0):
         refused(L, "qmm_kv8_attention", Q.QMM_E_SHAPE, Hq=Hq)
     refused(L, "qmm_kv8_read", Q.QMM_E_SHAPE, n=0)

@@ -847,7 +847,9 @@ Plan plan(const Kv8& c, int64_t T, int64_t Hq, int64_t S, int64_t W) {
   const int64_t tiles = ((W << c.bt_log2) + kTile - 1) / kTile;
   // Every workgroup takes the same number of tiles, so that ragged sequences
   // load the chip evenly: as many as make 2048 workgroups of sequences that
-  // fill their table rows, and no more than kMaxSplits parts of a sequence.
+  // fill their table rows (1024 for D = 256, whose registers leave room for half
+  // as many wavefronts: 121 against 140 us for 48 contexts to 4096), and no more
+  // than kMaxSplits parts of a sequence.
   // Contexts of up to 24 tiles are not cut: eight wavefronts walk them in
   // three steps, which costs less than the second launch that joins parts.
   // (48 contexts to 8192 tokens, 8 heads: 111 us with parts of 24 tiles and 4
@@ -855,7 +857,8 @@ Plan plan(const Kv8& c, int64_t T, int64_t Hq, int64_t S, int64_t W) {
   // 131071 tokens, 2 heads: 23.8 us with 128 parts, 26.7 with 64, 37 with 1
   // wavefront.)
   const int64_t cut = (tiles + kMaxSplits - 1) / kMaxSplits;
-  int64_t per = (units * tiles + 2047) / 2048;
+  const int64_t wanted = c.dim == 256 ? 1024 : 2048;
+  int64_t per = (units * tiles + wanted - 1) / wanted;
   per = per > cut ? per : cut;
   p.nw = 4;
   if (tiles <= 24) {

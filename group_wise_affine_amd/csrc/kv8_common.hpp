@@ -73,7 +73,7 @@ __device__ __forceinline__ SeqAt locate(const Kv8Seqs& q, int i, int unit, int e
 }
 
 // Copies part `part` of `parts` of a page (codes, and with part 0 the scales)
-// with 256 threads, four 16-byte pieces in flight per thread.
+// with 256 threads, eight 16-byte pieces in flight per thread.
 constexpr int kCopyBytes = 16384;   // of keys and of values each, per part
 __host__ __device__ inline int copy_parts(const Kv8& c) {
   const int64_t bytes = c.block(1, 0);
@@ -81,23 +81,30 @@ __host__ __device__ inline int copy_parts(const Kv8& c) {
 }
 __device__ __forceinline__ void copy_page(const Kv8& to, int64_t d, const Kv8& from, int64_t s,
                                           int part, int parts) {
-  const int64_t page = to.block(1, 0) / 16;   // pieces of a page
-  const int64_t per = (page + parts - 1) / parts, begin = part * per;
-  const int64_t end = begin + per < page ? begin + per : page;
-  const uint4* ks = reinterpret_cast<const uint4*>(from.k) + s * page;
-  const uint4* vs = reinterpret_cast<const uint4*>(from.v) + s * page;
-  uint4* kd = reinterpret_cast<uint4*>(to.k) + d * page;
-  uint4* vd = reinterpret_cast<uint4*>(to.v) + d * page;
-  for (int64_t i = begin + threadIdx.x; i < end; i += 512) {
-    const bool two = i + 256 < end;
-    const int64_t j = two ? i + 256 : i;
-    const uint4 a = ks[i], b = vs[i], e = ks[j], f = vs[j];
+  const int page = (int)(to.block(1, 0) / 16);   // pieces of a page
+  const int per = (page + parts - 1) / parts, begin = part * per;
+  const int end = begin + per < page ? begin + per : page;
+  const u32x4_t* ks = reinterpret_cast<const u32x4_t*>(from.k) + s * page;
+  const u32x4_t* vs = reinterpret_cast<const u32x4_t*>(from.v) + s * page;
+  u32x4_t* kd = reinterpret_cast<u32x4_t*>(to.k) + d * page;
+  u32x4_t* vd = reinterpret_cast<u32x4_t*>(to.v) + d * page;
+  int i = begin + threadIdx.x;
+  for (; i + 768 < end; i += 1024) {
+    const u32x4_t a0 = ks[i], a1 = ks[i + 256], a2 = ks[i + 512], a3 = ks[i + 768];
+    const u32x4_t b0 = vs[i], b1 = vs[i + 256], b2 = vs[i + 512], b3 = vs[i + 768];
+    kd[i] = a0;
+    kd[i + 256] = a1;
+    kd[i + 512] = a2;
+    kd[i + 768] = a3;
+    vd[i] = b0;
+    vd[i + 256] = b1;
+    vd[i + 512] = b2;
+    vd[i + 768] = b3;
+  }
+  for (; i < end; i += 256) {
+    const u32x4_t a = ks[i], b = vs[i];
     kd[i] = a;
     vd[i] = b;
-    if (two) {
-      kd[j] = e;
-      vd[j] = f;
-    }
   }
   if (part == 0)
     for (int h = threadIdx.x; h < to.heads; h += 256) {

@@ -116,26 +116,38 @@ __device__ __forceinline__ Last last_page(const Update& u, int s, int64_t keep) 
   l.copied = l.page >= 0 && !(p == s && u.ref[l.page] == 1 && u.shared[l.page] == 0);
   return l;
 }
-__device__ __forceinline__ int needed(const Update& u, int s) {
-  const int64_t keep = u.keep(s);
-  const int grow = u.pages(u.clip(u.new_lens[s])) - u.pages(keep);
-  return (grow > 0 ? grow : 0) + (last_page(u, s, keep).copied ? 1 : 0);
-}
-
 // One slot per blockIdx.x: its fresh pages are the free pages of rank r0 ..
 // r0 + need, r0 the pages that the slots before it take. The workgroups of
-// blockIdx.y > 0 find the same numbers and help to copy the last page.
+// blockIdx.y > 0 find the same numbers and help to copy the last page. What
+// bounds it is the chain of dependent loads, so a thread looks at each slot up
+// to this one, this one among them, and the first counts of free pages are
+// asked for before that.
 __global__ __launch_bounds__(256) void update_assign_kernel(Update u, Kv8 c) {
   const int s = blockIdx.x, tid = threadIdx.x;
   const bool writer = blockIdx.y == 0;
-  const int64_t keep = u.keep(s);
-  const Last last = last_page(u, s, keep);
-  if (!writer && !last.copied) return;
+  const int chunks = (u.P + kChunk - 1) / kChunk;
+  const int free0 = tid < chunks ? u.free_in[tid] : 0;
+  __shared__ int own_page, own_copied, own_need, own_full, own_kept;
   int sum = 0, r0 = 0;
-  for (int t = tid; t < s; t += 256) sum += needed(u, t);
-  scan256(sum, &r0);
-  const int need = needed(u, s);
-  const int full = (int)(keep >> u.bt_log2), kept = u.pages(keep);
+  for (int t = tid; t <= s; t += 256) {
+    const int64_t keep = u.keep(t);
+    const Last l = last_page(u, t, keep);
+    const int grow = u.pages(u.clip(u.new_lens[t])) - u.pages(keep);
+    const int need = (grow > 0 ? grow : 0) + (l.copied ? 1 : 0);
+    if (t < s) {
+      sum += need;
+    } else {
+      own_page = l.page;
+      own_copied = l.copied;
+      own_need = need;
+      own_full = (int)(keep >> u.bt_log2);
+      own_kept = u.pages(keep);
+    }
+  }
+  scan256(sum, &r0);   // (and a barrier)
+  const Last last{own_page, own_copied != 0};
+  if (!writer && !last.copied) return;
+  const int need = own_need, full = own_full, kept = own_kept;
   const int j0 = last.copied ? full : kept;   // fresh pages take columns j0 ..
   int32_t* row = u.table_out + (int64_t)s * u.W;
   __shared__ int copy_to, hit[256], start[256];   // chunks that hold wanted ranks
@@ -147,11 +159,10 @@ __global__ __launch_bounds__(256) void update_assign_kernel(Update u, Kv8 c) {
     if (tid == 0 && last.page >= 0 && !last.copied) atomicAdd(u.ref_out + last.page, 1);
   }
   // free pages by rank
-  const int chunks = (u.P + kChunk - 1) / kChunk;
   int seen = 0;
   const int want = writer ? need : 1;
   for (int b = 0; b < chunks && seen < r0 + want; b += 256) {
-    const int mine = b + tid < chunks ? u.free_in[b + tid] : 0;
+    const int mine = b == 0 ? free0 : b + tid < chunks ? u.free_in[b + tid] : 0;
     int all;
     const int before = seen + scan256(mine, &all);
     // this thread's chunk holds ranks before .. before + mine

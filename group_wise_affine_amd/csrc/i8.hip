@@ -17,12 +17,12 @@ namespace {
 // NT threads per row, each holding up to 4 chunks of 8 elements in registers
 // (rows longer than 32 * NT are read a second time).
 template <class T, int NT>
-__global__ __launch_bounds__(256) void i8_quantize_kernel(const uint16_t* __restrict__ x,
+__global__ __launch_bounds__(NT < 256 ? 256 : NT) void i8_quantize_kernel(const uint16_t* __restrict__ x,
                                                           int64_t ldx, int64_t rows, int K,
                                                           int8_t* __restrict__ xq,
                                                           float* __restrict__ sx) {
-  constexpr int kHold = 4;
-  const int64_t row = (int64_t)blockIdx.x * (256 / NT) + threadIdx.x / NT;
+  constexpr int kHold = 4, kBlock = NT < 256 ? 256 : NT;
+  const int64_t row = (int64_t)blockIdx.x * (kBlock / NT) + threadIdx.x / NT;
   const int t = threadIdx.x % NT;
   const bool live = row < rows;
   const uint16_t* xr = x + (live ? row : 0) * ldx;
@@ -41,7 +41,7 @@ __global__ __launch_bounds__(256) void i8_quantize_kernel(const uint16_t* __rest
     }
   uint32_t top = wave_umax(amax_halves(m));
   if constexpr (NT > 64) {
-    __shared__ uint32_t part[4];   // of the row's NT / 64 wavefronts
+    __shared__ uint32_t part[kBlock / 64];   // of the row's NT / 64 wavefronts
     const int wave = threadIdx.x / 64, w0 = wave - t / 64;
     if (t % 64 == 0) part[wave] = top;
     __syncthreads();
@@ -70,12 +70,11 @@ __global__ __launch_bounds__(256) void i8_quantize_kernel(const uint16_t* __rest
 }
 
 // --------------------------------------------------------------------- GEMV
-// 16 rows of W and up to 16 * MT rows of x per workgroup; the eight
-// wavefronts take 128-byte pieces of K in turn and their integer sums are
+// 16 rows of W and up to 16 * MT rows of x per workgroup; its NW wavefronts
+// take 128-byte pieces of K in turn and their integer sums are
 // added in LDS. v_mfma_i32_16x16x64_i8: A (W) row lane%16, B (x) column
 // lane%16, both k = 16 * (lane/16) .. +16; D column lane%16, rows
 // 4 * (lane/16) .. +4.
-constexpr int kGvWaves = 8;
 
 template <class T>
 __device__ __forceinline__ uint16_t i8_out(int acc, float sx, float sw, const uint16_t* bias,
@@ -89,16 +88,16 @@ __device__ __forceinline__ uint16_t i8_out(int acc, float sx, float sw, const ui
 // in, and every workgroup quantizes it into LDS while its first pieces of W
 // are on their way; otherwise codes and scales come in.
 // (13 x 2048: 14.2 us fused, 10.6 us in two launches; 1 x 4096: 5.7 and 10.0.)
-constexpr int kGvChunks = 2;
+constexpr int kGvChunks = 2, kGvFused = 8;   // (wavefronts)
 
-template <class T, int MT, bool FUSED>
-__global__ __launch_bounds__(64 * kGvWaves) void i8_gemv_kernel(
+template <class T, int MT, int NW, bool FUSED>
+__global__ __launch_bounds__(64 * NW) void i8_gemv_kernel(
     const uint16_t* __restrict__ x, int64_t ldx, const int8_t* __restrict__ xq,
     const float* __restrict__ sx, const int8_t* __restrict__ wq, const float* __restrict__ sw,
     const uint16_t* __restrict__ bias, uint16_t* __restrict__ y, int M, int N, int K) {
-  constexpr int kThreads = 64 * kGvWaves;
+  constexpr int kThreads = 64 * NW;
   constexpr int kGvHold = MT <= 2 ? 4 : 2;   // pieces in flight per wavefront
-  __shared__ int part[kGvWaves][MT * 256];
+  __shared__ int part[NW][MT * 256];
   __shared__ uint32_t top[16];
   extern __shared__ __attribute__((aligned(16))) uint8_t codes[];   // FUSED: [M][K + 16]
   const int tid = threadIdx.x, lane = tid % 64;
@@ -122,7 +121,7 @@ __global__ __launch_bounds__(64 * kGvWaves) void i8_gemv_kernel(
 #pragma unroll
       for (int h = 0; h < 2; h++)
         w[i][h] = __builtin_amdgcn_raw_buffer_load_b128(
-            rw, (int)at(row, k0 + i * kGvWaves * 128 + h * 64 + g * 16), 0, 0);
+            rw, (int)at(row, k0 + i * NW * 128 + h * 64 + g * 16), 0, 0);
   };
   fetch(wave * 128);
   const int ldc = K + 16;   // (16 rows' pieces fall on different banks)
@@ -164,7 +163,7 @@ __global__ __launch_bounds__(64 * kGvWaves) void i8_gemv_kernel(
     }
     __syncthreads();
   }
-  for (int k0 = wave * 128; k0 < K; k0 += kGvWaves * 128 * kGvHold) {
+  for (int k0 = wave * 128; k0 < K; k0 += NW * 128 * kGvHold) {
     if (k0 > wave * 128) fetch(k0);
     // x comes from the L2 (or LDS); all of it is asked for before its first use
     u32x4_t xv[MT][kGvHold][2];
@@ -172,7 +171,7 @@ __global__ __launch_bounds__(64 * kGvWaves) void i8_gemv_kernel(
     for (int i = 0; i < kGvHold; i++)
 #pragma unroll
       for (int h = 0; h < 2; h++) {
-        const int k = k0 + i * kGvWaves * 128 + h * 64 + g * 16;
+        const int k = k0 + i * NW * 128 + h * 64 + g * 16;
 #pragma unroll
         for (int t = 0; t < MT; t++) {
           if constexpr (FUSED)   // (past K: the last piece again, W is zero there)
@@ -203,7 +202,7 @@ __global__ __launch_bounds__(64 * kGvWaves) void i8_gemv_kernel(
     if (m >= M || n >= N) continue;
     int s = 0;
 #pragma unroll
-    for (int v = 0; v < kGvWaves; v++) s += part[v][i];
+    for (int v = 0; v < NW; v++) s += part[v][i];
     const float sm = FUSED ? amax_scale<T>(top[i / 16]) : sx[m];
     y[m * N + n] = i8_out<T>(s, sm, sw[n], bias, n);
   }
@@ -516,10 +515,16 @@ hipError_t launch_i8_quantize(int dt, const void* x, int64_t ldx, int64_t rows, 
   auto go = [&]<class T>() {
     const uint16_t* p = static_cast<const uint16_t*>(x);
     auto threads = [&]<int NT>() {   // per row: they hold 32 * NT elements
-      hipLaunchKernelGGL((i8_quantize_kernel<T, NT>), dim3((unsigned)((rows + 256 / NT - 1) / (256 / NT))),
-                         dim3(256), 0, st, p, ldx, rows, (int)K, xq, sx);
+      constexpr int block = NT < 256 ? 256 : NT, per = block / NT;
+      hipLaunchKernelGGL((i8_quantize_kernel<T, NT>), dim3((unsigned)((rows + per - 1) / per)),
+                         dim3(block), 0, st, p, ldx, rows, (int)K, xq, sx);
     };
-    if (K <= 2048) threads.template operator()<64>();
+    // few rows: the latency counts (13 x 2048: 3.6 us with 256 threads, 4.8 with
+    // 64; 13 x 8192: 4.2 with 512, 5.1 with 256); many: the fewer the better
+    // (777 x 8192: 10.0 with 512, 9.8 with 256)
+    if (rows <= 256 && K > 4096) threads.template operator()<512>();
+    else if (rows <= 256 && K > 512) threads.template operator()<256>();
+    else if (K <= 2048) threads.template operator()<64>();
     else if (K <= 4096) threads.template operator()<128>();
     else threads.template operator()<256>();
   };
@@ -529,15 +534,15 @@ hipError_t launch_i8_quantize(int dt, const void* x, int64_t ldx, int64_t rows, 
 }
 
 bool i8_fused(int64_t M, int64_t K) {
-  return M <= 16 && M * K <= kGvChunks * 64 * kGvWaves * 8;
+  return M <= 16 && M * K <= kGvChunks * 64 * kGvFused * 8;
 }
 
 hipError_t launch_i8_fused(int dt, const void* x, int64_t ldx, const int8_t* wq, const float* sw,
                            const void* bias, int64_t M, int64_t N, int64_t K, void* y,
                            hipStream_t st) {
   auto go = [&]<class T>() {
-    hipLaunchKernelGGL((i8_gemv_kernel<T, 1, true>), dim3((unsigned)((N + 15) / 16)),
-                       dim3(64 * kGvWaves), (size_t)(M * (K + 16)), st,
+    hipLaunchKernelGGL((i8_gemv_kernel<T, 1, kGvFused, true>), dim3((unsigned)((N + 15) / 16)),
+                       dim3(64 * kGvFused), (size_t)(M * (K + 16)), st,
                        static_cast<const uint16_t*>(x), ldx, nullptr, nullptr, wq, sw,
                        static_cast<const uint16_t*>(bias), static_cast<uint16_t*>(y), (int)M,
                        (int)N, (int)K);
@@ -584,10 +589,16 @@ hipError_t launch_i8_t(int dt, const int8_t* xq, const float* sx, const int8_t* 
   auto go = [&]<class T>() {
     if (p.gemv) {
       const unsigned nb = (unsigned)((N + 15) / 16);
+      auto waves = [&]<int MT, int NW>() {
+        hipLaunchKernelGGL((i8_gemv_kernel<T, MT, NW, false>),
+                           dim3(nb, (unsigned)((M + 16 * MT - 1) / (16 * MT))), dim3(64 * NW), 0,
+                           st, nullptr, 0, xq, sx, wq, sw, b, yo, (int)M, (int)N, (int)K);
+      };
       auto mv = [&]<int MT>() {
-        hipLaunchKernelGGL((i8_gemv_kernel<T, MT, false>),
-                           dim3(nb, (unsigned)((M + 16 * MT - 1) / (16 * MT))), dim3(64 * kGvWaves),
-                           0, st, nullptr, 0, xq, sx, wq, sw, b, yo, (int)M, (int)N, (int)K);
+        // (13 x 8192 x 2048: 6.5 us with 4 wavefronts, 7.2 with 8; at K = 4096 four
+        // would make two passes)
+        if (K <= 2048) waves.template operator()<MT, 4>();
+        else waves.template operator()<MT, 8>();
       };
       if (M <= 16) mv.template operator()<1>();
       else if (M <= 32) mv.template operator()<2>();

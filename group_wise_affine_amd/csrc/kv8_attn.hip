@@ -502,6 +502,12 @@ __global__ __launch_bounds__(256) void kv8_join_kernel(AttnArgs a) {
 }
 
 // ------------------------------------------------------------------ prompts
+// the value of the lane 32 away
+__device__ __forceinline__ float other_half(float x) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, x);
+  const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  return __builtin_bit_cast(float, threadIdx.x & 32 ? r[0] : r[1]);
+}
 // The work items of a prompt batch differ in length by as much as the contexts
 // do, and there are only a few of them per CU: the longest come first. Returns
 // the item of rank `rank` (every workgroup finds the ranks by itself: a few
@@ -551,6 +557,17 @@ __device__ __forceinline__ int longest_first(const AttnArgs& a, int rank, int it
 // over groups of 16 tokens, hence scalars. The running maximum is only raised
 // when it grows by more than 2^8: until then weights reach 256, which f16 and
 // the fp32 sums hold as well, and nothing is rescaled.
+//
+// Bound: the vector unit (conversions, exponentials and maxima: 1.4 cycles per
+// cycle of the matrix unit) and the clock under both; 725 to 790 TFLOP/s of visible
+// pairs for D = 128 in bf16, 600 in f16 (two products per value), 545 and 580 for
+// D = 64 and 256. Eight wavefronts that share a tile, and two groups of wavefronts
+// of which one multiplies while the other weighs, took the same time.
+//
+// No variant may need scratch memory: the compiler has put the stores of
+// spilled registers between a branch that some lanes take and its end, where the
+// other lanes store nothing. Hence the places that are computed again rather than
+// kept, and the scalar branches.
 template <class T, int D>
 __global__ __launch_bounds__(2 * kPromptRows, D == 256 ? 1 : 2) void kv8_prompt_kernel(AttnArgs a) {
   constexpr int NW = kPromptRows / 32;
@@ -582,7 +599,8 @@ __global__ __launch_bounds__(2 * kPromptRows, D == 256 ? 1 : 2) void kv8_prompt_
   const int tiles = most > 0 ? (most + kTile - 1) / kTile : 0;
   const int parts = tiles > 0 ? (tiles + a.per - 1) / a.per : 1;
   if (split >= parts) return;
-  const int first = split * a.per, last = min(first + a.per, tiles);
+  const int first = split * a.per;
+  const int last = __builtin_amdgcn_readfirstlane(min(first + a.per, tiles));   // scalar
 
   // this lane's query row; rows past the last repeat it, and nothing reads them
   const int rr = min(wave * 32 + col, rows - 1);
@@ -590,7 +608,6 @@ __global__ __launch_bounds__(2 * kPromptRows, D == 256 ? 1 : 2) void kv8_prompt_
   const int limit = len - n + i0 + ct;
   const int wave_min = len - n + i0 + min(wave * 32, rows - 1) / a.G;
   const int wave_max = len - n + i0 + min(wave * 32 + 31, rows - 1) / a.G;
-  const int64_t at = (int64_t)(t0 + i0 + ct) * (c.heads * a.G) + head * a.G + ch;
   half8_t qf[KS];
   float qs = a.scale;
   {
@@ -624,61 +641,70 @@ __global__ __launch_bounds__(2 * kPromptRows, D == 256 ? 1 : 2) void kv8_prompt_
 
   const int32_t* row = a.q.table + (int64_t)s * a.q.W;
   const int bt = c.bt_log2;
-  auto page_at = [&](int t) QMM_INLINE {
-    const int p = t < most ? row[t >> bt] : -1;   // most <= W << bt
-    return p < c.pages ? p : -1;
-  };
   // Each tile's pages are looked up two tiles ahead and its codes and scales
-  // loaded one tile ahead, so that no step waits for a load it has just asked
-  // for. Unit u of a thread: 16 columns of key token u / (D/16), 16 tokens of
-  // value column u / 4; threads 0 .. 3 carry the scales of their 16 tokens.
-  int kp[kUnits], vp[kUnits];
-  auto look_up = [&](int tile) QMM_INLINE {
+  // loaded one tile ahead, and nothing touches them before the next step (the
+  // page numbers are checked when they are used), so that no step waits for a
+  // load it has just asked for (783 us; 819 with the numbers checked as they
+  // came: four chunks of up to 2048 tokens behind up to 8000, 8 heads of 4,
+  // D = 128). Unit i of a thread: 16 columns of key token tk + i * kStep, 16
+  // tokens of value column vd + 64 i; the first wavefront carries the scales,
+  // its lane the ones of group lane modulo 4. Past the last token any page of
+  // the sequence will do.
+  constexpr int kStep = kThreads / (D / 16);   // tokens from one key unit to the next
+  const int tk = tid / (D / 16), vd = tid / 4, vc = tid % 4 * 16;
+  const uint32_t page_bytes = (uint32_t)c.block(1, 0);   // <= 2^24
+  const int in = (1 << bt) - 1;   // (bits of tk and of i * kStep do not overlap)
+  const int8_t* const kb = c.k + c.block(0, head) + (tk & in) * D + tid % (D / 16) * 16;
+  const int8_t* const vb = c.v + c.block(0, head) + (vd << bt) + (vc & in);
+  int kp[kUnits], vp;
+  auto look_up = [&](int tile) QMM_INLINE {   // most <= W << bt
 #pragma unroll
-    for (int i = 0; i < kUnits; i++) {
-      const int u = i * kThreads + tid;
-      kp[i] = page_at(tile * kTile + u / (D / 16));
-      vp[i] = page_at(tile * kTile + u % 4 * 16);
-    }
+    for (int i = 0; i < kUnits; i++)
+      kp[i] = row[min(tile * kTile + tk + i * kStep, most - 1) >> bt];
+    vp = row[min(tile * kTile + vc, most - 1) >> bt];
   };
+  // rows of keys in LDS, and where this thread's first units go
+  auto key_row = [](int t) QMM_INLINE {
+    return (t & 32) + 8 * ((t >> 4 & 1) * 2 + (t >> 2 & 1)) + 4 * (t >> 3 & 1) + (t & 3);
+  };
+  const int to_k = key_row(tk) * D + key_piece(key_row(tk), tid % (D / 16) * 2) * 8;
+  const int to_v = vd * kTile + ((vc / 8 ^ vd >> 1) & 7) * 8;
   u32x4_t kw[kUnits], vw[kUnits];
   float sk = 0, sv = 0;
   bool miss = false;
   auto fetch = [&]() QMM_INLINE {
-    if (tid < 4) {
-      miss = vp[0] < 0;
-      const int64_t blk = (int64_t)(miss ? 0 : vp[0]) * c.heads + head;
+    auto page = [&](int p) QMM_INLINE {
+      return (uint64_t)((uint32_t)p < (uint32_t)c.pages ? (uint32_t)p : 0);
+    };
+    if (wave == 0) {
+      miss = (uint32_t)vp >= (uint32_t)c.pages;
+      const int64_t blk = (int64_t)page(vp) * c.heads + head;
       sk = c.ks[blk];
       sv = c.vs[blk];
     }
 #pragma unroll
     for (int i = 0; i < kUnits; i++) {
-      const int u = i * kThreads + tid;
-      const int tk = u / (D / 16), kc = u % (D / 16), vd = u / 4, vc = u % 4 * 16;
-      kw[i] = *reinterpret_cast<const u32x4_t*>(c.k + c.block(kp[i] < 0 ? 0 : kp[i], head) +
-                                                (tk & ((1 << bt) - 1)) * D + kc * 16);
-      vw[i] = *reinterpret_cast<const u32x4_t*>(c.v + c.block(vp[i] < 0 ? 0 : vp[i], head) +
-                                                ((int64_t)vd << bt) + (vc & ((1 << bt) - 1)));
+      kw[i] = *reinterpret_cast<const u32x4_t*>(kb + (page(kp[i]) * page_bytes +
+                                                      (uint32_t)((i * kStep & in) * D)));
+      vw[i] = *reinterpret_cast<const u32x4_t*>(vb + (page(vp) * page_bytes +
+                                                      (uint32_t)(i * (kThreads / 4) << bt)));
     }
   };
   auto put = [&](int buf) QMM_INLINE {
-    if (tid < 4) {
-      lsk[buf][tid] = sk;
-      lsv[buf][tid] = miss ? -1.0f : sv;   // no scale is negative: not seen
+    if (wave == 0) {
+      lsk[buf][lane % 4] = sk;
+      lsv[buf][lane % 4] = miss ? -1.0f : sv;   // no scale is negative: not seen
     }
 #pragma unroll
     for (int i = 0; i < kUnits; i++) {
-      const int u = i * kThreads + tid;
-      const int tk = u / (D / 16), kc = u % (D / 16);
-      const int kr = (tk & 32) + 8 * ((tk >> 4 & 1) * 2 + (tk >> 2 & 1)) + 4 * (tk >> 3 & 1) + (tk & 3);
-      const int vd = u / 4, vc = u % 4;
-#pragma unroll
-      for (int j = 0; j < 2; j++) {
-        *reinterpret_cast<half8_t*>(&lk[buf][kr * D + key_piece(kr, kc * 2 + j) * 8]) =
-            codes_f16(kw[i][2 * j], kw[i][2 * j + 1]);
-        *reinterpret_cast<half8_t*>(&lv[buf][vd * kTile + (((vc * 2 + j) ^ vd >> 1) & 7) * 8]) =
-            codes_f16(vw[i][2 * j], vw[i][2 * j + 1]);
-      }
+      const int r = key_row(i * kStep);
+      uint16_t* kt = &lk[buf][(to_k ^ (r & (D / 8 - 1)) * 8) + r * D];
+      uint16_t* vt = &lv[buf][to_v + i * (kThreads / 4) * kTile];
+      const int odd = (to_k & 8) ? -8 : 8, odd_v = (to_v & 8) ? -8 : 8;   // the other piece
+      *reinterpret_cast<half8_t*>(kt) = codes_f16(kw[i][0], kw[i][1]);
+      *reinterpret_cast<half8_t*>(kt + odd) = codes_f16(kw[i][2], kw[i][3]);
+      *reinterpret_cast<half8_t*>(vt) = codes_f16(vw[i][0], vw[i][1]);
+      *reinterpret_cast<half8_t*>(vt + odd_v) = codes_f16(vw[i][2], vw[i][3]);
     }
   };
   // one tile's softmax and second product; MASK: some of its tokens are not
@@ -701,7 +727,7 @@ __global__ __launch_bounds__(2 * kPromptRows, D == 256 ? 1 : 2) void kv8_prompt_
       }
       mx = fmaxf(mx, MASK ? top : top * f[g]);
     }
-    mx = fmaxf(mx, __shfl_xor(mx, 32));
+    mx = fmaxf(mx, other_half(mx));
     if (__any(mx > m_run + 8.0f || ve != v_exp)) {
       const float mn = fmaxf(m_run, mx);
       const float al = mn == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(m_run - mn);
@@ -713,6 +739,8 @@ __global__ __launch_bounds__(2 * kPromptRows, D == 256 ? 1 : 2) void kv8_prompt_
       v_exp = ve;
     }
     const float mu = m_run == -__builtin_inff() ? 0.0f : m_run;
+    int at = col * kTile + ((h ^ col >> 1) & 7) * 8;
+    asm volatile("" : "+v"(at));
 #pragma unroll
     for (int g = 0; g < 4; g++) {
       const float r = ldexpf(vs[g], -v_exp);
@@ -729,9 +757,8 @@ __global__ __launch_bounds__(2 * kPromptRows, D == 256 ? 1 : 2) void kv8_prompt_
       }
 #pragma unroll
       for (int i = 0; i < VD; i++) {
-        const int d = i * 32 + col;
-        const half8_t vf = *reinterpret_cast<const half8_t*>(
-            &lv[buf][d * kTile + (((g * 2 + h) ^ d >> 1) & 7) * 8]);
+        const half8_t vf =
+            *reinterpret_cast<const half8_t*>(&lv[buf][(at ^ g * 16) + i * 32 * kTile]);
         o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, hi, o[i], 0, 0, 0);
         if constexpr (kTwo) o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, lo, o[i], 0, 0, 0);
       }
@@ -764,6 +791,8 @@ __global__ __launch_bounds__(2 * kPromptRows, D == 256 ? 1 : 2) void kv8_prompt_
         if (!gone && e <= 127) ve = max(ve, e);   // NaN and infinity leave it
         missing |= gone ? 1u << g : 0u;
       }
+      int at = col * D + key_piece(col, h) * 8;
+      asm volatile("" : "+v"(at));   // (places of operands are not kept either)
       float16_t sc[2];
 #pragma unroll
       for (int j = 0; j < 2; j++)
@@ -773,9 +802,7 @@ __global__ __launch_bounds__(2 * kPromptRows, D == 256 ? 1 : 2) void kv8_prompt_
       for (int ks = 0; ks < KS; ks++)
 #pragma unroll
         for (int j = 0; j < 2; j++) {
-          const int r = j * 32 + col;
-          const half8_t kf =
-              *reinterpret_cast<const half8_t*>(&lk[buf][r * D + key_piece(r, ks * 2 + h) * 8]);
+          const half8_t kf = *reinterpret_cast<const half8_t*>(&lk[buf][(at ^ ks * 16) + j * 32 * D]);
           sc[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, qf[ks], sc[j], 0, 0, 0);
         }
       const int left = limit - base - h * 8;   // tokens g * 16 + e up to this are seen
@@ -802,6 +829,9 @@ __global__ __launch_bounds__(2 * kPromptRows, D == 256 ? 1 : 2) void kv8_prompt_
             float4_t{o[i][q * 4], o[i][q * 4 + 1], o[i][q * 4 + 2], o[i][q * 4 + 3]} * vref;
     return;
   }
+  int r_out = wave * 32 + col;   // (not kept through the loop: registers are short)
+  asm volatile("" : "+v"(r_out));
+  const int64_t at = (int64_t)(t0 + i0 + r_out / a.G) * (c.heads * a.G) + head * a.G + r_out % a.G;
   const bool any = l_run > 0.0f || l_run != l_run;
   const float back = any ? ldexpf(1.0f, v_exp) / l_run : 0.0f;
 #pragma unroll

@@ -2,7 +2,7 @@
 // the C ABI cannot make (it sees pointers, not tensors), the outputs, the
 // scratch buffer of the stream, and the call. The calls
 // take a few microseconds on the GPU; in Python this part alone took longer
-// (13.5 us for a product that takes 9, 20 us for append and read).
+// (13.5 us for a product that takes 8, 20 us for append and read).
 //
 // group_wise_affine_amd/qmm.py holds the functions that users call and their
 // documentation.

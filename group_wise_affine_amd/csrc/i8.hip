@@ -562,9 +562,21 @@ hipError_t launch_i8_fused(int dt, const void* x, int64_t ldx, const int8_t* wq,
   return hipGetLastError();
 }
 
+// Whether the GEMV takes the product. Beyond kI8GemvMaxM rows it reads W once
+// per 64 of them, which it pays 9 us per 2^30 multiply-adds for; the tile kernel's
+// start, end and exchange of K parts cost more than that where there is little
+// to do (512 x 512 x 2048: 7.5 us against 13.8; 300 x 1000 x 1504: 7.5 and 10.8;
+// 1024 x 512 x 2048: 12.6 and 15.1; but 1024 x 1024 x 1024: 12.9 and 9.5, 2048 x
+// 2048 x 128: 14.3 and 7.4).
+static bool i8_few(int64_t M, int64_t N, int64_t K) {
+  if (M <= kI8GemvMaxM) return true;
+  if (M > 8192 || K <= 512) return false;
+  return (M + 63) / 64 * 64 * N * K <= (int64_t)1 << (K >= 2048 ? 30 : 29);
+}
+
 I8Plan i8_plan(int64_t M, int64_t N, int64_t K) {
   I8Plan p{};
-  if (M <= kI8GemvMaxM) {
+  if (i8_few(M, N, K)) {
     p.gemv = true;
     p.ks = 1;
     return p;

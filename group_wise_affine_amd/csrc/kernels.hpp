@@ -220,8 +220,8 @@ void force_route(Route r);
 Route forced_route();   // the current override (kRouteNone: automatic)
 
 // ------------------------------------------------------------ int8 products
-// Rows of x that the GEMV takes (it reads W once). 64 x 4096 x 4096: 13.2 us,
-// the tile kernel 15.9; 96 rows: 18.4 and 16.1.
+// Rows of x that the GEMV takes whatever N and K (it reads W once). 64 x 4096 x
+// 4096: 13.2 us, the tile kernel 15.9; 96 rows: 18.4 and 16.1.
 constexpr int64_t kI8GemvMaxM = 64;
 // arrival counters (4 bytes each) at the start of a scratch buffer
 constexpr int64_t kScratchCounters = 16384;

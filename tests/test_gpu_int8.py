@@ -93,6 +93,14 @@ def test_linear(M, N, K, dt):
     check(y, y64, mag, dt, f"linear {M}x{N}x{K} {dt}")
 
 
+# more rows than the GEMV's one pass over W, on both sides of where it ends
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("M,N,K", [(65, 64, 528), (65, 64, 512), (130, 515, 2064), (300, 1000, 1504), (320, 1640, 1024),
+                                   (320, 1639, 1024), (1000, 50, 2048), (4100, 17, 1040), (8200, 9, 1040)])
+def test_linear_many_rows_little_work(M, N, K, dt):
+    test_linear(M, N, K, dt)
+
+
 @pytest.mark.parametrize("M,N,K", [(1, 40, 131056), (40, 40, 131056), (300, 300, 131056)])
 def test_largest_sums_are_exact(M, N, K):
     """Every code at its bound and the longest row: the sum 131056 * 127^2 =

@@ -29,7 +29,8 @@ struct Refused : std::runtime_error {   // -> ValueError
 struct Failed {};                       // a Python exception is set
 
 PyObject* g_fail = nullptr;   // fail(status, message) raises the binding's error
-PyObject* g_grow = nullptr;   // grow(bytes, device, stream) -> scratch tensor, counters zero
+PyObject* g_grow = nullptr;   // grow(bytes, device, stream, number of its capture or 0)
+                              // -> scratch, counters zero
 
 template <class... A>
 [[noreturn]] void refuse(const A&... a) {
@@ -109,7 +110,8 @@ Place place(PyObject* stream, std::initializer_list<std::pair<const Tensor*, con
 // Scratch for calls on one stream, kept and reused as a program's workspace
 // is. (The interpreter's lock is held from here until a call's launches are
 // queued, so that calls of two threads on one stream do not mix.) A graph
-// under capture gets its own, cleared in the graph.
+// under capture gets its own, cleared in the graph, which goes back to the
+// graph's pool in the order of the stream when the call returns.
 struct Scratch {
   void* p = nullptr;
   int64_t bytes = 0;
@@ -119,14 +121,15 @@ Scratch scratch(int64_t need, const Place& at) {
   // never destroyed: the allocator may be gone when the process ends
   static auto& held = *new std::map<std::pair<int, hipStream_t>, Tensor>;
   hipStreamCaptureStatus cs = hipStreamCaptureStatusNone;
-  const bool capturing = hipStreamIsCapturing(at.st, &cs) == hipSuccess && cs != hipStreamCaptureStatusNone;
+  unsigned long long id = 0;
+  const bool capturing = hipStreamGetCaptureInfo(at.st, &cs, &id) == hipSuccess && cs != hipStreamCaptureStatusNone;
   Tensor* t = nullptr;
   if (!capturing) {
     t = &held[{at.dev, at.st}];
     if (t->defined() && t->numel() >= need) return {t->data_ptr(), t->numel()};
   }
-  PyObject* r = PyObject_CallFunction(g_grow, "LiLi", (long long)need, at.dev,
-                                      (long long)(intptr_t)at.st, capturing ? 1 : 0);
+  PyObject* r = PyObject_CallFunction(g_grow, "LiLK", (long long)need, at.dev,
+                                      (long long)(intptr_t)at.st, capturing ? id + 1 : 0ull);
   if (!r) throw Failed();
   const Tensor fresh = THPVariable_Unpack(r);
   Py_DECREF(r);

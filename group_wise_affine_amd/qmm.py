@@ -572,23 +572,38 @@ WORK_COUNTERS = 65536
 BINDING_PATH = os.path.join(_HERE, "_serving.so")
 _native = None
 _have_gpu = False
+_captured = 0   # the last capture that was found to own its memory
 
 
 def _raise(status, msg):
     raise QmmError(status, msg)
 
 
-def _grow(nbytes, dev, handle, capturing):
-    """Scratch for calls on one stream, its counters zero; under capture memory
-    of the graph, cleared in it."""
-    def make(n):
-        t = torch.empty(n, dtype=torch.uint8, device=f"cuda:{dev}")
-        t[:WORK_COUNTERS].zero_()
-        return t
-    if capturing:
-        return make(nbytes)
+def _grow(nbytes, dev, handle, capture):
+    """Scratch for calls on one stream, allocated and cleared on that stream, its
+    counters zero. With capture (the number of the capture that the stream is
+    in) it is memory of that graph, cleared in it: what frees it is ordered on the
+    stream, and nobody outside the graph can get it. The ordinary pool would
+    hand it out again while the graph still uses it, so a capture that torch
+    keeps no pool for is refused."""
+    global _captured
     with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=dev)):
-        return make(max(nbytes, 1 << 20))
+        t = torch.empty(nbytes if capture else max(nbytes, 1 << 20), dtype=torch.uint8, device=f"cuda:{dev}")
+        if capture and capture != _captured:   # looked up once per capture
+            if not _of_a_graph(t.data_ptr(), torch.cuda.memory_snapshot()):
+                raise ValueError("the stream is captured into a graph whose memory torch does not keep: "
+                                 "capture it with torch.cuda.graph")
+            _captured = capture
+        t[:WORK_COUNTERS].zero_()
+    return t
+
+
+def _of_a_graph(address, segments):
+    """Whether the allocator's segment at this address belongs to a pool of its own."""
+    for s in segments:
+        if s["address"] <= address < s["address"] + s["total_size"]:
+            return tuple(s["segment_pool_id"]) != (0, 0)
+    return False
 
 
 def _serving():

@@ -169,3 +169,53 @@ def test_graph_replays(M):
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(want, y)
+
+
+def test_graph_of_two_streams():
+    """A capture that forks to a side stream: the scratch of the call there (arrival
+    counters, codes, parts of K) is ordered on that stream, and memory that the
+    capture gives out meanwhile on its own stream is other memory."""
+    M, N, K = 128, 1030, 12288
+    assert Q.lib().qmm_i8_t_work(M, N, K) > 0   # K is cut: counters are used
+    x = rows(M, K, "bf16", 1).cuda()
+    wc, ws = Q.i8_quantize(rows(N, K, "bf16", 2).cuda())
+    side, out = torch.cuda.Stream(), torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+    Q.i8_linear(x, wc, ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        for _ in range(3):
+            Q.i8_linear(x, wc, ws, out=out, stream=side)
+            other = [torch.empty(1 << n, dtype=torch.uint8, device="cuda").fill_(255) for n in range(16, 24)]
+        mine = Q.i8_linear(x, wc, ws)
+        here.wait_stream(side)
+    for i in range(4):
+        x.copy_(rows(M, K, "bf16", 10 + i))
+        want = Q.i8_linear(x, wc, ws)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(want, out) and torch.equal(want, mine)
+    assert all(int(t.min()) == 255 for t in other)
+
+
+def test_graph_of_calls_that_cut_k():
+    """Counters and parts in a graph's own scratch, on the current stream."""
+    M, N, K = 100, 1100, 8192
+    assert Q.lib().qmm_i8_t_work(M, N, K) > 0
+    x = rows(M, K, "f16", 1).cuda()
+    wc, ws = Q.i8_quantize(rows(N, K, "f16", 2).cuda())
+    Q.i8_linear(x, wc, ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        ys = [Q.i8_linear(x, wc, ws) for _ in range(3)]
+    for i in range(4):
+        x.copy_(rows(M, K, "f16", 10 + i))
+        want = Q.i8_linear(x, wc, ws)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(want, y) for y in ys)

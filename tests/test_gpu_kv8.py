@@ -333,3 +333,34 @@ def test_offsets_past_32_bits():
                        Q.kv8_attention(small, q, i32([[0, 1, 2, 3]]), i32([T]), i32([0, 3])))
     Q.kv8_copy(dev, i32([P - 4]), dev, i32([P - 1]))
     assert torch.equal(dev.k[P - 4], dev.k[P - 1]) and torch.equal(dev.v[P - 4], dev.v[P - 1])
+
+
+def test_attention_graph_of_two_streams():
+    """Parts of a call on a side stream of a capture lie in memory that nothing
+    else of the capture gets."""
+    B, D, H, G = 16, 128, 2, 4
+    dev, ref = make(200, H, B, D, 50)
+    tab = i32(tables([1900, 900], B, 200, 51, W=400))
+    lens, cu = i32([1850, 7]), i32([0, 1, 2])
+    assert Q.lib().qmm_kv8_attention_work(dev._at, 2, H * G, 2, 400) > 0   # cut into parts
+    q = fresh(2, H * G, D, "f16", 52).cuda()
+    side, out = torch.cuda.Stream(), torch.empty(2, H * G, D, dtype=torch.float16, device="cuda")
+    Q.kv8_attention(dev, q, tab, lens, cu)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        for _ in range(3):
+            Q.kv8_attention(dev, q, tab, lens, cu, out=out, stream=side)
+            other = [torch.empty(1 << n, dtype=torch.uint8, device="cuda").fill_(255) for n in range(16, 25)]
+        here.wait_stream(side)
+    for i in range(4):
+        q.copy_(fresh(2, H * G, D, "f16", 60 + i))
+        lens.copy_(i32([1300 + 100 * i, 10 + 200 * i]))
+        want = Q.kv8_attention(dev, q, tab, lens, cu)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(want, out)
+    assert all(int(t.min()) == 255 for t in other)

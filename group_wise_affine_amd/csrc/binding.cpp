@@ -227,17 +227,29 @@ PyObject* i8_linear(PyObject* const* a) {
 }
 
 // -------------------------------------------------------------- 8-bit cache
-// A cache arrives as the address of its C structure and its key tensor (for
-// the device); the Python object that owns both checked its tensors once.
+// A cache arrives as the address of its C structure and the tuple of its four
+// tensors; the Python object that owns both checked their shapes once. That
+// they still lie where the structure says (a tensor can be given other memory
+// in place) is checked at each call.
 struct Cache {
   const qmm_kv8_cache* c;
   const Tensor* k;
 };
-Cache cache(PyObject* at, PyObject* k) {
+Cache cache(PyObject* at, PyObject* held) {
   Cache c;
   c.c = static_cast<const qmm_kv8_cache*>(PyLong_AsVoidPtr(at));
   if (PyErr_Occurred()) throw Failed();
-  c.k = &tensor(k, "cache");
+  if (!PyTuple_Check(held) || PyTuple_GET_SIZE(held) != 4) refuse("a cache has four tensors");
+  const std::pair<const void*, const char*> parts[4] = {
+      {c.c->k, "k"}, {c.c->v, "v"}, {c.c->k_scales, "k_scales"}, {c.c->v_scales, "v_scales"}};
+  const int64_t blocks = c.c->pages * c.c->heads;
+  const int64_t codes = blocks * c.c->page_tokens * c.c->head_dim;
+  for (int i = 0; i < 4; i++) {
+    const Tensor& t = tensor(PyTuple_GET_ITEM(held, i), parts[i].second);
+    if (t.numel() != (i < 2 ? codes : blocks) || t.data_ptr() != parts[i].first)
+      refuse("the cache's ", parts[i].second, " was given other memory: make a cache of the new tensors");
+  }
+  c.k = &tensor(PyTuple_GET_ITEM(held, 0), "cache");
   return c;
 }
 struct Batch {
@@ -261,7 +273,7 @@ const Tensor& new_rows(PyObject* o, const char* name, int64_t heads, int64_t dim
   return t;
 }
 
-// kv8_append(cache, cache.k, k, v, table, lens, cu, stream)
+// kv8_append(cache, its tensors, k, v, table, lens, cu, stream)
 PyObject* kv8_append(PyObject* const* a) {
   const Cache c = cache(a[0], a[1]);
   const Tensor& k = new_rows(a[2], "k", c.c->heads, c.c->head_dim);
@@ -277,7 +289,7 @@ PyObject* kv8_append(PyObject* const* a) {
   Py_RETURN_NONE;
 }
 
-// kv8_read(cache, cache.k, pages, bf16, stream)
+// kv8_read(cache, its tensors, pages, bf16, stream)
 PyObject* kv8_read(PyObject* const* a) {
   const Cache c = cache(a[0], a[1]);
   const Tensor& pages = tensor(a[2], "pages", 1);
@@ -293,7 +305,7 @@ PyObject* kv8_read(PyObject* const* a) {
   return tuple(k, v);
 }
 
-// kv8_attention(cache, cache.k, q, table, lens, cu, scale | None, out | None, lse wanted, stream)
+// kv8_attention(cache, its tensors, q, table, lens, cu, scale | None, out | None, lse wanted, stream)
 PyObject* kv8_attention(PyObject* const* a) {
   const Cache c = cache(a[0], a[1]);
   const Tensor& q = new_rows(a[2], "q", 0, c.c->head_dim);
@@ -323,7 +335,7 @@ PyObject* kv8_attention(PyObject* const* a) {
   return tuple(out, lse);
 }
 
-// kv8_update(cache, cache.k, ref, table, lens, parent, new_lens, stream)
+// kv8_update(cache, its tensors, ref, table, lens, parent, new_lens, stream)
 PyObject* kv8_update(PyObject* const* a) {
   const Cache c = cache(a[0], a[1]);
   const Batch b = batch(a[3], a[4], nullptr);
@@ -340,7 +352,7 @@ PyObject* kv8_update(PyObject* const* a) {
   return tuple(ref_out, table_out, shortage);
 }
 
-// kv8_compact(cache, cache.k, ref, table, stream)
+// kv8_compact(cache, its tensors, ref, table, stream)
 PyObject* kv8_compact(PyObject* const* a) {
   const Cache c = cache(a[0], a[1]);
   const Batch b = batch(a[3], nullptr, nullptr);
@@ -354,7 +366,7 @@ PyObject* kv8_compact(PyObject* const* a) {
   return tuple(ref_out, table_out, remap, used);
 }
 
-// kv8_copy(to, to.k, dst, source, source.k, src, stream)
+// kv8_copy(to, its tensors, dst, source, its tensors, src, stream)
 PyObject* kv8_copy(PyObject* const* a) {
   const Cache to = cache(a[0], a[1]), from = cache(a[3], a[4]);
   const Tensor& dst = tensor(a[2], "dst", 1);

@@ -645,7 +645,7 @@ def _bf16(dtype):
 def _cache(cache, name="cache"):
     if not isinstance(cache, Kv8Cache):
         raise ValueError(f"{name} must be a Kv8Cache")
-    return cache._at
+    return cache._at, cache._held
 
 
 def i8_quantize(x, out=None, stream=None):
@@ -698,26 +698,36 @@ class Kv8Cache:
         _check_tensor(v_scales, "v_scales", (P, H), torch.float32)
         if len({t.device for t in (k, v, k_scales, v_scales)}) > 1:
             raise ValueError("the cache's tensors must be on one device")
-        self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
-        self.pages, self.heads, self.page_tokens, self.head_dim = P, H, B, D
+        self._held = k, v, k_scales, v_scales
         self._c = _Kv8(k.data_ptr(), v.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
                        P, H, B, D)
         self._at = ctypes.addressof(self._c)
+
+    # The library is given these tensors' addresses, so they stay the cache's own:
+    # another tensor means another Kv8Cache.
+    k = property(lambda self: self._held[0])
+    v = property(lambda self: self._held[1])
+    k_scales = property(lambda self: self._held[2])
+    v_scales = property(lambda self: self._held[3])
+    pages = property(lambda self: self._c.pages)
+    heads = property(lambda self: self._c.heads)
+    page_tokens = property(lambda self: self._c.page_tokens)
+    head_dim = property(lambda self: self._c.head_dim)
 
 
 def kv8_append(cache, k, v, table, lens, cu, stream=None):
     """Write the new tokens' k and v [T, heads, head_dim] into the cache: sequence s
     owns rows cu[s] .. cu[s+1], its last places; lens [S] counts its tokens with
     them, table [S, W] (int32) names its pages."""
-    at = _cache(cache)
-    _serving().kv8_append(at, cache.k, k, v, table, lens, cu, _on(stream))
+    at, held = _cache(cache)
+    _serving().kv8_append(at, held, k, v, table, lens, cu, _on(stream))
 
 
 def kv8_read(cache, pages, dtype=torch.bfloat16, stream=None):
     """Pages as values: (k, v), both [n, heads, page_tokens, head_dim] in dtype, for
     int32 page numbers pages [n]."""
-    at = _cache(cache)
-    return _serving().kv8_read(at, cache.k, pages, _bf16(dtype), _on(stream))
+    at, held = _cache(cache)
+    return _serving().kv8_read(at, held, pages, _bf16(dtype), _on(stream))
 
 
 def kv8_attention(cache, q, table, lens, cu, scale=None, out=None, return_lse=False, stream=None):
@@ -725,8 +735,8 @@ def kv8_attention(cache, q, table, lens, cu, scale=None, out=None, return_lse=Fa
     their sequences in the cache (which hold the new tokens already). scale
     defaults to head_dim ** -0.5. Returns out [T, q_heads, head_dim], with
     return_lse (out, lse fp32 [T, q_heads])."""
-    at = _cache(cache)
-    return _serving().kv8_attention(at, cache.k, q, table, lens, cu, scale, out, return_lse, _on(stream))
+    at, held = _cache(cache)
+    return _serving().kv8_attention(at, held, q, table, lens, cu, scale, out, return_lse, _on(stream))
 
 
 def kv8_update(cache, ref, table, lens, parent, new_lens, stream=None):
@@ -734,20 +744,20 @@ def kv8_update(cache, ref, table, lens, parent, new_lens, stream=None):
     parent[s] and gets pages for new_lens[s] tokens. Returns (ref, table,
     shortage), new tensors; shortage int32 [1] counts pages that were wanted
     and not there."""
-    at = _cache(cache)
-    return _serving().kv8_update(at, cache.k, ref, table, lens, parent, new_lens, _on(stream))
+    at, held = _cache(cache)
+    return _serving().kv8_update(at, held, ref, table, lens, parent, new_lens, _on(stream))
 
 
 def kv8_compact(cache, ref, table, stream=None):
     """Pack the pages in use to the front of the cache (libqmm.h, qmm_kv8_compact).
     Returns (ref, table, remap, used): the new counts and table, each page's new
     number, and int32 [1] the number of pages in use."""
-    at = _cache(cache)
-    return _serving().kv8_compact(at, cache.k, ref, table, _on(stream))
+    at, held = _cache(cache)
+    return _serving().kv8_compact(at, held, ref, table, _on(stream))
 
 
 def kv8_copy(to, dst, source, src, stream=None):
     """Copy pages src [n] of the cache `source` to pages dst [n] of the cache `to`
     (int32 tensors; the dst distinct, none of them also a src of one cache)."""
     a, b = _cache(to, "to"), _cache(source, "source")
-    _serving().kv8_copy(a, to.k, dst, b, source.k, src, _on(stream))
+    _serving().kv8_copy(*a, dst, *b, src, _on(stream))

@@ -205,3 +205,30 @@ def test_binding_refuses_dtypes():
     w, s = cpu(8, 64, dt=torch.int8), cpu(8, dt=torch.float32)
     with pytest.raises(Q.QmmError):
         Q.i8_linear(cpu(4, 64, dt=torch.int32), w, s)
+
+
+@pytest.mark.parametrize("name", ["k", "v", "k_scales", "v_scales", "pages", "heads", "page_tokens", "head_dim"])
+def test_a_cache_keeps_its_tensors(name):
+    """The library holds their addresses: another tensor is another cache."""
+    c = Q.Kv8Cache(4, 2, 16, 64, device="cpu")
+    with pytest.raises(AttributeError):
+        setattr(c, name, getattr(c, name))
+
+
+@pytest.mark.parametrize("name", ["k", "v", "k_scales", "v_scales"])
+@pytest.mark.parametrize("how", ["data", "resize"])
+def test_a_cache_whose_memory_was_replaced_is_refused(name, how):
+    tab, lens, cu = cpu(2, 3, dt=torch.int32), cpu(2, dt=torch.int32), cpu(3, dt=torch.int32)
+    ref, x = cpu(4, dt=torch.int32), cpu(5, 2, 64)
+    good, c = (Q.Kv8Cache(4, 2, 16, 64, device="cpu") for _ in range(2))
+    keep = getattr(c, name).clone()
+    if how == "data":
+        getattr(c, name).data = keep
+    else:
+        getattr(c, name).resize_(0)
+    for call in (lambda: Q.kv8_append(c, x, x, tab, lens, cu), lambda: Q.kv8_read(c, ref),
+                 lambda: Q.kv8_attention(c, x, tab, lens, cu), lambda: Q.kv8_update(c, ref, tab, lens, lens, lens),
+                 lambda: Q.kv8_compact(c, ref, tab), lambda: Q.kv8_copy(good, ref, c, ref),
+                 lambda: Q.kv8_copy(c, ref, good, ref)):
+        with pytest.raises(ValueError, match="other memory"):
+            call()

@@ -732,8 +732,9 @@ __global__ __launch_bounds__(2 * kPromptRows, D == 256 ? 1 : 2) void kv8_prompt_
       mx = fmaxf(mx, MASK ? top : top * f[g]);
     }
     mx = fmaxf(mx, other_half(mx));
-    if (__any(mx > m_run + 8.0f || ve != v_exp)) {
-      const float mn = fmaxf(m_run, mx);
+    const bool raise = mx > m_run + 8.0f || ve != v_exp;
+    if (__any(raise)) {   // (a row's results do not depend on the other rows')
+      const float mn = raise ? fmaxf(m_run, mx) : m_run;
       const float al = mn == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(m_run - mn);
       const float down = ldexpf(al, v_exp - ve);
       l_run *= al;
@@ -792,7 +793,8 @@ __global__ __launch_bounds__(2 * kPromptRows, D == 256 ? 1 : 2) void kv8_prompt_
         vs[g] = lsv[buf][g];
         const int e = (int)(__builtin_bit_cast(uint32_t, vs[g]) >> 23 & 255) - 127;
         const bool gone = __builtin_bit_cast(uint32_t, vs[g]) == 0xbf800000u;
-        if (!gone && e <= 127) ve = max(ve, e);   // NaN and infinity leave it
+        // NaN and infinity leave it, and so does what this row does not see
+        if (!gone && e <= 127 && base + g * 16 <= limit) ve = max(ve, e);
         missing |= gone ? 1u << g : 0u;
       }
       int at = col * D + key_piece(col, h) * 8;

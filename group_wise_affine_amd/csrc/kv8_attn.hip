@@ -10,9 +10,9 @@
 //
 // Both products run on the f16 matrix units: codes are exact in f16, queries
 // too (bf16 rows are first scaled by a power of two), so only the weights
-// exp(x - m) * vs are rounded on their way into the second product (to 11
-// bits for bf16 results, to two f16 terms for f16 ones); sums, maxima and the
-// normaliser stay in fp32.
+// exp(x - m) * vs are rounded on their way into the second product, relative
+// to the row's largest (to 11 bits for bf16 results, to two f16 terms for f16
+// ones); sums, maxima and the normaliser stay in fp32.
 #include "kernels.hpp"
 #include "kv8_common.hpp"
 
@@ -78,6 +78,32 @@ __device__ __forceinline__ half8_t bf16_to_f16(const uint4& u, float down) {
 #pragma unroll
   for (int i = 0; i < 8; i++) r[i] = (_Float16)(f[i] * down);
   return r;
+}
+
+// The weights 2^x * vs (x a score times log2 e) go into the second product as
+// f16 relative to 2^w, w the largest x + log2 vs that the row has seen: the
+// page that carries a result keeps its bits, however small its scale beside
+// others of no weight. The sum of 2^x is held relative to 2^base, base the
+// largest x, or up to 2^64 below it where w lies far below (the keys of weight
+// have values of nearly no scale): the exponentials that then matter stay within
+// fp32. Both only rise as a row goes on.
+struct Refs {
+  float w, base;
+};
+constexpr float kNone = -0x1.fffffep+127f;   // before a row's first key
+// from tokens whose largest x is m and whose largest x + log2 vs is w
+__device__ __forceinline__ Refs rise(Refs r, float m, float w) {
+  Refs n;
+  n.w = fmaxf(r.w, w);
+  n.base = fmaxf(r.base, fmaxf(m - 64.0f, fminf(m, n.w + 64.0f)));
+  n.w = fmaxf(n.w, n.base - 126.0f);
+  return n;
+}
+// vs * 2^(base - w), finite for a finite scale (where the product would not be,
+// 2^(x - base) is 0); a NaN stays
+__device__ __forceinline__ float weight_scale(float vs, const Refs& at) {
+  const float r = vs * __builtin_amdgcn_exp2f(at.base - at.w);
+  return r > 0x1.fffffep+127f ? 0x1.fffffep+127f : r;
 }
 
 // two outputs of a row, and whether it has seen a key at all
@@ -188,10 +214,8 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : D == 128 ? 2 : 3) void kv8_
   float4_t o[VD];
 #pragma unroll
   for (int i = 0; i < VD; i++) o[i] = float4_t{0, 0, 0, 0};
-  float m_run = -__builtin_inff(), l_run = 0.0f;
-  // O holds sums of codes weighted with p * vs / vref, vref = 2^v_exp a power
-  // of two that follows the largest value scale seen
-  int v_exp = -126;
+  Refs at{kNone, kNone};   // O relative to 2^at.w, l to 2^at.base
+  float l_run = 0.0f;
 
   const int32_t* row = a.q.table + (int64_t)s * a.q.W;
   // Every wavefront walks a run of tiles. The numbers and scales of the next 64
@@ -287,23 +311,20 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : D == 128 ? 2 : 3) void kv8_
       for (int i = 0; i < 16; i++) p[i] = i <= left ? p[i] : -__builtin_inff();
       r = left < 0 ? 0.0f : r;
     }
-    float mx = m_run;
+    float mx = -__builtin_inff();
 #pragma unroll
     for (int i = 0; i < 16; i++) mx = fmaxf(mx, p[i]);
+    // (an infinite or NaN scale leaves the reference, a zero's logarithm is -inf)
+    float wx = r < __builtin_inff() ? mx + __builtin_amdgcn_logf(r) : -__builtin_inff();
     mx = fmaxf(mx, __shfl_xor(mx, 16));
+    wx = fmaxf(wx, __shfl_xor(wx, 16));
     mx = fmaxf(mx, __shfl_xor(mx, 32));
-    const float mu = mx == -__builtin_inff() ? 0.0f : mx;
-    // the largest value scale's exponent (NaN and infinity leave it)
-    int ve = (int)(__builtin_bit_cast(uint32_t, r) >> 23 & 255) - 127;
-    ve = ve > 127 ? -126 : ve;
-    ve = max(ve, __shfl_xor(ve, 16));
-    ve = max(max(ve, __shfl_xor(ve, 32)), v_exp);
-    const float al = __builtin_amdgcn_exp2f(m_run - mu);
-    const float down = ldexpf(al, v_exp - ve);   // what the values so far shrink by
-    l_run *= al;
-    m_run = mx;
-    v_exp = ve;
-    r = ldexpf(r, -v_exp);
+    wx = fmaxf(wx, __shfl_xor(wx, 32));
+    const Refs to = rise(at, mx, wx);
+    const float down = __builtin_amdgcn_exp2f(at.w - to.w);   // what the values so far shrink by
+    l_run *= __builtin_amdgcn_exp2f(at.base - to.base);
+    at = to;
+    r = weight_scale(r, at);
     // (always: a branch around it costs more registers than it saves cycles)
 #pragma unroll
     for (int i = 0; i < VD; i++) o[i] *= down;
@@ -312,7 +333,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : D == 128 ? 2 : 3) void kv8_
       half8_t pf, pl;
 #pragma unroll
       for (int i = 0; i < 8; i++) {
-        const float e = __builtin_amdgcn_exp2f(p[8 * h + i] - mu);
+        const float e = __builtin_amdgcn_exp2f(p[8 * h + i] - at.base);
         l_run += e;
         const float w = e * r;
         pf[i] = (_Float16)w;
@@ -338,10 +359,10 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : D == 128 ? 2 : 3) void kv8_
   __shared__ float jm[NW][16], jl[NW][16];
   extern __shared__ __attribute__((aligned(16))) float jo[];   // [NW][16][D]
   if (g == 0) {
-    jm[wave][col] = m_run;
+    jm[wave][col] = at.base;
     jl[wave][col] = l_run;
   }
-  const float vref = ldexpf(1.0f, v_exp);
+  const float vref = __builtin_amdgcn_exp2f(at.w - at.base);
 #pragma unroll
   for (int i = 0; i < VD; i++)
     *reinterpret_cast<float4_t*>(jo + ((wave * 16 + col) * D + i * 16 + g * 4)) = o[i] * vref;
@@ -349,14 +370,13 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : D == 128 ? 2 : 3) void kv8_
   float* part = a.ws + (((int64_t)blockIdx.x * gridDim.y + blockIdx.y) * a.splits + split) * kPart<D, 16>;
   for (int i = tid; i < rows * (D / 2); i += 64 * NW) {
     const int r = i / (D / 2), d = i % (D / 2) * 2;
-    float m = -__builtin_inff();
+    float m = kNone;
 #pragma unroll
     for (int w = 0; w < NW; w++) m = fmaxf(m, jm[w][r]);
-    const float mu = m == -__builtin_inff() ? 0.0f : m;
     float l = 0.0f, v0 = 0.0f, v1 = 0.0f;
 #pragma unroll
     for (int w = 0; w < NW; w++) {
-      const float e = __builtin_amdgcn_exp2f(jm[w][r] - mu);
+      const float e = __builtin_amdgcn_exp2f(jm[w][r] - m);
       const float2 v = *reinterpret_cast<const float2*>(jo + (w * 16 + r) * D + d);
       l += jl[w][r] * e;
       v0 += v.x * e;
@@ -423,15 +443,14 @@ __global__ __launch_bounds__(256) void kv8_join_few_kernel(AttnArgs a) {
     }
   const JoinAt j = join_at<R == kPromptRows>(a, blockIdx.x, r);
   if (j.parts <= 1) return;
-  float m = -__builtin_inff(), l = 0.0f, v0 = 0.0f, v1 = 0.0f;
+  float m = kNone, l = 0.0f, v0 = 0.0f, v1 = 0.0f;
 #pragma unroll
   for (int w = 0; w < kFewParts; w++)
     if (w < j.parts) m = fmaxf(m, ml[w].x);
-  const float mu = m == -__builtin_inff() ? 0.0f : m;
 #pragma unroll
   for (int w = 0; w < kFewParts; w++)
     if (w < j.parts) {
-      const float e = __builtin_amdgcn_exp2f(ml[w].x - mu);
+      const float e = __builtin_amdgcn_exp2f(ml[w].x - m);
       l += ml[w].y * e;
       v0 = fmaf(v[w].x, e, v0);
       v1 = fmaf(v[w].y, e, v1);
@@ -467,17 +486,16 @@ __global__ __launch_bounds__(256) void kv8_join_kernel(AttnArgs a) {
   const int parts = j.parts;
   if (parts <= 1) return;   // written already
   // the parts' factors exp2(m - max) and the sum, by every wavefront
-  float m = -__builtin_inff(), l = 0.0f;
+  float m = kNone, l = 0.0f;
 #pragma unroll
   for (int k = 0; k < kMaxSplits / 64; k++)
     if (k * 64 + lane < parts) m = fmaxf(m, ml[k].x);
 #pragma unroll
   for (int x = 32; x >= 1; x >>= 1) m = fmaxf(m, __shfl_xor(m, x));
-  const float mu = m == -__builtin_inff() ? 0.0f : m;
 #pragma unroll
   for (int k = 0; k < kMaxSplits / 64; k++)
     if (k * 64 + lane < parts) {
-      const float e = __builtin_amdgcn_exp2f(ml[k].x - mu);
+      const float e = __builtin_amdgcn_exp2f(ml[k].x - m);
       l += ml[k].y * e;
       if (tid < 64) fac[k * 64 + lane] = e;
     }
@@ -558,9 +576,10 @@ __device__ __forceinline__ int longest_first(const AttnArgs& a, int rank, int it
 // S^T = K Q^T with v_mfma_f32_32x32x16_f16; D row 8 i + 4 h + r of lane half h
 // is made token 16 (i/2) + 8 h + 4 (i%2) + r, so that a lane's registers are,
 // eight by eight, the B operand of O^T = V^T P^T. A page's scales are uniform
-// over groups of 16 tokens, hence scalars. The running maximum is only raised
-// when it grows by more than 2^8: until then weights reach 256, which f16 and
-// the fp32 sums hold as well, and nothing is rescaled.
+// over groups of 16 tokens, hence scalars. The running maxima (of the scores
+// and of the weights with their scales) are only raised when one grows by more
+// than 2^8: until then weights reach 256, which f16 and the fp32 sums hold as
+// well, and nothing is rescaled.
 //
 // Bound: the vector unit (conversions, exponentials, maxima: 60 % of the cycles)
 // and after it the matrix unit (35 %); 725 to 790 TFLOP/s of visible
@@ -582,7 +601,7 @@ __global__ __launch_bounds__(2 * kPromptRows, D == 256 ? 1 : 2) void kv8_prompt_
   constexpr bool kTwo = __is_same(T, F16);
   static_assert(kUnits >= 1, "a unit per thread");
   __shared__ __attribute__((aligned(16))) uint16_t lk[2][kTile * D], lv[2][kTile * D];
-  __shared__ float lsk[2][4], lsv[2][4];
+  __shared__ float lsk[2][4], lsv[2][4], lsw[2][4];   // scales; log2 of the values'
   // position of 16-byte piece p of key row r (rows of D * 2 bytes)
   auto key_piece = [](int r, int p) QMM_INLINE {
     return (p ^ (D == 64 ? r >> 1 : r)) & (D / 8 - 1);
@@ -640,8 +659,8 @@ __global__ __launch_bounds__(2 * kPromptRows, D == 256 ? 1 : 2) void kv8_prompt_
   for (int i = 0; i < VD; i++)
 #pragma unroll
     for (int e = 0; e < 16; e++) o[i][e] = 0.0f;
-  float m_run = -__builtin_inff(), l_run = 0.0f;
-  int v_exp = -126;   // O holds sums of codes weighted with p * vs / 2^v_exp
+  Refs at{kNone, kNone};   // O relative to 2^at.w, l to 2^at.base
+  float l_run = 0.0f;
 
   const int32_t* row = a.q.table + (int64_t)s * a.q.W;
   const int bt = c.bt_log2;
@@ -698,6 +717,8 @@ __global__ __launch_bounds__(2 * kPromptRows, D == 256 ? 1 : 2) void kv8_prompt_
     if (wave == 0) {
       lsk[buf][lane % 4] = sk;
       lsv[buf][lane % 4] = miss ? -1.0f : sv;   // no scale is negative: not seen
+      // (an infinite or NaN scale leaves the reference of the weights)
+      lsw[buf][lane % 4] = !miss && sv < __builtin_inff() ? __builtin_amdgcn_logf(sv) : -__builtin_inff();
     }
 #pragma unroll
     for (int i = 0; i < kUnits; i++) {
@@ -713,10 +734,10 @@ __global__ __launch_bounds__(2 * kPromptRows, D == 256 ? 1 : 2) void kv8_prompt_
   };
   // one tile's softmax and second product; MASK: some of its tokens are not
   // seen by some of the wavefront's rows
-  auto weigh = [&]<bool MASK>(float16_t* sc, const float* f, const float* vs, int ve, int left,
+  auto weigh = [&]<bool MASK>(float16_t* sc, const float* f, const float* vs, int left,
                               uint32_t missing, int buf) QMM_INLINE {
     // element e of sc[j]: token 32 j + 16 (e/8) + 8 h + e%8
-    float mx = -__builtin_inff();
+    float mx = -__builtin_inff(), wx = -__builtin_inff();
 #pragma unroll
     for (int g = 0; g < 4; g++) {
       float top = -__builtin_inff();
@@ -729,31 +750,31 @@ __global__ __launch_bounds__(2 * kPromptRows, D == 256 ? 1 : 2) void kv8_prompt_
         }
         top = fmaxf(top, x);
       }
-      mx = fmaxf(mx, MASK ? top : top * f[g]);
+      if constexpr (!MASK) top *= f[g];
+      mx = fmaxf(mx, top);
+      wx = fmaxf(wx, top + lsw[buf][g]);
     }
     mx = fmaxf(mx, other_half(mx));
-    const bool raise = mx > m_run + 8.0f || ve != v_exp;
+    wx = fmaxf(wx, other_half(wx));
+    const bool raise = mx > at.base + 8.0f || wx > at.w + 8.0f;
     if (__any(raise)) {   // (a row's results do not depend on the other rows')
-      const float mn = raise ? fmaxf(m_run, mx) : m_run;
-      const float al = mn == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(m_run - mn);
-      const float down = ldexpf(al, v_exp - ve);
-      l_run *= al;
+      const Refs to = rise(at, raise ? mx : kNone, raise ? wx : kNone);
+      const float down = __builtin_amdgcn_exp2f(at.w - to.w);
+      l_run *= __builtin_amdgcn_exp2f(at.base - to.base);
 #pragma unroll
       for (int i = 0; i < VD; i++) o[i] *= down;
-      m_run = mn;
-      v_exp = ve;
+      at = to;
     }
-    const float mu = m_run == -__builtin_inff() ? 0.0f : m_run;
-    int at = col * kTile + ((h ^ col >> 1) & 7) * 8;
-    asm volatile("" : "+v"(at));
+    int piece = col * kTile + ((h ^ col >> 1) & 7) * 8;
+    asm volatile("" : "+v"(piece));
 #pragma unroll
     for (int g = 0; g < 4; g++) {
-      const float r = ldexpf(vs[g], -v_exp);
+      const float r = weight_scale(vs[g], at);
       half8_t hi, lo;
 #pragma unroll
       for (int e = 0; e < 8; e++) {
         const float x = sc[g / 2][g % 2 * 8 + e];
-        const float p = __builtin_amdgcn_exp2f(MASK ? x - mu : fmaf(x, f[g], -mu));
+        const float p = __builtin_amdgcn_exp2f(MASK ? x - at.base : fmaf(x, f[g], -at.base));
         l_run += p;
         float w = p * r;
         if constexpr (MASK) w = g * 16 + e <= left && !(missing >> g & 1) ? w : 0.0f;
@@ -763,9 +784,18 @@ __global__ __launch_bounds__(2 * kPromptRows, D == 256 ? 1 : 2) void kv8_prompt_
 #pragma unroll
       for (int i = 0; i < VD; i++) {
         const half8_t vf =
-            *reinterpret_cast<const half8_t*>(&lv[buf][(at ^ g * 16) + i * 32 * kTile]);
+            *reinterpret_cast<const half8_t*>(&lv[buf][(piece ^ g * 16) + i * 32 * kTile]);
         o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, hi, o[i], 0, 0, 0);
         if constexpr (kTwo) o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, lo, o[i], 0, 0, 0);
+      }
+      // (operands of the product after next are asked for before the present one)
+      if constexpr (D == 256) {
+        __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+#pragma unroll
+        for (int i = 0; i < VD; i++) {
+          __builtin_amdgcn_sched_group_barrier(0x008, kTwo ? 2 : 1, 0);
+          if (i < VD - 2) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        }
       }
     }
   };
@@ -785,20 +815,16 @@ __global__ __launch_bounds__(2 * kPromptRows, D == 256 ? 1 : 2) void kv8_prompt_
     const int base = tile * kTile;
     if (base <= wave_max) {
       float f[4], vs[4];
-      int ve = v_exp;
       uint32_t missing = 0;
 #pragma unroll
       for (int g = 0; g < 4; g++) {
         f[g] = lsk[buf][g] * qs;
         vs[g] = lsv[buf][g];
-        const int e = (int)(__builtin_bit_cast(uint32_t, vs[g]) >> 23 & 255) - 127;
         const bool gone = __builtin_bit_cast(uint32_t, vs[g]) == 0xbf800000u;
-        // NaN and infinity leave it, and so does what this row does not see
-        if (!gone && e <= 127 && base + g * 16 <= limit) ve = max(ve, e);
         missing |= gone ? 1u << g : 0u;
       }
-      int at = col * D + key_piece(col, h) * 8;
-      asm volatile("" : "+v"(at));   // (places of operands are not kept either)
+      int piece = col * D + key_piece(col, h) * 8;
+      asm volatile("" : "+v"(piece));   // (places of operands are not kept either)
       float16_t sc[2];
 #pragma unroll
       for (int j = 0; j < 2; j++)
@@ -808,14 +834,14 @@ __global__ __launch_bounds__(2 * kPromptRows, D == 256 ? 1 : 2) void kv8_prompt_
       for (int ks = 0; ks < KS; ks++)
 #pragma unroll
         for (int j = 0; j < 2; j++) {
-          const half8_t kf = *reinterpret_cast<const half8_t*>(&lk[buf][(at ^ ks * 16) + j * 32 * D]);
+          const half8_t kf = *reinterpret_cast<const half8_t*>(&lk[buf][(piece ^ ks * 16) + j * 32 * D]);
           sc[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, qf[ks], sc[j], 0, 0, 0);
         }
       const int left = limit - base - h * 8;   // tokens g * 16 + e up to this are seen
       if (base + kTile - 1 <= wave_min && missing == 0)
-        weigh.template operator()<false>(sc, f, vs, ve, left, missing, buf);
+        weigh.template operator()<false>(sc, f, vs, left, missing, buf);
       else
-        weigh.template operator()<true>(sc, f, vs, ve, left, missing, buf);
+        weigh.template operator()<true>(sc, f, vs, left, missing, buf);
     }
     if (tile + 1 < last) put(buf ^ 1);
   }
@@ -824,8 +850,8 @@ __global__ __launch_bounds__(2 * kPromptRows, D == 256 ? 1 : 2) void kv8_prompt_
   if (parts > 1) {   // kv8_join_kernel adds them up
     const int64_t unit = (int64_t)index * c.heads + head;
     float* part = a.ws + (unit * a.splits + split) * kPart<D, kPromptRows>;
-    const float vref = ldexpf(1.0f, v_exp);
-    if (h == 0) *reinterpret_cast<float2*>(part + 2 * (wave * 32 + col)) = make_float2(m_run, l_run);
+    const float vref = __builtin_amdgcn_exp2f(at.w - at.base);
+    if (h == 0) *reinterpret_cast<float2*>(part + 2 * (wave * 32 + col)) = make_float2(at.base, l_run);
     float* mine = part + 2 * kPromptRows + (wave * 32 + col) * D + h * 4;
 #pragma unroll
     for (int i = 0; i < VD; i++)
@@ -837,9 +863,9 @@ __global__ __launch_bounds__(2 * kPromptRows, D == 256 ? 1 : 2) void kv8_prompt_
   }
   int r_out = wave * 32 + col;   // (not kept through the loop: registers are short)
   asm volatile("" : "+v"(r_out));
-  const int64_t at = (int64_t)(t0 + i0 + r_out / a.G) * (c.heads * a.G) + head * a.G + r_out % a.G;
+  const int64_t to = (int64_t)(t0 + i0 + r_out / a.G) * (c.heads * a.G) + head * a.G + r_out % a.G;
   const bool any = l_run > 0.0f || l_run != l_run;
-  const float back = any ? ldexpf(1.0f, v_exp) / l_run : 0.0f;
+  const float back = any ? __builtin_amdgcn_exp2f(at.w - at.base) / l_run : 0.0f;
 #pragma unroll
   for (int i = 0; i < VD; i++)
 #pragma unroll
@@ -847,10 +873,10 @@ __global__ __launch_bounds__(2 * kPromptRows, D == 256 ? 1 : 2) void kv8_prompt_
       uint16_t w[4];
 #pragma unroll
       for (int e = 0; e < 4; e++) w[e] = from_f32(T{}, any ? o[i][q * 4 + e] * back : 0.0f);
-      *reinterpret_cast<uint2*>(a.out + at * D + i * 32 + q * 8 + h * 4) =
+      *reinterpret_cast<uint2*>(a.out + to * D + i * 32 + q * 8 + h * 4) =
           make_uint2(w[0] | (uint32_t)w[1] << 16, w[2] | (uint32_t)w[3] << 16);
     }
-  if (h == 0 && a.lse) a.lse[at] = any ? fmaf(m_run, kLn2, logf(l_run)) : -__builtin_inff();
+  if (h == 0 && a.lse) a.lse[to] = any ? fmaf(at.base, kLn2, logf(l_run)) : -__builtin_inff();
 }
 
 // Sequences with at most this many query rows (new tokens x heads of a group)

@@ -545,8 +545,9 @@ qmm_status qmm_kv8_read(const qmm_kv8_cache* cache, const int32_t* pages, int64_
  * q_heads, head_dim] in dt, 16-byte aligned; lse [T, q_heads] fp32 (NULL: not
  * wanted) the natural logarithm of the sum of exponentials of the scores. A
  * query that sees nothing gets 0 and -inf. Sums, maxima and the normaliser
- * are held in fp32; exp(score - max) * v scale is rounded to f16 for the
- * matrix product with the codes.
+ * are held in fp32. The weights exp(score) * v scale enter the matrix product
+ * with the codes relative to the row's largest: with 11 bits for bf16 results
+ * and 22 for f16 ones, below 2^-14 of the largest to 2^-25 of it.
  */
 int64_t qmm_kv8_attention_work(const qmm_kv8_cache* cache, int64_t T, int64_t q_heads, int64_t S,
                                int64_t W);

@@ -67,7 +67,7 @@ struct Pow2 {
 };
 __device__ __forceinline__ Pow2 row_power(uint32_t m) {
   int e = (int)(m >> 7) - 127;
-  e = e < -100 ? -100 : e > 100 ? 100 : e;
+  e = e < -126 ? -126 : e > 126 ? 126 : e;   // both powers are finite and normal
   return {__builtin_bit_cast(float, (uint32_t)(127 + e) << 23),
           __builtin_bit_cast(float, (uint32_t)(127 - e) << 23)};
 }

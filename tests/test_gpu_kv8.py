@@ -364,3 +364,22 @@ def test_attention_graph_of_two_streams():
         torch.cuda.synchronize()
         assert torch.equal(want, out)
     assert all(int(t.min()) == 255 for t in other)
+
+
+@pytest.mark.parametrize("new", [1, 70])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("power", [124, 118, -118, -126])
+def test_attention_queries_of_any_magnitude(power, D, new):
+    """bf16 queries near the ends of their range, brought back by the scale: rows
+    with the largest finite and with subnormal values among them."""
+    B = 16
+    dev, ref = make(12, 1, B, D, 70)
+    lens, cu = [new + 90], [0, new]
+    tab = tables(lens, B, 12, 71)
+    q = fresh(new, 2, D, "bf16", 72).float().clamp(-15, 15) * 2.0 ** power
+    if power > 0:
+        q[0, 0, 3] = 3.38953e38
+    q = q.to(torch.bfloat16)
+    scale = 2.0 ** (-4 - power)
+    out, lse = Q.kv8_attention(dev, q.cuda(), i32(tab), i32(lens), i32(cu), return_lse=True, scale=scale)
+    check_attention(out, lse, ref, q, tab, lens, cu, scale, "bf16", f"queries of 2^{power}, D {D}, {new} new")

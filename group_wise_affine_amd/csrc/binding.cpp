@@ -77,7 +77,7 @@ int64_t rows(const Tensor& t, const char* name) {
       refuse(name, ": all dimensions but the first must be packed");
     width *= t.size(i);
   }
-  return t.size(0) > 1 || t.stride(0) > width ? t.stride(0) : width;
+  return t.size(0) > 1 ? t.stride(0) : width;   // (one row has no next one)
 }
 qmm_dtype element(at::ScalarType t) {
   if (t == at::kHalf) return QMM_F16;

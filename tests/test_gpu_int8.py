@@ -219,3 +219,18 @@ def test_graph_of_calls_that_cut_k():
         g.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(want, y) for y in ys)
+
+
+def test_one_row_of_a_wider_tensor():
+    """The distance to a next row, which is none, is no condition: a row of a tensor
+    whose rows are not a multiple of 8 long."""
+    big = rows(3, 260, "bf16", 1).cuda()
+    wc, ws = Q.i8_quantize(rows(40, 256, "bf16", 2).cuda())
+    part = big[:1, :256]
+    assert part.stride(0) == 260
+    c, s = Q.i8_quantize(part)
+    c2, s2 = Q.i8_quantize(part.contiguous())
+    assert torch.equal(c, c2) and torch.equal(s, s2)
+    assert torch.equal(Q.i8_linear(part, wc, ws), Q.i8_linear(part.contiguous(), wc, ws))
+    with pytest.raises(Q.QmmError):
+        Q.i8_linear(big[:2, :256], wc, ws)

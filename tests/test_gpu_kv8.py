@@ -383,3 +383,17 @@ def test_attention_queries_of_any_magnitude(power, D, new):
     scale = 2.0 ** (-4 - power)
     out, lse = Q.kv8_attention(dev, q.cuda(), i32(tab), i32(lens), i32(cu), return_lse=True, scale=scale)
     check_attention(out, lse, ref, q, tab, lens, cu, scale, "bf16", f"queries of 2^{power}, D {D}, {new} new")
+
+
+def test_one_token_of_a_wider_tensor():
+    B, D, H, G = 16, 64, 2, 4
+    a, _ = make(6, H, B, D, 80)
+    b, _ = make(6, H, B, D, 80)
+    line = fresh(1, 1, 800, "bf16", 81).cuda().view(-1)
+    take = lambda n, at: line.as_strided((1, n, D), (n * D + 3, D, 1), at)  # noqa: E731
+    k, v, q = take(H, 0), take(H, 128), take(H * G, 256)
+    args = (i32([[3, 1]]), i32([20]), i32([0, 1]))
+    Q.kv8_append(a, k, v, *args)
+    Q.kv8_append(b, k.contiguous(), v.contiguous(), *args)
+    assert torch.equal(a.k, b.k) and torch.equal(a.v, b.v)
+    assert torch.equal(Q.kv8_attention(a, q, *args), Q.kv8_attention(b, q.contiguous(), *args))

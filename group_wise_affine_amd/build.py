@@ -7,9 +7,12 @@ group_wise_affine_amd/libqmm.so. Flags:
                                          codes depend on it)
   -Xclang -target-feature -Xclang -packed-fp32-ops
                                          no packed fp32 VALU instructions
+The compiler's resource report says of every kernel in NO_SCRATCH that it spills
+no vector registers; a build in which one does fails.
 """
 import concurrent.futures as cf
 import os
+import re
 import subprocess
 import sys
 
@@ -34,16 +37,46 @@ FLAGS = [
     "-I" + os.path.join(ROOT, "include"),
 ]
 
+# Sources whose kernels may not use scratch memory: the compiler has put the
+# stores of spilled registers between a branch that some lanes take and its end,
+# so that the other lanes read back what they never stored.
+NO_SCRATCH = {"i8.hip", "kv8.hip", "kv8_attn.hip", "kv8_pages.hip"}
+REPORT = "-Rpass-analysis=kernel-resource-usage"
+
+
+def check_no_scratch(src, report):
+    """Raises unless the compiler's resource report names kernels of src and no
+    scratch memory or spilled vector register in any of them."""
+    kernel, seen, bad = None, set(), []
+    for line in report.splitlines():
+        m = re.search(r"remark: .*?(Function Name|ScratchSize \[bytes/lane\]|VGPRs Spill): (\S+)", line)
+        if not m:
+            continue
+        if m[1] == "Function Name":
+            kernel = m[2]
+            continue
+        seen.add((kernel, m[1]))
+        if m[2] != "0":
+            bad.append(f"{kernel}: {m[1]} {m[2]}")
+    kernels = {k for k, _ in seen}
+    if not kernels or len(seen) != 2 * len(kernels):
+        raise RuntimeError(f"{src}: the compiler reported no kernel's registers ({REPORT})")
+    if bad:
+        raise RuntimeError(f"{src}: kernels that may not use scratch memory do:\n" + "\n".join(bad))
+
 
 def _compile(src):
     obj = os.path.join(BUILD, os.path.basename(src) + ".o")
-    cmd = [HIPCC, *FLAGS, "-c", os.path.join(CSRC, src), "-o", obj]
+    checked = src in NO_SCRATCH
+    cmd = [HIPCC, *FLAGS, *([REPORT, "-fno-caret-diagnostics"] if checked else []), "-c", os.path.join(CSRC, src), "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"hipcc failed for {src}:\n{' '.join(cmd)}\n{r.stderr}")
+    if checked:
+        check_no_scratch(src, r.stderr)
     # the host pass warns about the device-only target feature; drop that noise
     msgs = [l for l in r.stderr.splitlines() if "packed-fp32-ops" not in l
-            and "not a recognized feature" not in l]
+            and "not a recognized feature" not in l and REPORT not in l]
     return obj, "\n".join(msgs)
 
 

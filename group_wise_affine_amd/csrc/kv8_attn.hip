@@ -589,8 +589,10 @@ __device__ __forceinline__ int longest_first(const AttnArgs& a, int rank, int it
 //
 // No variant may need scratch memory: the compiler has put the stores of
 // spilled registers between a branch that some lanes take and its end, where the
-// other lanes store nothing. Hence the places that are computed again rather than
-// kept, and the scalar branches.
+// other lanes store nothing; the build refuses a kernel here that does. Hence the
+// places that are computed again rather than kept, and the scalar branches. (26
+// to 38 scalar registers do not fit and wait in lanes of a vector register,
+// which needs no memory.)
 template <class T, int D>
 __global__ __launch_bounds__(2 * kPromptRows, D == 256 ? 1 : 2) void kv8_prompt_kernel(AttnArgs a) {
   constexpr int NW = kPromptRows / 32;

@@ -590,7 +590,7 @@ __device__ __forceinline__ int longest_first(const AttnArgs& a, int rank, int it
 // No variant may need scratch memory: the compiler has put the stores of
 // spilled registers between a branch that some lanes take and its end, where the
 // other lanes store nothing; the build refuses a kernel here that does. Hence the
-// places that are computed again rather than kept, and the scalar branches. (26
+// places that are computed again rather than kept, and the scalar branches. (30
 // to 38 scalar registers do not fit and wait in lanes of a vector register,
 // which needs no memory.)
 template <class T, int D>

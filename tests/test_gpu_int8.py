@@ -234,3 +234,23 @@ def test_one_row_of_a_wider_tensor():
     assert torch.equal(Q.i8_linear(part, wc, ws), Q.i8_linear(part.contiguous(), wc, ws))
     with pytest.raises(Q.QmmError):
         Q.i8_linear(big[:2, :256], wc, ws)
+
+
+# many tiles: those of 128 x 128 beyond one round of the chip, and those of 256 x
+# 256; ragged in M, N and K, rows of y that start on 2, 4 and 16 bytes
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("M,N,K", [(2100, 2201, 208), (2100, 2198, 272), (2100, 2200, 1040),
+                                   (3900, 3901, 208), (3971, 3898, 272), (3900, 3904, 1040)])
+def test_many_tiles(M, N, K, dt):
+    g = torch.Generator().manual_seed(M + N + K)
+    codes = lambda n: torch.randint(-127, 128, (n, K), generator=g).to(torch.int8)  # noqa: E731
+    xq, wq = codes(M), codes(N)
+    sx, sw = torch.rand(M, generator=g) * 0.1, torch.rand(N, generator=g) * 0.01
+    bias = rows(1, N, dt, 5)[0] if K != 272 else None
+    y = Q.i8_t(xq.cuda(), sx.cuda(), wq.cuda(), sw.cuda(), dtype=TORCH_DT[dt],
+               bias=None if bias is None else bias.cuda())
+    y64 = (xq.double() @ wq.double().t()) * (sx.double()[:, None] * sw.double())   # sums below 2^53: exact
+    mag = y64.abs()
+    if bias is not None:
+        y64, mag = y64 + bias.double(), mag + bias.double().abs()
+    check(y, y64.numpy(), mag.numpy(), dt, f"{M}x{N}x{K} {dt}")

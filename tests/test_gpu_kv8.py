@@ -397,3 +397,57 @@ def test_one_token_of_a_wider_tensor():
     Q.kv8_append(b, k.contiguous(), v.contiguous(), *args)
     assert torch.equal(a.k, b.k) and torch.equal(a.v, b.v)
     assert torch.equal(Q.kv8_attention(a, q, *args), Q.kv8_attention(b, q.contiguous(), *args))
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("B,D,G", [(16, 64, 4), (16, 64, 20), (32, 128, 20), (64, 256, 3), (64, 256, 20)])
+@pytest.mark.parametrize("n", [2500, 5003])
+def test_parts_of_every_head_size(n, B, D, G, dt):
+    """Few parts and many (two kernels join them), groups of more heads than a
+    workgroup takes, a second sequence that is not cut."""
+    lens, cu = [n, 40], [0, 1, 2]
+    held = -(-n // B)
+    dev, ref = make(held + 8, 1, B, D, n)
+    tab = tables(lens, B, held + 8, 2)
+    q = fresh(2, G, D, dt, 3)
+    out, lse = Q.kv8_attention(dev, q.cuda(), i32(tab), i32(lens), i32(cu), return_lse=True)
+    check_attention(out, lse, ref, q, tab, lens, cu, D ** -0.5, dt, f"{n} B{B} D{D} G{G} {dt}")
+
+
+@pytest.mark.parametrize("lens,new,G", [([310], [300], 128),                      # more items than threads
+                                        ([70 + i % 7 for i in range(300)], [1] * 299 + [70], 2),   # more sequences
+                                        ([5, 90] * 130, [1, 3] * 129 + [1, 80], 2)])
+def test_prompts_in_large_batches(lens, new, G):
+    """Batches whose work items are not sorted by length."""
+    B, D = 16, 64
+    P = sum(-(-n // B) for n in lens) + 3
+    dev, ref = make(P, 1, B, D, 90)
+    tab = tables(lens, B, P, 91)
+    cu = [0] + [int(c) for c in np.cumsum(new)]
+    q = fresh(cu[-1], G, D, "bf16", 92)
+    out, lse = Q.kv8_attention(dev, q.cuda(), i32(tab), i32(lens), i32(cu), return_lse=True)
+    check_attention(out, lse, ref, q, tab, lens, cu, D ** -0.5, "bf16", f"{len(lens)} sequences, {cu[-1]} new")
+
+
+@pytest.mark.parametrize("S", [64, 65, 700, 4096, 4097, 5000])
+def test_many_sequences(S):
+    """A sequence of an item is found in one, two or three looks at 64 boundaries:
+    append and attention, some sequences without a token."""
+    B, D, H = 16, 64, 1
+    r = np.random.default_rng(S)
+    new = [int(x) for x in r.choice([0, 1, 1, 1, 3], S)]
+    new[0] = new[S - 1] = 1
+    lens = [n + int(x) for n, x in zip(new, r.integers(0, 40, S))]
+    P = sum(-(-n // B) for n in lens) + 1
+    dev, ref = make(P, H, B, D, S)
+    tab = tables(lens, B, P, 93)
+    cu = [0] + [int(c) for c in np.cumsum(new)]
+    T = cu[-1]
+    k, v = fresh(T, H, D, "f16", 94), fresh(T, H, D, "f16", 95)
+    args = (i32(tab), i32(lens), i32(cu))
+    Q.kv8_append(dev, k.cuda(), v.cuda(), *args)
+    ref.append(k.float().numpy(), v.float().numpy(), tab, lens, cu)
+    same_cache(dev, ref)
+    q = fresh(T, 2, D, "f16", 96)
+    out, lse = Q.kv8_attention(dev, q.cuda(), *args, return_lse=True)
+    check_attention(out, lse, ref, q, tab, lens, cu, D ** -0.5, "f16", f"{S} sequences")

@@ -8,7 +8,9 @@ group_wise_affine_amd/libqmm.so. Flags:
   -Xclang -target-feature -Xclang -packed-fp32-ops
                                          no packed fp32 VALU instructions
 The compiler's resource report says of every kernel in NO_SCRATCH that it spills
-no vector registers; a build in which one does fails.
+no vector registers, and the assembly of the sources in ASM_PRODUCTS that it
+leaves the sums of matrix products written in assembly alone between them; a
+build in which this is not so fails.
 """
 import concurrent.futures as cf
 import os
@@ -65,6 +67,54 @@ def check_no_scratch(src, report):
         raise RuntimeError(f"{src}: kernels that may not use scratch memory do:\n" + "\n".join(bad))
 
 
+# Sources with matrix products in inline assembly, of whose results the compiler
+# knows nothing: read or moved less than 12 instructions after the product, they
+# are not there yet. The products' blocks stand in loops; the last block of an
+# iteration ends with the wait where the loop ends.
+ASM_PRODUCTS = {"i8.hip"}
+_SUMS = re.compile(r"\ba(\d|\[\d)|accvgpr")
+
+
+def check_products(src, asm):
+    """Raises if, in this assembly, a sum (they are in the accumulation registers)
+    is touched between one block of products and the next, on the way back of a
+    loop too, or if the last block of a loop does not end with a wait."""
+    found = 0
+    for name, body in re.findall(r"^(_Z\w+):[^\n]*\n(.*?)^\.Lfunc_end", asm, re.S | re.M):
+        lines = body.split("\n")
+        code = [re.sub(r";.*", "", l).strip() if "#ASM" not in l else l.strip() for l in lines]
+        blocks, start = [], None
+        for i, l in enumerate(code):
+            if l.endswith("#ASMSTART"):
+                start = i
+            elif l.endswith("#ASMEND") and any("v_mfma" in x for x in code[start:i]):
+                blocks.append((start, i))
+        found += len(blocks)
+
+        def bad(what, i):
+            raise RuntimeError(f"{src}: {name}: {what}: {lines[i].strip()}")
+
+        for (a, end), nxt in zip(blocks, [*blocks[1:], None]):
+            # as far as the code runs straight on to the next block
+            stop = nxt[0] if nxt else len(code)
+            branch = next((i for i in range(end, stop) if re.match(r"s_c?branch", code[i])), None)
+            for i in range(end + 1, stop if branch is None else branch):
+                if _SUMS.search(code[i]):
+                    bad("a sum is touched between products", i)
+            if branch is None and nxt:
+                continue
+            if not any(x.startswith("s_nop 15") for x in code[a:end]):
+                bad("no wait after the last products", end)
+            label = code[branch].split()[1] + ":" if branch is not None else None
+            if label in code:   # the loop's way back, to its first block
+                back = code.index(label)
+                for i in range(back, next((s for s, _ in blocks if s > back), back)):
+                    if back < end and _SUMS.search(code[i]):
+                        bad("a sum is touched between products", i)
+    if not found:
+        raise RuntimeError(f"{src}: no matrix products in its assembly")
+
+
 def _compile(src):
     obj = os.path.join(BUILD, os.path.basename(src) + ".o")
     checked = src in NO_SCRATCH
@@ -74,10 +124,20 @@ def _compile(src):
         raise RuntimeError(f"hipcc failed for {src}:\n{' '.join(cmd)}\n{r.stderr}")
     if checked:
         check_no_scratch(src, r.stderr)
+    if src in ASM_PRODUCTS:
+        check_products(src, _assembly(src))
     # the host pass warns about the device-only target feature; drop that noise
     msgs = [l for l in r.stderr.splitlines() if "packed-fp32-ops" not in l
             and "not a recognized feature" not in l and REPORT not in l]
     return obj, "\n".join(msgs)
+
+
+def _assembly(src):
+    cmd = [HIPCC, *[f for f in FLAGS if f != "-fPIC"], "--cuda-device-only", "-S", os.path.join(CSRC, src), "-o", "-"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"hipcc failed for {src}:\n{' '.join(cmd)}\n{r.stderr}")
+    return r.stdout
 
 
 def build(verbose=False, jobs=None):

@@ -263,6 +263,16 @@ struct Operands {
 };
 #define QMM_LD(d, p, o) "ds_read_b128 %[" #d "], %[" #p "] offset:" #o "\n\t"
 #define QMM_MM(i, j) "v_mfma_i32_32x32x32_i8 %[c" #i #j "], %[a" #i "], %[b" #j "], %[c" #i #j "]\n\t"
+// The compiler does not see the products and leaves no cycles around them: it
+// would give them 2 between a write of an operand and the product, with which
+// each block therefore begins, and 12 before a result is read or moved. Where no
+// further block follows (left is 0) the block itself ends with more than that;
+// between blocks nothing but the next one touches the sums, which the build
+// checks.
+#define QMM_BEGIN "s_nop 1\n\t"
+#define QMM_SETTLE                                                    \
+  "s_cmp_lg_u32 %[left], 0\n\ts_cbranch_scc1 .Lgo%=\n\t"            \
+  "s_nop 15\n\ts_nop 15\n.Lgo%=:"
 __device__ __forceinline__ void read_operands(uint32_t pa, uint32_t pb, Operands<2>& n) {
   asm volatile(QMM_LD(na0, pa, 0) QMM_LD(nb0, pb, 0) QMM_LD(na1, pa, 4096) QMM_LD(nb1, pb, 4096)
                "s_waitcnt lgkmcnt(0)"
@@ -279,45 +289,50 @@ __device__ __forceinline__ void read_operands(uint32_t pa, uint32_t pb, Operands
                : [pa] "v"(pa), [pb] "v"(pb)
                : "memory");
 }
+// LAST: of a step; `left` steps follow
+#define QMM_MULTIPLY_READ(body, sums, next, operands)                                             \
+  if constexpr (LAST)                                                                             \
+    asm volatile(QMM_BEGIN body "s_waitcnt lgkmcnt(0)\n\t" QMM_SETTLE                            \
+                 : sums, next : operands, [pa] "v"(pa), [pb] "v"(pb), [left] "s"(left)             \
+                 : "memory", "scc");                                                              \
+  else                                                                                            \
+    asm volatile(QMM_BEGIN body "s_waitcnt lgkmcnt(0)"                                            \
+                 : sums, next : operands, [pa] "v"(pa), [pb] "v"(pb) : "memory")
+#define QMM_LIST(...) __VA_ARGS__
+template <bool LAST>
 __device__ __forceinline__ void multiply_read(int16v_t (&c)[2][2], const Operands<2>& u,
-                                              uint32_t pa, uint32_t pb, Operands<2>& n) {
-  asm volatile(QMM_MM(0, 0) QMM_LD(na0, pa, 0) QMM_LD(nb0, pb, 0)
-               QMM_MM(0, 1) QMM_LD(na1, pa, 4096) QMM_LD(nb1, pb, 4096)
-               QMM_MM(1, 0) QMM_MM(1, 1) "s_waitcnt lgkmcnt(0)"
-               : [c00] "+a"(c[0][0]), [c01] "+a"(c[0][1]), [c10] "+a"(c[1][0]), [c11] "+a"(c[1][1]),
-                 [na0] "=&v"(n.a[0]), [na1] "=&v"(n.a[1]), [nb0] "=&v"(n.b[0]), [nb1] "=&v"(n.b[1])
-               : [a0] "v"(u.a[0]), [a1] "v"(u.a[1]), [b0] "v"(u.b[0]), [b1] "v"(u.b[1]),
-                 [pa] "v"(pa), [pb] "v"(pb)
-               : "memory");
+                                              uint32_t pa, uint32_t pb, Operands<2>& n, int left) {
+  QMM_MULTIPLY_READ(
+      QMM_MM(0, 0) QMM_LD(na0, pa, 0) QMM_LD(nb0, pb, 0)
+      QMM_MM(0, 1) QMM_LD(na1, pa, 4096) QMM_LD(nb1, pb, 4096)
+      QMM_MM(1, 0) QMM_MM(1, 1),
+      QMM_LIST([c00] "+a"(c[0][0]), [c01] "+a"(c[0][1]), [c10] "+a"(c[1][0]), [c11] "+a"(c[1][1])),
+      QMM_LIST([na0] "=&v"(n.a[0]), [na1] "=&v"(n.a[1]), [nb0] "=&v"(n.b[0]), [nb1] "=&v"(n.b[1])),
+      QMM_LIST([a0] "v"(u.a[0]), [a1] "v"(u.a[1]), [b0] "v"(u.b[0]), [b1] "v"(u.b[1])));
 }
+template <bool LAST>
 __device__ __forceinline__ void multiply_read(int16v_t (&c)[4][4], const Operands<4>& u,
-                                              uint32_t pa, uint32_t pb, Operands<4>& n) {
-  asm volatile(QMM_MM(0, 0) QMM_LD(na0, pa, 0) QMM_MM(0, 1) QMM_LD(nb0, pb, 0)
-               QMM_MM(0, 2) QMM_LD(nb1, pb, 4096) QMM_MM(0, 3) QMM_LD(nb2, pb, 8192)
-               QMM_MM(1, 0) QMM_LD(nb3, pb, 12288) QMM_MM(1, 1) QMM_LD(na1, pa, 4096)
-               QMM_MM(1, 2) QMM_LD(na2, pa, 8192) QMM_MM(1, 3) QMM_LD(na3, pa, 12288)
-               QMM_MM(2, 0) QMM_MM(2, 1) QMM_MM(2, 2) QMM_MM(2, 3)
-               QMM_MM(3, 0) QMM_MM(3, 1) QMM_MM(3, 2) QMM_MM(3, 3) "s_waitcnt lgkmcnt(0)"
-               : [c00] "+a"(c[0][0]), [c01] "+a"(c[0][1]), [c02] "+a"(c[0][2]), [c03] "+a"(c[0][3]),
-                 [c10] "+a"(c[1][0]), [c11] "+a"(c[1][1]), [c12] "+a"(c[1][2]), [c13] "+a"(c[1][3]),
-                 [c20] "+a"(c[2][0]), [c21] "+a"(c[2][1]), [c22] "+a"(c[2][2]), [c23] "+a"(c[2][3]),
-                 [c30] "+a"(c[3][0]), [c31] "+a"(c[3][1]), [c32] "+a"(c[3][2]), [c33] "+a"(c[3][3]),
-                 [na0] "=&v"(n.a[0]), [na1] "=&v"(n.a[1]), [na2] "=&v"(n.a[2]), [na3] "=&v"(n.a[3]),
-                 [nb0] "=&v"(n.b[0]), [nb1] "=&v"(n.b[1]), [nb2] "=&v"(n.b[2]), [nb3] "=&v"(n.b[3])
-               : [a0] "v"(u.a[0]), [a1] "v"(u.a[1]), [a2] "v"(u.a[2]), [a3] "v"(u.a[3]),
-                 [b0] "v"(u.b[0]), [b1] "v"(u.b[1]), [b2] "v"(u.b[2]), [b3] "v"(u.b[3]),
-                 [pa] "v"(pa), [pb] "v"(pb)
-               : "memory");
+                                              uint32_t pa, uint32_t pb, Operands<4>& n, int left) {
+  QMM_MULTIPLY_READ(
+      QMM_MM(0, 0) QMM_LD(na0, pa, 0) QMM_MM(0, 1) QMM_LD(nb0, pb, 0)
+      QMM_MM(0, 2) QMM_LD(nb1, pb, 4096) QMM_MM(0, 3) QMM_LD(nb2, pb, 8192)
+      QMM_MM(1, 0) QMM_LD(nb3, pb, 12288) QMM_MM(1, 1) QMM_LD(na1, pa, 4096)
+      QMM_MM(1, 2) QMM_LD(na2, pa, 8192) QMM_MM(1, 3) QMM_LD(na3, pa, 12288)
+      QMM_MM(2, 0) QMM_MM(2, 1) QMM_MM(2, 2) QMM_MM(2, 3)
+      QMM_MM(3, 0) QMM_MM(3, 1) QMM_MM(3, 2) QMM_MM(3, 3),
+      QMM_LIST([c00] "+a"(c[0][0]), [c01] "+a"(c[0][1]), [c02] "+a"(c[0][2]), [c03] "+a"(c[0][3]),
+               [c10] "+a"(c[1][0]), [c11] "+a"(c[1][1]), [c12] "+a"(c[1][2]), [c13] "+a"(c[1][3]),
+               [c20] "+a"(c[2][0]), [c21] "+a"(c[2][1]), [c22] "+a"(c[2][2]), [c23] "+a"(c[2][3]),
+               [c30] "+a"(c[3][0]), [c31] "+a"(c[3][1]), [c32] "+a"(c[3][2]), [c33] "+a"(c[3][3])),
+      QMM_LIST([na0] "=&v"(n.a[0]), [na1] "=&v"(n.a[1]), [na2] "=&v"(n.a[2]), [na3] "=&v"(n.a[3]),
+               [nb0] "=&v"(n.b[0]), [nb1] "=&v"(n.b[1]), [nb2] "=&v"(n.b[2]), [nb3] "=&v"(n.b[3])),
+      QMM_LIST([a0] "v"(u.a[0]), [a1] "v"(u.a[1]), [a2] "v"(u.a[2]), [a3] "v"(u.a[3]),
+               [b0] "v"(u.b[0]), [b1] "v"(u.b[1]), [b2] "v"(u.b[2]), [b3] "v"(u.b[3])));
 }
-// the products' results may be read: the compiler does not see them in the
-// assembly and would not leave the cycles that they need
-template <int R>
-__device__ __forceinline__ void settle(int16v_t (&c)[R][R]) {
-#pragma unroll
-  for (int i = 0; i < R; i++)
-#pragma unroll
-    for (int j = 0; j < R; j++) asm volatile("s_nop 15\n\ts_nop 15" : "+a"(c[i][j]));
-}
+#undef QMM_LIST
+#undef QMM_MULTIPLY_READ
+#undef QMM_SETTLE
+#undef QMM_BEGIN
 #undef QMM_LD
 #undef QMM_MM
 
@@ -398,21 +413,17 @@ __global__ __launch_bounds__(64 * WM * WN, BM * BN == 65536 || NS > 2 ? 1 : 2) v
   read_operands(at_w + piece(0), at_x + piece(0), u[0]);
   int slot = 0;
   for (int step = 0; step < steps; step++) {
-#pragma unroll
-    for (int ks = 0; ks < 4; ks++) {
-      const int from = slot;
-      if (ks == 3) {
-        // every wavefront has read the last piece of this step's slot, and this
-        // wavefront's copies of the next step have landed
-        ring_wait<(NS - 2) * kLoads>();
-        copy(step + NS, from);
-        slot = from + kSlot < NS * kSlot ? from + kSlot : 0;
-      }
-      const uint32_t p = (uint32_t)slot + piece((ks + 1) % 4);
-      multiply_read(acc, u[ks % 2], at_w + p, at_x + p, u[(ks + 1) % 2]);
-    }
+    auto next = [&](int ks) QMM_INLINE { return (uint32_t)slot + piece(ks); };
+    multiply_read<false>(acc, u[0], at_w + next(1), at_x + next(1), u[1], 0);
+    multiply_read<false>(acc, u[1], at_w + next(2), at_x + next(2), u[0], 0);
+    multiply_read<false>(acc, u[0], at_w + next(3), at_x + next(3), u[1], 0);
+    // every wavefront has read the last piece of this step's slot, and this
+    // wavefront's copies of the next step have landed
+    ring_wait<(NS - 2) * kLoads>();
+    copy(step + NS, slot);
+    slot = slot + kSlot < NS * kSlot ? slot + kSlot : 0;
+    multiply_read<true>(acc, u[1], at_w + next(0), at_x + next(0), u[0], steps - 1 - step);
   }
-  settle(acc);
   __builtin_amdgcn_s_waitcnt(0);   // no copy is left in flight when LDS is given up
 
   // acc[i][j][e]: n = n0 + 32 * (wn * TN + i) + 8 * (e / 4) + 4 * lh + e % 4,

@@ -36,3 +36,44 @@ def test_no_report_fails_the_build(text):
 
 def test_the_attention_is_checked():
     assert "kv8_attn.hip" in build.NO_SCRATCH and build.NO_SCRATCH <= set(build.SOURCES)
+
+
+BLOCK = """\t;;#ASMSTART
+\ts_nop 1
+\tv_mfma_i32_32x32x32_i8 a[0:15], v[2:5], v[6:9], a[0:15]
+\ts_waitcnt lgkmcnt(0)
+%s\t;;#ASMEND
+"""
+PLAIN = BLOCK % ""
+LAST = BLOCK % "\ts_cmp_lg_u32 s8, 0\n\ts_cbranch_scc1 .Lgo1\n\ts_nop 15\n\ts_nop 15\n.Lgo1:\n"
+ADDRESS = "\tv_add_u32_e32 v44, 1, v45   ; a0 is not meant\n"
+MOVE = "\tv_accvgpr_read_b32 v2, a0\n"
+STORE = "\tglobal_store_dwordx4 v[0:1], a[0:3], off\n"
+
+
+def kernel(before="\tv_accvgpr_write_b32 a0, 0\n", top=ADDRESS, between=ADDRESS, last=LAST, tail="\ts_add_i32 s8, s8, -1\n",
+           after=MOVE):
+    return ("_Z4kernv:   ; @_Z4kernv\n" + before + ".LBB0_1:\n" + top + PLAIN + between + last + tail +
+            "\ts_cbranch_scc1 .LBB0_1\n" + after + "\ts_endpgm\n.Lfunc_end0:\n")
+
+
+def test_products_in_assembly_pass():
+    build.check_products("i8.hip", kernel())
+
+
+@pytest.mark.parametrize("where", ["top", "between", "tail"])
+@pytest.mark.parametrize("what", [MOVE, STORE])
+def test_a_sum_touched_between_products_fails_the_build(where, what):
+    with pytest.raises(RuntimeError, match="between products"):
+        build.check_products("i8.hip", kernel(**{where: what}))
+
+
+def test_products_without_a_wait_fail_the_build():
+    with pytest.raises(RuntimeError, match="no wait"):
+        build.check_products("i8.hip", kernel(last=PLAIN))
+    with pytest.raises(RuntimeError, match="no matrix products"):
+        build.check_products("i8.hip", kernel().replace("v_mfma", "v_add"))
+
+
+def test_the_tile_product_is_checked():
+    assert "i8.hip" in build.ASM_PRODUCTS and build.ASM_PRODUCTS <= set(build.SOURCES)

@@ -11,10 +11,8 @@
 // Both products run on the f16 matrix units: codes are exact in f16, queries
 // too (bf16 rows are first scaled by a power of two), so only the weights
 // exp(x - m) * vs are rounded on their way into the second product, relative
-// to the row's largest: to two f16 terms, and to one (11 bits) for the bf16
-// results of prompts, which rounding to 8 bits follows and where the second
-// product costs a quarter of the time. Sums, maxima and the normaliser stay in
-// fp32.
+// to the row's largest (to 11 bits for bf16 results, to two f16 terms for f16
+// ones); sums, maxima and the normaliser stay in fp32.
 #include "kernels.hpp"
 #include "kv8_common.hpp"
 
@@ -147,6 +145,9 @@ constexpr int kPart = R * (D + 2);
 template <class T, int D, int BT, int NW>   // pages of 1 << BT tokens
 __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : D == 128 ? 2 : 3) void kv8_decode_kernel(AttnArgs a) {
   constexpr int KD = D / 64, VD = D / 16;
+  // f16 results: the weights go in as two f16 terms, since 11 bits of them would
+  // cost as much as rounding the result
+  constexpr bool kTwo = __is_same(T, F16);
   const int tid = threadIdx.x, lane = tid % 64;
   const int wave = __builtin_amdgcn_readfirstlane(tid / 64);   // uniform: scalar
   const int col = lane % 16, g = lane / 16;
@@ -334,15 +335,15 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : D == 128 ? 2 : 3) void kv8_
       for (int i = 0; i < 8; i++) {
         const float e = __builtin_amdgcn_exp2f(p[8 * h + i] - at.base);
         l_run += e;
-        const float w = e * r;   // two terms: the codes' loads leave time for both
+        const float w = e * r;
         pf[i] = (_Float16)w;
-        pl[i] = (_Float16)(w - (float)pf[i]);
+        if constexpr (kTwo) pl[i] = (_Float16)(w - (float)pf[i]);
       }
 #pragma unroll
       for (int i = 0; i < VD; i++) {
         const half8_t vf = codes_f16(vw[i][2 * h], vw[i][2 * h + 1]);
         o[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, pf, o[i], 0, 0, 0);
-        o[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, pl, o[i], 0, 0, 0);
+        if constexpr (kTwo) o[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, pl, o[i], 0, 0, 0);
         if (i % 2 == 1) __builtin_amdgcn_sched_barrier(0);
       }
     }

@@ -546,10 +546,8 @@ qmm_status qmm_kv8_read(const qmm_kv8_cache* cache, const int32_t* pages, int64_
  * wanted) the natural logarithm of the sum of exponentials of the scores. A
  * query that sees nothing gets 0 and -inf. Sums, maxima and the normaliser
  * are held in fp32. The weights exp(score) * v scale enter the matrix product
- * with the codes relative to the row's largest, with 22 bits (11 for the bf16
- * results of sequences with more than 64 query rows per cache head), below
- * 2^-14 of the largest to 2^-25 of it. bf16 queries are exact down to 2^-14 of
- * their row's largest value, smaller ones to 2^-25 of it.
+ * with the codes relative to the row's largest: with 11 bits for bf16 results
+ * and 22 for f16 ones, below 2^-14 of the largest to 2^-25 of it.
  */
 int64_t qmm_kv8_attention_work(const qmm_kv8_cache* cache, int64_t T, int64_t q_heads, int64_t S,
                                int64_t W);

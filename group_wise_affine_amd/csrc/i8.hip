@@ -220,8 +220,8 @@ __global__ __launch_bounds__(64 * NW) void i8_gemv_kernel(
 // a slot row r's 16-byte piece c sits at position c ^ (r / 2 & 7), so the 16
 // rows that are read together touch all banks. W is the A operand, so a lane
 // ends up with runs of four consecutive n of one row of y.
-// Bound by the matrix units and the clock that their power leaves (1.65 to 1.75
-// GHz): 8192 x 8192 x 4096 in 275 to 290 us, 1.9 to 2.0 Pop/s, 16384 x 8192 x
+// Bound by the matrix units and the clock that their power leaves (1.65 to 1.9
+// GHz): 8192 x 8192 x 4096 in 268 to 290 us, 1.9 to 2.05 Pop/s, 16384 x 8192 x
 // 8192 in 990, 2.2; the library's product of 8192^3 reaches 2.04. Small tiles, whose
 // wavefronts share less, are bound by LDS: 777 x 2050 x 8192 in 31 us, two parts of
 // K, of which a third is the exchange of the parts (a ticket and a wait in place

@@ -11,7 +11,7 @@ namespace {
 // when the page holds earlier tokens; the earlier codes are then brought to
 // the new scale, rint(fl32(fl32(c * old) / new)). Slots behind the last token
 // become zero. Bound by memory: new values are read once, codes written once
-// (30005 tokens of 8 x 128, f16: 31 us, 3.9 TB/s; 64 single tokens: 7 us, the
+// (20278 tokens of 8 x 128, f16: 31 us, 4.0 TB/s; 64 single tokens: 7 us, the
 // chain of loads from the sequence to the page's old codes).
 //
 // A thread's unit is 4 slots by 8 columns of the keys or of the values: four
@@ -163,7 +163,7 @@ __global__ __launch_bounds__(256) void kv8_append_kernel(Kv8 c, Kv8Seqs q,
 
 // --------------------------------------------------------------------- read
 // One workgroup per (listed page, head): T(fl32(scale * code)) as [B][D]. Bound by
-// memory (30016 tokens of 8 x 128: 21 us).
+// memory (20352 tokens of 8 x 128: 21 us).
 template <class T>
 __global__ __launch_bounds__(256) void kv8_read_kernel(Kv8 c, const int32_t* __restrict__ pages,
                                                        uint16_t* __restrict__ ko,

@@ -581,11 +581,15 @@ __device__ __forceinline__ int longest_first(const AttnArgs& a, int rank, int it
 // than 2^8: until then weights reach 256, which f16 and the fp32 sums hold as
 // well, and nothing is rescaled.
 //
-// Bound: the vector unit (conversions, exponentials, maxima: 60 % of the cycles)
-// and after it the matrix unit (35 %); 725 to 790 TFLOP/s of visible
-// pairs for D = 128 in bf16, 600 in f16 (two products per value), 545 and 580 for
-// D = 64 and 256. Eight wavefronts that share a tile, and two groups of wavefronts
-// of which one multiplies while the other weighs, took the same time.
+// Bound: the vector unit (conversions, exponentials, maxima: 61 % of the cycles)
+// and after it the matrix unit (34 %). Of visible pairs, four chunks of 2048 tokens
+// behind 3952, 8 heads of 4: 760 to 805 TFLOP/s for D = 128 in bf16, 600 to 635 in
+// f16 (two products per value), 655 and 485 for D = 64; 580 and 505 for D = 256
+// (two chunks of 1024 behind 4976). Eight wavefronts that share a tile, and two
+// groups of wavefronts of which one multiplies while the other weighs, took the
+// same time. The references of the weights and of the sum that follow each row by
+// itself cost 2 % (822 us, 806 with the largest value scale of a tile as the only
+// one, which loses bits: four chunks of up to 2048 tokens behind up to 8000).
 //
 // No variant may need scratch memory: the compiler has put the stores of
 // spilled registers between a branch that some lanes take and its end, where the
@@ -790,7 +794,8 @@ __global__ __launch_bounds__(2 * kPromptRows, D == 256 ? 1 : 2) void kv8_prompt_
         o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, hi, o[i], 0, 0, 0);
         if constexpr (kTwo) o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, lo, o[i], 0, 0, 0);
       }
-      // (operands of the product after next are asked for before the present one)
+      // (operands of the product after next are asked for before the present one,
+      // for which the compiler finds no registers by itself: 634 us, 725 without)
       if constexpr (D == 256) {
         __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
 #pragma unroll

@@ -472,7 +472,8 @@ qmm_status qmm_i8_quantize(const void* x, int64_t ldx, qmm_dtype dt, int64_t row
  * with codes xq [M, K], wq [N, K], fp32 scales sx [M] (tokens), sw [N]
  * (channels) and an optional bias [N] in dt (NULL: none). The integer sum is
  * exact; scales, bias and the one rounding to dt follow in fp32. A GEMV up to
- * 64 rows, an MFMA tile kernel beyond. xq, wq and y 16-byte aligned.
+ * 64 rows and, where there is little to do, up to 8192; an MFMA tile kernel
+ * beyond. xq, wq and y 16-byte aligned.
  */
 int64_t qmm_i8_t_work(int64_t M, int64_t N, int64_t K);
 qmm_status qmm_i8_t(const int8_t* xq, const float* sx, const int8_t* wq, const float* sw,
@@ -547,7 +548,9 @@ qmm_status qmm_kv8_read(const qmm_kv8_cache* cache, const int32_t* pages, int64_
  * query that sees nothing gets 0 and -inf. Sums, maxima and the normaliser
  * are held in fp32. The weights exp(score) * v scale enter the matrix product
  * with the codes relative to the row's largest: with 11 bits for bf16 results
- * and 22 for f16 ones, below 2^-14 of the largest to 2^-25 of it.
+ * and 22 for f16 ones, below 2^-14 of the largest to 2^-25 of it. bf16 queries
+ * are exact down to 2^-14 of their row's largest value, smaller ones to 2^-25 of
+ * it.
  */
 int64_t qmm_kv8_attention_work(const qmm_kv8_cache* cache, int64_t T, int64_t q_heads, int64_t S,
                                int64_t W);

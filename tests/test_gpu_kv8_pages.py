@@ -165,3 +165,55 @@ def test_a_block_of_steps_together():
     got = Q.kv8_attention(dev, q, table, i32([41, 0, 41]), cu)
     assert torch.equal(got[0], want[0]) and torch.equal(got[2], want[2])
     assert int(got[1].abs().max()) == 0
+
+
+def test_a_captured_step():
+    """Bookkeeping, append and attention of a step captured together, the pages'
+    scratch on a stream of its own: each replay gives what the eager calls give."""
+    B, D, H, G, P, S, W = 16, 64, 2, 2, 900, 40, 16
+    r = np.random.default_rng(7)
+    lens0 = [int(x) for x in r.integers(1, B * W - 8, S)]
+    table0 = tables(lens0, B, P, 8, W=W)
+    caches = [make(P, H, B, D, 9)[0] for _ in range(2)]
+    state = [dict(ref=i32(counts(table0, P)), table=i32(table0), lens=i32(lens0)) for _ in range(2)]
+    parent, new, cu = i32(list(range(S))), i32([n + 1 for n in lens0]), i32(list(range(S + 1)))
+    kv = torch.zeros(S, 2 * H, D, dtype=torch.float16, device="cuda")
+    q = torch.zeros(S, H * G, D, dtype=torch.float16, device="cuda")
+    side = torch.cuda.Stream()
+
+    def step(c, s, on=None):
+        ref, table, short = Q.kv8_update(c, s["ref"], s["table"], s["lens"], parent, new, stream=on)
+        if on is not None:
+            torch.cuda.current_stream().wait_stream(on)
+        Q.kv8_append(c, kv[:, :H], kv[:, H:], table, new, cu)
+        out = Q.kv8_attention(c, q, table, new, cu)
+        return ref, table, short, out
+
+    step(caches[1], dict(state[1]))   # (before the capture; the cache is set again below)
+    caches[1].k.copy_(caches[0].k), caches[1].v.copy_(caches[0].v)
+    caches[1].k_scales.copy_(caches[0].k_scales), caches[1].v_scales.copy_(caches[0].v_scales)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        side.wait_stream(torch.cuda.current_stream())
+        got = step(caches[1], state[1], on=side)
+    gen = torch.Generator().manual_seed(3)
+    lens = lens0
+    for i in range(4):
+        u = r.random(S)
+        par = [s if x < 0.6 else int(r.integers(S)) for s, x in enumerate(u)]
+        want_lens = [min(lens[p] + 1, B * W) for p in par]
+        parent.copy_(i32(par)), new.copy_(i32(want_lens))
+        kv.copy_(torch.randn(S, 2 * H, D, generator=gen).half()), q.copy_(torch.randn(S, H * G, D, generator=gen).half())
+        want = step(caches[0], state[0])
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert want[2].item() == 0
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+        for s, w in zip(state, (want, got)):
+            s["ref"].copy_(w[0]), s["table"].copy_(w[1]), s["lens"].copy_(new)
+        lens = want_lens
+        for a, b in zip((caches[0].k, caches[0].v, caches[0].k_scales, caches[0].v_scales),
+                        (caches[1].k, caches[1].v, caches[1].k_scales, caches[1].v_scales)):
+            assert torch.equal(a, b)

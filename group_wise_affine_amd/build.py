@@ -30,7 +30,7 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 SOURCES = ["api.cpp", "quantize.hip", "qmv.hip", "qmn.hip", "qmn_tile.hip", "fpq.hip", "apk.hip", "qmv_mfma_f16.hip", "qmv_mfma_bf16.hip", "qmm.hip",
            "tile_gemm_f16.hip", "tile_gemm_bf16.hip", "tile_conv_f16.hip", "tile_conv_bf16.hip",
            "tile_fp.hip", "tile_apk.hip", "api_serving.cpp", "i8.hip", "kv8.hip", "kv8_attn.hip",
-           "kv8_pages.hip"]
+           "kv8_attn_window.hip", "kv8_attn_tree.hip", "kv8_pages.hip", "rope.hip", "logprobs.hip"]
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++20", "-fPIC",
     "-fhip-fp32-correctly-rounded-divide-sqrt", "-fno-fast-math",
@@ -42,7 +42,8 @@ FLAGS = [
 # Sources whose kernels may not use scratch memory: the compiler has put the
 # stores of spilled registers between a branch that some lanes take and its end,
 # so that the other lanes read back what they never stored.
-NO_SCRATCH = {"i8.hip", "kv8.hip", "kv8_attn.hip", "kv8_pages.hip"}
+NO_SCRATCH = {"i8.hip", "kv8.hip", "kv8_attn.hip", "kv8_attn_window.hip", "kv8_attn_tree.hip", "kv8_pages.hip",
+              "rope.hip", "logprobs.hip"}
 REPORT = "-Rpass-analysis=kernel-resource-usage"
 
 

@@ -101,6 +101,33 @@ bool any_null(std::initializer_list<const void*> ps) {
   return false;
 }
 
+// what the calls of the attention have in common; `work` and `go` are the
+// mask's own
+template <class Work, class Go>
+qmm_status attention(const char* tag, const qmm_kv8_cache* cache, const void* q, int64_t ldq,
+                     qmm_dtype dt, int64_t T, int64_t q_heads, const int32_t* table,
+                     const int32_t* lens, const int32_t* cu, int64_t S, int64_t W, void* out,
+                     float* lse, void* work, int64_t work_bytes, void* stream, Work need_of,
+                     Go go) {
+  if (qmm_status s = check_stream(tag, stream)) return s;
+  qmm::Kv8 c;
+  if (qmm_status s = check_cache(tag, cache, &c)) return s;
+  if (any_null({q, table, lens, cu, out}))
+    return fail(QMM_E_NULL, "%s: q, table, lens, cu and out must be non-NULL", tag);
+  if (qmm_status s = check_float(tag, dt)) return s;
+  if (qmm_status s = check_batch(tag, T, S, W)) return s;
+  if (q_heads < c.heads || q_heads % c.heads != 0 || q_heads > 65535)
+    return fail(QMM_E_SHAPE, "%s: q_heads (%lld) must be a multiple of the cache's heads (%d)", tag,
+                (long long)q_heads, c.heads);
+  if (T * q_heads > kI32) return fail(QMM_E_SHAPE, "%s: problem too large", tag);
+  if (qmm_status s = check_rows(tag, "q", q, ldq, q_heads * c.dim)) return s;
+  if (!aligned4({table, lens, cu, lse}) || !aligned(out, 16))
+    return fail(QMM_E_ALIGN, "%s: out must be 16-byte aligned, table, lens, cu and lse 4-byte", tag);
+  const int64_t need = need_of(c);
+  if (qmm_status s = check_work(tag, work, work_bytes, need > 0 ? kCounterBytes + need : 0)) return s;
+  return launched(go(c, work ? reinterpret_cast<float*>(past_counters(work)) : nullptr), tag);
+}
+
 }  // namespace
 
 extern "C" {
@@ -235,28 +262,64 @@ qmm_status qmm_kv8_attention(const qmm_kv8_cache* cache, const void* q, int64_t 
                              int64_t T, int64_t q_heads, const int32_t* table, const int32_t* lens,
                              const int32_t* cu, int64_t S, int64_t W, float scale, void* out,
                              float* lse, void* work, int64_t work_bytes, void* stream) {
-  const char* tag = "qmm_kv8_attention";
-  if (qmm_status s = check_stream(tag, stream)) return s;
+  return attention(
+      "qmm_kv8_attention", cache, q, ldq, dt, T, q_heads, table, lens, cu, S, W, out, lse, work,
+      work_bytes, stream,
+      [&](const qmm::Kv8& c) { return qmm::kv8_attention_work(c, T, q_heads, S, W); },
+      [&](const qmm::Kv8& c, float* ws) {
+        return qmm::launch_kv8_attention(c, (int)dt, q, ldq, T, q_heads, table, lens, cu, S, W,
+                                         scale, out, lse, ws, (hipStream_t)stream);
+      });
+}
+
+// positions stay below 2^30, so that a longer window or more sinks see no more
+static int64_t cap30(int64_t n) { return n < ((int64_t)1 << 30) ? n : (int64_t)1 << 30; }
+
+int64_t qmm_kv8_attention_window_work(const qmm_kv8_cache* cache, int64_t T, int64_t q_heads,
+                                      int64_t S, int64_t W, int64_t window, int64_t sinks) {
   qmm::Kv8 c;
-  if (qmm_status s = check_cache(tag, cache, &c)) return s;
-  if (any_null({q, table, lens, cu, out}))
-    return fail(QMM_E_NULL, "%s: q, table, lens, cu and out must be non-NULL", tag);
-  if (qmm_status s = check_float(tag, dt)) return s;
-  if (qmm_status s = check_batch(tag, T, S, W)) return s;
-  if (q_heads < c.heads || q_heads % c.heads != 0 || q_heads > 65535)
-    return fail(QMM_E_SHAPE, "%s: q_heads (%lld) must be a multiple of the cache's heads (%d)", tag,
-                (long long)q_heads, c.heads);
-  if (T * q_heads > kI32) return fail(QMM_E_SHAPE, "%s: problem too large", tag);
-  if (qmm_status s = check_rows(tag, "q", q, ldq, q_heads * c.dim)) return s;
-  if (!aligned4({table, lens, cu, lse}) || !aligned(out, 16))
-    return fail(QMM_E_ALIGN, "%s: out must be 16-byte aligned, table, lens, cu and lse 4-byte", tag);
-  const int64_t need = qmm::kv8_attention_work(c, T, q_heads, S, W);
-  if (qmm_status s = check_work(tag, work, work_bytes, need > 0 ? kCounterBytes + need : 0)) return s;
-  return launched(
-      qmm::launch_kv8_attention(c, (int)dt, q, ldq, T, q_heads, table, lens, cu, S, W, scale, out,
-                                lse, work ? reinterpret_cast<float*>(past_counters(work)) : nullptr,
-                                (hipStream_t)stream),
-      tag);
+  if (check_cache("qmm_kv8_attention_window_work", cache, &c) ||
+      check_batch("qmm_kv8_attention_window_work", T, S, W) || q_heads < c.heads || window < 1 ||
+      sinks < 0)
+    return 0;
+  const int64_t b = qmm::kv8_attention_window_work(c, T, q_heads, S, W, cap30(window), cap30(sinks));
+  return b > 0 ? kCounterBytes + b : 0;
+}
+
+qmm_status qmm_kv8_attention_window(const qmm_kv8_cache* cache, const void* q, int64_t ldq,
+                                    qmm_dtype dt, int64_t T, int64_t q_heads, const int32_t* table,
+                                    const int32_t* lens, const int32_t* cu, int64_t S, int64_t W,
+                                    int64_t window, int64_t sinks, float scale, void* out, float* lse,
+                                    void* work, int64_t work_bytes, void* stream) {
+  const char* tag = "qmm_kv8_attention_window";
+  if (window < 1 || sinks < 0)
+    return fail(QMM_E_ARG, "%s: window (%lld) must be at least 1 and sinks (%lld) at least 0", tag,
+                (long long)window, (long long)sinks);
+  const int64_t w = cap30(window), n = cap30(sinks);
+  return attention(
+      tag, cache, q, ldq, dt, T, q_heads, table, lens, cu, S, W, out, lse, work, work_bytes, stream,
+      [&](const qmm::Kv8& c) { return qmm::kv8_attention_window_work(c, T, q_heads, S, W, w, n); },
+      [&](const qmm::Kv8& c, float* ws) {
+        return qmm::launch_kv8_attention_window(c, (int)dt, q, ldq, T, q_heads, table, lens, cu, S,
+                                                W, w, n, scale, out, lse, ws, (hipStream_t)stream);
+      });
+}
+
+qmm_status qmm_kv8_attention_tree(const qmm_kv8_cache* cache, const void* q, int64_t ldq,
+                                  qmm_dtype dt, int64_t T, int64_t q_heads, const int32_t* table,
+                                  const int32_t* lens, const int32_t* cu, int64_t S, int64_t W,
+                                  const int32_t* parent, float scale, void* out, float* lse,
+                                  void* work, int64_t work_bytes, void* stream) {
+  const char* tag = "qmm_kv8_attention_tree";
+  if (!parent) return fail(QMM_E_NULL, "%s: parent must be non-NULL", tag);
+  if (!aligned(parent, 4)) return fail(QMM_E_ALIGN, "%s: parent must be 4-byte aligned", tag);
+  return attention(
+      tag, cache, q, ldq, dt, T, q_heads, table, lens, cu, S, W, out, lse, work, work_bytes, stream,
+      [&](const qmm::Kv8& c) { return qmm::kv8_attention_work(c, T, q_heads, S, W); },
+      [&](const qmm::Kv8& c, float* ws) {
+        return qmm::launch_kv8_attention_tree(c, (int)dt, q, ldq, T, q_heads, table, lens, cu, S, W,
+                                              parent, scale, out, lse, ws, (hipStream_t)stream);
+      });
 }
 
 int64_t qmm_kv8_pages_work(int64_t pages) {
@@ -320,6 +383,91 @@ qmm_status qmm_kv8_copy(const qmm_kv8_cache* to, const int32_t* dst, const qmm_k
   if (n < 1 || n > kI32) return fail(QMM_E_SHAPE, "%s: n (%lld) must be in [1, 2^31)", tag, (long long)n);
   if (!aligned4({dst, src})) return fail(QMM_E_ALIGN, "%s: dst and src must be 4-byte aligned", tag);
   return launched(qmm::launch_kv8_copy(a, b, dst, src, n, (hipStream_t)stream), tag);
+}
+
+qmm_status qmm_qk_norm_rope(const void* q, int64_t ldq, const void* k, int64_t ldk, qmm_dtype dt,
+                            int64_t T, int64_t q_heads, int64_t k_heads, int64_t head_dim,
+                            const int32_t* positions, const float* inv_freq, int64_t rot_dim,
+                            int interleaved, const void* q_weight, const void* k_weight, float eps,
+                            void* q_out, int64_t ldqo, void* k_out, int64_t ldko, void* stream) {
+  const char* tag = "qmm_qk_norm_rope";
+  if (qmm_status s = check_stream(tag, stream)) return s;
+  if (any_null({q, k, positions, inv_freq, q_out, k_out}))
+    return fail(QMM_E_NULL, "%s: q, k, positions, inv_freq, q_out and k_out must be non-NULL", tag);
+  if (qmm_status s = check_float(tag, dt)) return s;
+  if (T < 1 || T > (1 << 24))
+    return fail(QMM_E_SHAPE, "%s: tokens (%lld) must be in [1, 2^24]", tag, (long long)T);
+  if (q_heads < 1 || k_heads < 1 || q_heads > 65535 || k_heads > 65535)
+    return fail(QMM_E_SHAPE, "%s: q_heads (%lld) and k_heads (%lld) must be in [1, 65535]", tag,
+                (long long)q_heads, (long long)k_heads);
+  if (head_dim < 8 || head_dim > 512 || head_dim % 8 != 0 || rot_dim < 8 || rot_dim > head_dim ||
+      rot_dim % 8 != 0)
+    return fail(QMM_E_SHAPE,
+                "%s: head_dim (%lld) must be a multiple of 8 up to 512, rot_dim (%lld) one up to "
+                "head_dim",
+                tag, (long long)head_dim, (long long)rot_dim);
+  if (T * (q_heads + k_heads) > kI32) return fail(QMM_E_SHAPE, "%s: problem too large", tag);
+  const int64_t wide_q = q_heads * head_dim, wide_k = k_heads * head_dim;
+  if (qmm_status s = check_rows(tag, "q", q, ldq, wide_q)) return s;
+  if (qmm_status s = check_rows(tag, "k", k, ldk, wide_k)) return s;
+  if (qmm_status s = check_rows(tag, "q_out", q_out, ldqo, wide_q)) return s;
+  if (qmm_status s = check_rows(tag, "k_out", k_out, ldko, wide_k)) return s;
+  if (!aligned(inv_freq, 16) || !aligned(q_weight, 16) || !aligned(k_weight, 16) ||
+      !aligned(positions, 4))
+    return fail(QMM_E_ALIGN, "%s: inv_freq and weights must be 16-byte aligned, positions 4-byte",
+                tag);
+  if (!(eps >= 0.0f)) return fail(QMM_E_ARG, "%s: eps must not be negative", tag);
+  if ((q_out == q && ldqo != ldq) || (k_out == k && ldko != ldk) || q_out == k || k_out == q ||
+      q_out == k_out)
+    return fail(QMM_E_ARG,
+                "%s: an output may be its own input with the same stride, and no other array", tag);
+  return launched(qmm::launch_qk_norm_rope((int)dt, q, ldq, k, ldk, T, q_heads, k_heads, head_dim,
+                                           positions, inv_freq, rot_dim, interleaved != 0, q_weight,
+                                           k_weight, eps, q_out, ldqo, k_out, ldko,
+                                           (hipStream_t)stream),
+                  tag);
+}
+
+static bool logprobs_sizes(qmm_dtype dt, int64_t M, int64_t V, int64_t top) {
+  return (dt == QMM_F16 || dt == QMM_BF16 || dt == QMM_F32) && M >= 1 && M <= (1 << 24) && V >= 1 &&
+         V <= (1 << 30) && top >= 0 && top <= 64 && top <= V;
+}
+
+int64_t qmm_logprobs_work(qmm_dtype dt, int64_t M, int64_t V, int64_t top) {
+  if (!logprobs_sizes(dt, M, V, top)) return 0;
+  const int64_t b = qmm::logprobs_work((int)dt, M, V, top);
+  return b > 0 ? kCounterBytes + b : 0;
+}
+
+qmm_status qmm_logprobs(const void* logits, int64_t ld, qmm_dtype dt, int64_t M, int64_t V,
+                        const int32_t* tokens, int64_t top, float* logprob, float* entropy,
+                        int32_t* top_ids, float* top_logprobs, void* work, int64_t work_bytes,
+                        void* stream) {
+  const char* tag = "qmm_logprobs";
+  if (qmm_status s = check_stream(tag, stream)) return s;
+  if (any_null({logits, tokens, logprob, entropy}) || (top > 0 && any_null({top_ids, top_logprobs})))
+    return fail(QMM_E_NULL,
+                "%s: logits, tokens, logprob and entropy (with top > 0 also top_ids and "
+                "top_logprobs) must be non-NULL",
+                tag);
+  if (dt != QMM_F16 && dt != QMM_BF16 && dt != QMM_F32)
+    return fail(QMM_E_DTYPE, "%s: only float16, bfloat16 and float32 are supported (got dtype %d)",
+                tag, (int)dt);
+  if (!logprobs_sizes(dt, M, V, top))
+    return fail(QMM_E_SHAPE,
+                "%s: rows (%lld) must be in [1, 2^24], V (%lld) in [1, 2^30], top (%lld) in [0, 64] "
+                "and at most V",
+                tag, (long long)M, (long long)V, (long long)top);
+  if (ld < V)
+    return fail(QMM_E_SHAPE, "%s: the row stride (%lld) must not be below V", tag, (long long)ld);
+  if (!aligned(logits, elem_bytes(dt)) ||
+      !aligned4({tokens, logprob, entropy, top_ids, top_logprobs}))
+    return fail(QMM_E_ALIGN, "%s: logits must be aligned to their type, the others 4-byte", tag);
+  if (qmm_status s = check_work(tag, work, work_bytes, qmm_logprobs_work(dt, M, V, top))) return s;
+  return launched(qmm::launch_logprobs((int)dt, logits, ld, M, V, tokens, top, logprob, entropy,
+                                       top_ids, top_logprobs, work ? past_counters(work) : nullptr,
+                                       (hipStream_t)stream),
+                  tag);
 }
 
 }  // extern "C"

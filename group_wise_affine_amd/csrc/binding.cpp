@@ -305,34 +305,146 @@ PyObject* kv8_read(PyObject* const* a) {
   return tuple(k, v);
 }
 
-// kv8_attention(cache, its tensors, q, table, lens, cu, scale | None, out | None, lse wanted, stream)
-PyObject* kv8_attention(PyObject* const* a) {
+// What the calls of the attention have in common: arguments (cache, its tensors,
+// q, table, lens, cu, the mask's own, scale | None, out | None, lse wanted, stream),
+// of which `rest` are those from the scale on. work() says the scratch bytes, go()
+// makes the call.
+struct Queries {
+  Cache c;
+  const Tensor& q;
+  int64_t T, H, ld;
+  qmm_dtype dt;
+  Batch b;
+};
+Queries queries(PyObject* const* a) {
   const Cache c = cache(a[0], a[1]);
   const Tensor& q = new_rows(a[2], "q", 0, c.c->head_dim);
-  const int64_t T = q.size(0), Hq = q.size(1), D = q.size(2), ld = rows(q, "q");
-  const qmm_dtype dt = element(q.scalar_type());
-  const Batch b = batch(a[3], a[4], a[5]);
+  const int64_t ld = rows(q, "q");
+  return {c, q, q.size(0), q.size(1), ld, element(q.scalar_type()), batch(a[3], a[4], a[5])};
+}
+template <class Work, class Go>
+PyObject* attention(const Queries& x, PyObject* const* rest, const Tensor* parent, Work work, Go go) {
+  const int64_t D = x.q.size(2);
   double scale = 1.0 / std::sqrt((double)D);
-  if (!none(a[6])) {
-    scale = PyFloat_AsDouble(a[6]);
+  if (!none(rest[0])) {
+    scale = PyFloat_AsDouble(rest[0]);
     if (PyErr_Occurred()) throw Failed();
   }
   Tensor out, lse;
-  if (none(a[7])) {
-    on_gpu(q, "q");
-    out = at::empty({T, Hq, D}, q.options());
+  if (none(rest[1])) {
+    on_gpu(x.q, "q");
+    out = at::empty({x.T, x.H, D}, x.q.options());
   } else {
-    out = exact(a[7], "out", {T, Hq, D}, q.scalar_type());
+    out = exact(rest[1], "out", {x.T, x.H, D}, x.q.scalar_type());
   }
-  const bool want = PyObject_IsTrue(a[8]);
-  const Place p = place(a[9], {{c.k, "cache"}, {&q, "q"}, {b.table, "table"}, {b.lens, "lens"}, {b.cu, "cu"}, {&out, "out"}});
-  if (want) lse = at::empty({T, Hq}, q.options().dtype(at::kFloat));
-  const Scratch w = scratch(qmm_kv8_attention_work(c.c, T, Hq, b.S, b.W), p);
-  check(qmm_kv8_attention(c.c, q.data_ptr(), ld, dt, T, Hq, ints(*b.table), ints(*b.lens), ints(*b.cu), b.S, b.W,
-                          (float)scale, out.data_ptr(), want ? static_cast<float*>(lse.data_ptr()) : nullptr, w.p,
-                          w.bytes, p.st));
+  const bool want = PyObject_IsTrue(rest[2]);
+  const Place p = place(rest[3], {{x.c.k, "cache"}, {&x.q, "q"}, {x.b.table, "table"}, {x.b.lens, "lens"}, {x.b.cu, "cu"}, {parent, "parent"}, {&out, "out"}});
+  if (want) lse = at::empty({x.T, x.H}, x.q.options().dtype(at::kFloat));
+  const Scratch w = scratch(work(), p);
+  check(go((float)scale, out.data_ptr(), want ? static_cast<float*>(lse.data_ptr()) : nullptr, w, p.st));
   if (!want) return THPVariable_Wrap(out);
   return tuple(out, lse);
+}
+
+// kv8_attention(cache, its tensors, q, table, lens, cu, scale | None, out | None, lse wanted, stream)
+PyObject* kv8_attention(PyObject* const* a) {
+  const Queries x = queries(a);
+  return attention(
+      x, a + 6, nullptr, [&] { return qmm_kv8_attention_work(x.c.c, x.T, x.H, x.b.S, x.b.W); },
+      [&](float scale, void* out, float* lse, const Scratch& w, hipStream_t st) {
+        return qmm_kv8_attention(x.c.c, x.q.data_ptr(), x.ld, x.dt, x.T, x.H, ints(*x.b.table), ints(*x.b.lens),
+                                 ints(*x.b.cu), x.b.S, x.b.W, scale, out, lse, w.p, w.bytes, st);
+      });
+}
+
+int64_t whole(PyObject* o) {
+  const int64_t v = PyLong_AsLongLong(o);
+  if (PyErr_Occurred()) throw Failed();
+  return v;
+}
+
+// kv8_attention_window(cache, its tensors, q, table, lens, cu, window, sinks, scale | None, out | None, lse wanted, stream)
+PyObject* kv8_attention_window(PyObject* const* a) {
+  const Queries x = queries(a);
+  const int64_t window = whole(a[6]), sinks = whole(a[7]);
+  return attention(
+      x, a + 8, nullptr,
+      [&] { return qmm_kv8_attention_window_work(x.c.c, x.T, x.H, x.b.S, x.b.W, window, sinks); },
+      [&](float scale, void* out, float* lse, const Scratch& w, hipStream_t st) {
+        return qmm_kv8_attention_window(x.c.c, x.q.data_ptr(), x.ld, x.dt, x.T, x.H, ints(*x.b.table),
+                                        ints(*x.b.lens), ints(*x.b.cu), x.b.S, x.b.W, window, sinks, scale, out, lse,
+                                        w.p, w.bytes, st);
+      });
+}
+
+// kv8_attention_tree(cache, its tensors, q, table, lens, cu, parent, scale | None, out | None, lse wanted, stream)
+PyObject* kv8_attention_tree(PyObject* const* a) {
+  const Queries x = queries(a);
+  const Tensor& parent = exact(a[6], "parent", {x.T}, at::kInt);
+  return attention(
+      x, a + 7, &parent, [&] { return qmm_kv8_attention_work(x.c.c, x.T, x.H, x.b.S, x.b.W); },
+      [&](float scale, void* out, float* lse, const Scratch& w, hipStream_t st) {
+        return qmm_kv8_attention_tree(x.c.c, x.q.data_ptr(), x.ld, x.dt, x.T, x.H, ints(*x.b.table), ints(*x.b.lens),
+                                      ints(*x.b.cu), x.b.S, x.b.W, ints(parent), scale, out, lse, w.p, w.bytes, st);
+      });
+}
+
+// --------------------------------------- queries, keys and tokens of a step
+// qk_norm_rope(q, k, positions, inv_freq, q_weight | None, k_weight | None, eps, interleaved, out | None, stream)
+PyObject* qk_norm_rope(PyObject* const* a) {
+  const Tensor& q = tensor(a[0], "q", 3);
+  const Tensor& k = tensor(a[1], "k", 3);
+  const int64_t T = q.size(0), D = q.size(2), Hq = q.size(1), Hk = k.size(1);
+  if (k.size(0) != T || k.size(2) != D || k.scalar_type() != q.scalar_type())
+    refuse("q and k must have the same tokens, head size and dtype, got ", q.sizes(), " and ", k.sizes());
+  const int64_t ldq = rows(q, "q"), ldk = rows(k, "k");
+  const qmm_dtype dt = element(q.scalar_type());
+  const Tensor& pos = exact(a[2], "positions", {T}, at::kInt);
+  const Tensor& freq = tensor(a[3], "inv_freq", 1);
+  exact(freq, "inv_freq", {freq.size(0)}, at::kFloat);
+  const Tensor* wq = none(a[4]) ? nullptr : &exact(a[4], "q_weight", {D}, q.scalar_type());
+  const Tensor* wk = none(a[5]) ? nullptr : &exact(a[5], "k_weight", {D}, q.scalar_type());
+  const double eps = PyFloat_AsDouble(a[6]);
+  if (PyErr_Occurred()) throw Failed();
+  Tensor qo, ko;
+  if (none(a[8])) {
+    on_gpu(q, "q");
+    on_gpu(k, "k");
+    qo = at::empty({T, Hq, D}, q.options());
+    ko = at::empty({T, Hk, D}, k.options());
+  } else {
+    if (!PyTuple_Check(a[8]) || PyTuple_GET_SIZE(a[8]) != 2) refuse("out must be (q, k)");
+    qo = tensor(PyTuple_GET_ITEM(a[8], 0), "out[0]", 3);
+    ko = tensor(PyTuple_GET_ITEM(a[8], 1), "out[1]", 3);
+    if (qo.sizes() != q.sizes() || ko.sizes() != k.sizes() || qo.scalar_type() != q.scalar_type() ||
+        ko.scalar_type() != q.scalar_type())
+      refuse("out must have the shapes and the dtype of q and k");
+  }
+  const int64_t ldqo = rows(qo, "out[0]"), ldko = rows(ko, "out[1]");
+  const Place p = place(a[9], {{&q, "q"}, {&k, "k"}, {&pos, "positions"}, {&freq, "inv_freq"}, {wq, "q_weight"}, {wk, "k_weight"}, {&qo, "out[0]"}, {&ko, "out[1]"}});
+  check(qmm_qk_norm_rope(q.data_ptr(), ldq, k.data_ptr(), ldk, dt, T, Hq, Hk, D, ints(pos), floats(freq),
+                         2 * freq.size(0), PyObject_IsTrue(a[7]), wq ? wq->data_ptr() : nullptr,
+                         wk ? wk->data_ptr() : nullptr, (float)eps, qo.data_ptr(), ldqo, ko.data_ptr(), ldko, p.st));
+  return tuple(qo, ko);
+}
+
+// logprobs(logits, tokens, top, stream)
+PyObject* logprobs(PyObject* const* a) {
+  const Tensor& x = tensor(a[0], "logits", 2);
+  const int64_t M = x.size(0), V = x.size(1), ld = rows(x, "logits"), top = whole(a[2]);
+  const qmm_dtype dt = x.scalar_type() == at::kFloat ? QMM_F32 : element(x.scalar_type());
+  const Tensor& tokens = exact(a[1], "tokens", {M}, at::kInt);
+  if (top < 0 || top > V) refuse("top must be in [0, ", V, "], got ", top);
+  on_gpu(x, "logits");
+  const Place p = place(a[3], {{&x, "logits"}, {&tokens, "tokens"}});
+  const auto f32 = x.options().dtype(at::kFloat);
+  const Tensor lp = at::empty({M}, f32), h = at::empty({M}, f32), top_lp = at::empty({M, top}, f32);
+  const Tensor ids = at::empty({M, top}, tokens.options());
+  const Scratch w = scratch(qmm_logprobs_work(dt, M, V, top), p);
+  check(qmm_logprobs(x.data_ptr(), ld, dt, M, V, ints(tokens), top, static_cast<float*>(lp.data_ptr()),
+                     static_cast<float*>(h.data_ptr()), ints_out(ids), static_cast<float*>(top_lp.data_ptr()), w.p,
+                     w.bytes, p.st));
+  return tuple(lp, h, ids, top_lp);
 }
 
 // kv8_update(cache, its tensors, ref, table, lens, parent, new_lens, stream)
@@ -411,7 +523,9 @@ PyMethodDef methods[] = {
     QMM_ENTRY(set_hooks, 2),  QMM_ENTRY(i8_quantize, 3),   QMM_ENTRY(i8_t, 8),
     QMM_ENTRY(i8_linear, 6),  QMM_ENTRY(kv8_append, 8),    QMM_ENTRY(kv8_read, 5),
     QMM_ENTRY(kv8_attention, 10), QMM_ENTRY(kv8_update, 8), QMM_ENTRY(kv8_compact, 5),
-    QMM_ENTRY(kv8_copy, 7),   {nullptr, nullptr, 0, nullptr}};
+    QMM_ENTRY(kv8_copy, 7),   QMM_ENTRY(kv8_attention_window, 12),
+    QMM_ENTRY(kv8_attention_tree, 11), QMM_ENTRY(qk_norm_rope, 10), QMM_ENTRY(logprobs, 4),
+    {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_serving", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -265,5 +265,31 @@ hipError_t launch_kv8_attention(const Kv8& c, int dt, const void* q, int64_t ldq
                                 int64_t Hq, const int32_t* table, const int32_t* lens,
                                 const int32_t* cu, int64_t S, int64_t W, float scale, void* out,
                                 float* lse, float* ws, hipStream_t st);
+// window >= 1, 0 <= sinks, both at most 2^30
+int64_t kv8_attention_window_work(const Kv8& c, int64_t T, int64_t Hq, int64_t S, int64_t W,
+                                  int64_t window, int64_t sinks);
+hipError_t launch_kv8_attention_window(const Kv8& c, int dt, const void* q, int64_t ldq, int64_t T,
+                                       int64_t Hq, const int32_t* table, const int32_t* lens,
+                                       const int32_t* cu, int64_t S, int64_t W, int64_t window,
+                                       int64_t sinks, float scale, void* out, float* lse, float* ws,
+                                       hipStream_t st);
+// scratch as kv8_attention_work says
+hipError_t launch_kv8_attention_tree(const Kv8& c, int dt, const void* q, int64_t ldq, int64_t T,
+                                     int64_t Hq, const int32_t* table, const int32_t* lens,
+                                     const int32_t* cu, int64_t S, int64_t W, const int32_t* parent,
+                                     float scale, void* out, float* lse, float* ws, hipStream_t st);
+
+// ------------------------------------- queries, keys and tokens of a step
+// D a multiple of 8 up to 512, rot one of 8 up to D
+hipError_t launch_qk_norm_rope(int dt, const void* q, int64_t ldq, const void* k, int64_t ldk,
+                               int64_t T, int64_t hq, int64_t hk, int64_t D, const int32_t* pos,
+                               const float* freq, int64_t rot, bool neighbours, const void* wq,
+                               const void* wk, float eps, void* qo, int64_t ldqo, void* ko,
+                               int64_t ldko, hipStream_t st);
+// top <= 64
+int64_t logprobs_work(int dt, int64_t M, int64_t V, int64_t top);
+hipError_t launch_logprobs(int dt, const void* x, int64_t ld, int64_t M, int64_t V,
+                           const int32_t* tokens, int64_t top, float* logprob, float* entropy,
+                           int32_t* ids, float* top_lp, void* work, hipStream_t st);
 
 }  // namespace qmm

@@ -27,6 +27,8 @@ EXPORTS = ["qmm_quantize", "qmm_dequantize", "qmm_t", "qmv", "qmm_n", "qconv2d_n
            "qmm_affine_pack", "qmv_affine_packed", "qmm_t_affine_packed",
            "qmm_i8_quantize", "qmm_i8_t_work", "qmm_i8_t", "qmm_i8_linear_work", "qmm_i8_linear",
            "qmm_kv8_append", "qmm_kv8_read", "qmm_kv8_attention_work", "qmm_kv8_attention",
+           "qmm_kv8_attention_window_work", "qmm_kv8_attention_window", "qmm_kv8_attention_tree",
+           "qmm_qk_norm_rope", "qmm_logprobs_work", "qmm_logprobs",
            "qmm_kv8_pages_work", "qmm_kv8_update", "qmm_kv8_compact", "qmm_kv8_copy",
            "qmm_crossover_m", "qmm_route", "qmm_force_kernel", "qmm_last_error"]
 
@@ -87,18 +89,28 @@ def lib():
         L.qmm_kv8_read.argtypes = [vp, vp, i64, i32, vp, vp, vp]
         L.qmm_kv8_attention.argtypes = [vp, vp, i64, i32, i64, i64, vp, vp, vp, i64, i64, f32,
                                         vp, vp, vp, i64, vp]
+        L.qmm_kv8_attention_window.argtypes = [vp, vp, i64, i32, i64, i64, vp, vp, vp, i64, i64, i64, i64,
+                                               f32, vp, vp, vp, i64, vp]
+        L.qmm_kv8_attention_tree.argtypes = [vp, vp, i64, i32, i64, i64, vp, vp, vp, i64, i64, vp, f32,
+                                             vp, vp, vp, i64, vp]
+        L.qmm_qk_norm_rope.argtypes = [vp, i64, vp, i64, i32, i64, i64, i64, i64, vp, vp, i64, i32, vp, vp,
+                                       f32, vp, i64, vp, i64, vp]
+        L.qmm_logprobs.argtypes = [vp, i64, i32, i64, i64, vp, i64, vp, vp, vp, vp, vp, i64, vp]
         L.qmm_kv8_update.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, vp, vp, vp, vp, i64, vp]
         L.qmm_kv8_compact.argtypes = [vp, vp, vp, i64, i64, vp, vp, vp, vp, vp, i64, vp]
         L.qmm_kv8_copy.argtypes = [vp, vp, vp, vp, i64, vp]
         for f in ("qmm_i8_quantize", "qmm_i8_t", "qmm_i8_linear", "qmm_kv8_append",
                   "qmm_kv8_read", "qmm_kv8_attention", "qmm_kv8_update", "qmm_kv8_compact",
-                  "qmm_kv8_copy"):
+                  "qmm_kv8_copy", "qmm_kv8_attention_window", "qmm_kv8_attention_tree", "qmm_qk_norm_rope",
+                  "qmm_logprobs"):
             getattr(L, f).restype = i32
         L.qmm_i8_t_work.argtypes = L.qmm_i8_linear_work.argtypes = [i64, i64, i64]
         L.qmm_kv8_attention_work.argtypes = [vp, i64, i64, i64, i64]
+        L.qmm_kv8_attention_window_work.argtypes = [vp, i64, i64, i64, i64, i64, i64]
+        L.qmm_logprobs_work.argtypes = [i32, i64, i64, i64]
         L.qmm_kv8_pages_work.argtypes = [i64]
         for f in ("qmm_i8_t_work", "qmm_i8_linear_work", "qmm_kv8_attention_work",
-                  "qmm_kv8_pages_work"):
+                  "qmm_kv8_attention_window_work", "qmm_logprobs_work", "qmm_kv8_pages_work"):
             getattr(L, f).restype = i64
         L.qmm_crossover_m.argtypes = [i32, i32, i32, i64, i64]
         L.qmm_crossover_m.restype = i64
@@ -739,6 +751,24 @@ def kv8_attention(cache, q, table, lens, cu, scale=None, out=None, return_lse=Fa
     return _serving().kv8_attention(at, held, q, table, lens, cu, scale, out, return_lse, _on(stream))
 
 
+def kv8_attention_window(cache, q, table, lens, cu, window, sinks=0, scale=None, out=None, return_lse=False, stream=None):
+    """kv8_attention with a sliding window: a query at position p sees the positions
+    above p - window up to its own, and those below sinks. Pages that no query sees
+    are not read."""
+    at, held = _cache(cache)
+    return _serving().kv8_attention_window(at, held, q, table, lens, cu, window, sinks, scale, out, return_lse,
+                                           _on(stream))
+
+
+def kv8_attention_tree(cache, q, table, lens, cu, parent, scale=None, out=None, return_lse=False, stream=None):
+    """kv8_attention of drafted tokens: the last new tokens of each sequence, up to 64,
+    are a tree, and each sees what precedes the tree, its ancestors and itself.
+    parent [T] int32: the index of each token's parent among its sequence's new
+    tokens, an earlier one of the tree; -1 (or any other number) for a root."""
+    at, held = _cache(cache)
+    return _serving().kv8_attention_tree(at, held, q, table, lens, cu, parent, scale, out, return_lse, _on(stream))
+
+
 def kv8_update(cache, ref, table, lens, parent, new_lens, stream=None):
     """One step of page bookkeeping (libqmm.h, qmm_kv8_update): slot s continues slot
     parent[s] and gets pages for new_lens[s] tokens. Returns (ref, table,
@@ -761,3 +791,21 @@ def kv8_copy(to, dst, source, src, stream=None):
     (int32 tensors; the dst distinct, none of them also a src of one cache)."""
     a, b = _cache(to, "to"), _cache(source, "source")
     _serving().kv8_copy(*a, dst, *b, src, _on(stream))
+
+
+def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, out=None,
+                 stream=None):
+    """Queries q [T, q_heads, head_dim] and keys k [T, k_heads, head_dim] (f16 or bf16,
+    tokens may be strided) with each head's norm (where its weight [head_dim] is
+    given) and its rotation by positions [T] (int32) times inv_freq [rot_dim / 2]
+    (fp32): of elements i and i + rot_dim/2, or 2i and 2i + 1 where interleaved.
+    Returns (q, k), new tensors or those of out = (q, k), which may be the inputs."""
+    return _serving().qk_norm_rope(q, k, positions, inv_freq, q_weight, k_weight, eps, interleaved, out, _on(stream))
+
+
+def logprobs(logits, tokens, top=0, stream=None):
+    """For each row of logits [M, V] (f16, bf16 or fp32, rows may be strided): the log
+    probability of tokens [M] (int32), the entropy, and the `top` (at most 64) most
+    likely tokens. Returns (logprob [M], entropy [M], ids int32 [M, top], their
+    log probabilities [M, top])."""
+    return _serving().logprobs(logits, tokens, top, _on(stream))

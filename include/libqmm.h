@@ -560,6 +560,39 @@ qmm_status qmm_kv8_attention(const qmm_kv8_cache* cache, const void* q, int64_t 
                              float* lse, void* work, int64_t work_bytes, void* stream);
 
 /*
+ * The same with a sliding window: a query at position p sees the positions
+ * above p - window (window >= 1) up to its own, and besides them those below
+ * `sinks` (>= 0: first tokens that stay visible) up to its own. Pages that no
+ * query sees are not read: their table places may hold anything. QMM_E_ARG for
+ * other windows and sinks.
+ */
+int64_t qmm_kv8_attention_window_work(const qmm_kv8_cache* cache, int64_t T, int64_t q_heads,
+                                      int64_t S, int64_t W, int64_t window, int64_t sinks);
+qmm_status qmm_kv8_attention_window(const qmm_kv8_cache* cache, const void* q, int64_t ldq,
+                                    qmm_dtype dt, int64_t T, int64_t q_heads, const int32_t* table,
+                                    const int32_t* lens, const int32_t* cu, int64_t S, int64_t W,
+                                    int64_t window, int64_t sinks, float scale, void* out, float* lse,
+                                    void* work, int64_t work_bytes, void* stream);
+
+/*
+ * The same for drafted tokens: the last min(n, QMM_TREE_TOKENS) of a sequence's
+ * n new tokens are a tree. parent [T]: the parent of a sequence's i-th new token
+ * is its parent[cu + i]-th new one, which must come before it and be of the tree
+ * itself (any other number, -1 say, makes it a root). A token of the tree sees
+ * every position before the tree, its ancestors and itself; the new tokens before
+ * the tree (longer prompts in one batch with drafts) are causal, and their
+ * parents are not read. Where each token's parent is the one before it this is
+ * qmm_kv8_attention. The tokens lie in the cache in the order of the batch, one
+ * position each, whatever their depth. Scratch: qmm_kv8_attention_work.
+ */
+#define QMM_TREE_TOKENS 64
+qmm_status qmm_kv8_attention_tree(const qmm_kv8_cache* cache, const void* q, int64_t ldq,
+                                  qmm_dtype dt, int64_t T, int64_t q_heads, const int32_t* table,
+                                  const int32_t* lens, const int32_t* cu, int64_t S, int64_t W,
+                                  const int32_t* parent, float scale, void* out, float* lse,
+                                  void* work, int64_t work_bytes, void* stream);
+
+/*
  * One step of page bookkeeping for S slots, on the device: slot s continues
  * the first min(lens[parent[s]], new_lens[s]) tokens of slot parent[s] (s
  * itself: the sequence goes on; another slot: a fork; outside [0, S): nothing)
@@ -600,6 +633,46 @@ qmm_status qmm_kv8_compact(const qmm_kv8_cache* cache, const int32_t* ref, const
  */
 qmm_status qmm_kv8_copy(const qmm_kv8_cache* to, const int32_t* dst, const qmm_kv8_cache* from,
                         const int32_t* src, int64_t n, void* stream);
+
+/*
+ * Queries q [T, q_heads, head_dim] and keys k [T, k_heads, head_dim] (token t at
+ * q + t*ldq, k + t*ldk elements; strides multiples of 8, pointers 16-byte
+ * aligned) ready for the cache: each head's norm and its rotation by the token's
+ * position, in one pass with one rounding.
+ *  - Norm (where the weight [head_dim] in dt is not NULL): x * weight /
+ *    sqrt(mean x^2 + eps).
+ *  - Rotation of the first rot_dim elements: with t = positions[token] *
+ *    inv_freq[i], i < rot_dim / 2, the pair (a, b) of elements i and i +
+ *    rot_dim/2 (interleaved 0) or 2i and 2i + 1 (interleaved 1) becomes (a cos t -
+ *    b sin t, b cos t + a sin t). The angle is taken in 64 bits. positions [T]
+ *    int32 (any value), inv_freq [rot_dim / 2] fp32, 16-byte aligned, as the
+ *    weights are.
+ * head_dim a multiple of 8 up to 512, rot_dim one from 8 to head_dim; eps >= 0. q_out may be q
+ * (with its stride) and k_out may be k; apart from that the outputs overlap no
+ * other array.
+ */
+qmm_status qmm_qk_norm_rope(const void* q, int64_t ldq, const void* k, int64_t ldk, qmm_dtype dt,
+                            int64_t T, int64_t q_heads, int64_t k_heads, int64_t head_dim,
+                            const int32_t* positions, const float* inv_freq, int64_t rot_dim,
+                            int interleaved, const void* q_weight, const void* k_weight, float eps,
+                            void* q_out, int64_t ldqo, void* k_out, int64_t ldko, void* stream);
+
+/*
+ * For each row of logits [M, V] (f16, bf16 or f32; row r starts at logits + r*ld
+ * elements, any stride >= V and the alignment of the type): with lse = ln sum
+ * exp(x), logprob [M] = x[tokens[r]] - lse (tokens [M] int32; -inf for one
+ * outside [0, V)), entropy [M] = lse - sum softmax(x) x, and the `top` (0 to 64,
+ * at most V) most likely tokens, top_ids [M, top] int32 and top_logprobs [M, top],
+ * most likely first, among equal logits the lowest number first (top 0: both may
+ * be NULL). Logits of -inf are tokens that cannot be; a row of nothing else gives
+ * -inf, entropy 0 and the lowest numbers. A row that holds a NaN or +inf gives NaN
+ * and numbers -1. Sums in fp32.
+ */
+int64_t qmm_logprobs_work(qmm_dtype dt, int64_t M, int64_t V, int64_t top);
+qmm_status qmm_logprobs(const void* logits, int64_t ld, qmm_dtype dt, int64_t M, int64_t V,
+                        const int32_t* tokens, int64_t top, float* logprob, float* entropy,
+                        int32_t* top_ids, float* top_logprobs, void* work, int64_t work_bytes,
+                        void* stream);
 
 /* Message for the last non-OK status returned on the calling thread. */
 const char* qmm_last_error(void);

@@ -129,7 +129,8 @@ def _compile(src):
         check_products(src, _assembly(src))
     # the host pass warns about the device-only target feature; drop that noise
     msgs = [l for l in r.stderr.splitlines() if "packed-fp32-ops" not in l
-            and "not a recognized feature" not in l and REPORT not in l]
+            and "not a recognized feature" not in l and REPORT not in l
+            and not l.startswith("In file included from")]
     return obj, "\n".join(msgs)
 
 

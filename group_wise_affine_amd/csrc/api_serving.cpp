@@ -305,6 +305,16 @@ qmm_status qmm_kv8_attention_window(const qmm_kv8_cache* cache, const void* q, i
       });
 }
 
+int64_t qmm_kv8_attention_tree_work(const qmm_kv8_cache* cache, int64_t T, int64_t q_heads, int64_t S,
+                                    int64_t W) {
+  qmm::Kv8 c;
+  if (check_cache("qmm_kv8_attention_tree_work", cache, &c) ||
+      check_batch("qmm_kv8_attention_tree_work", T, S, W) || q_heads < c.heads)
+    return 0;
+  const int64_t b = qmm::kv8_attention_tree_work(c, T, q_heads, S, W);
+  return b > 0 ? kCounterBytes + b : 0;
+}
+
 qmm_status qmm_kv8_attention_tree(const qmm_kv8_cache* cache, const void* q, int64_t ldq,
                                   qmm_dtype dt, int64_t T, int64_t q_heads, const int32_t* table,
                                   const int32_t* lens, const int32_t* cu, int64_t S, int64_t W,
@@ -315,7 +325,7 @@ qmm_status qmm_kv8_attention_tree(const qmm_kv8_cache* cache, const void* q, int
   if (!aligned(parent, 4)) return fail(QMM_E_ALIGN, "%s: parent must be 4-byte aligned", tag);
   return attention(
       tag, cache, q, ldq, dt, T, q_heads, table, lens, cu, S, W, out, lse, work, work_bytes, stream,
-      [&](const qmm::Kv8& c) { return qmm::kv8_attention_work(c, T, q_heads, S, W); },
+      [&](const qmm::Kv8& c) { return qmm::kv8_attention_tree_work(c, T, q_heads, S, W); },
       [&](const qmm::Kv8& c, float* ws) {
         return qmm::launch_kv8_attention_tree(c, (int)dt, q, ldq, T, q_heads, table, lens, cu, S, W,
                                               parent, scale, out, lse, ws, (hipStream_t)stream);

@@ -382,7 +382,7 @@ PyObject* kv8_attention_tree(PyObject* const* a) {
   const Queries x = queries(a);
   const Tensor& parent = exact(a[6], "parent", {x.T}, at::kInt);
   return attention(
-      x, a + 7, &parent, [&] { return qmm_kv8_attention_work(x.c.c, x.T, x.H, x.b.S, x.b.W); },
+      x, a + 7, &parent, [&] { return qmm_kv8_attention_tree_work(x.c.c, x.T, x.H, x.b.S, x.b.W); },
       [&](float scale, void* out, float* lse, const Scratch& w, hipStream_t st) {
         return qmm_kv8_attention_tree(x.c.c, x.q.data_ptr(), x.ld, x.dt, x.T, x.H, ints(*x.b.table), ints(*x.b.lens),
                                       ints(*x.b.cu), x.b.S, x.b.W, ints(parent), scale, out, lse, w.p, w.bytes, st);

@@ -273,7 +273,7 @@ hipError_t launch_kv8_attention_window(const Kv8& c, int dt, const void* q, int6
                                        const int32_t* cu, int64_t S, int64_t W, int64_t window,
                                        int64_t sinks, float scale, void* out, float* lse, float* ws,
                                        hipStream_t st);
-// scratch as kv8_attention_work says
+int64_t kv8_attention_tree_work(const Kv8& c, int64_t T, int64_t Hq, int64_t S, int64_t W);
 hipError_t launch_kv8_attention_tree(const Kv8& c, int dt, const void* q, int64_t ldq, int64_t T,
                                      int64_t Hq, const int32_t* table, const int32_t* lens,
                                      const int32_t* cu, int64_t S, int64_t W, const int32_t* parent,

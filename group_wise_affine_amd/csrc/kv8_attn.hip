@@ -4,8 +4,7 @@
 namespace qmm {
 
 int64_t kv8_attention_work(const Kv8& c, int64_t T, int64_t Hq, int64_t S, int64_t W) {
-  const Plan p = plan(c, T, Hq, S, W);
-  return decode_bytes(p, c) + prompt_bytes(p, c);
+  return attention_work<Mask::kCausal>(c, T, Hq, S, W);
 }
 
 hipError_t launch_kv8_attention(const Kv8& c, int dt, const void* q, int64_t ldq, int64_t T,

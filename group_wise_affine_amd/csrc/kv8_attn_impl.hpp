@@ -45,6 +45,7 @@ struct AttnArgs {
   int64_t ldq;
   int G;               // query heads per cache head, 16 at a time
   int unit, extra;     // new tokens per workgroup, spare items per sequence
+  int items, each;     // of the batch; of every sequence, or 0: as many as its tokens need
   int many;            // sequences with more query rows than this are the prompt kernel's
   float scale;         // magnitude of the scores' scale, times log2 e
   uint32_t flip;       // its sign, as the sign bits of two queries
@@ -55,6 +56,11 @@ struct AttnArgs {
   int window, sinks;       // kWindow; sinks <= 2^30
   const int32_t* parent;   // kTree: [T]
 };
+
+__device__ __forceinline__ SeqAt locate_item(const AttnArgs& a, int i, int bt_log2) {
+  return a.each > 0 ? of_sequence(a.q, i / a.each, i % a.each, bt_log2)
+                    : locate(a.q, i, a.unit, a.extra, bt_log2);
+}
 
 // The tiles that an item looks at: those of its sequence up to `most`, without
 // the ones that lie between the sinks and the window of its first row (at
@@ -210,10 +216,19 @@ __device__ __forceinline__ Share share(float v0, float v1, float l) {
   return s;
 }
 // A part in the scratch buffer: R rows' maxima and sums, then the rows. R is 16
-// for the decode kernel and kPromptRows for the prompt kernel.
+// for the decode kernel, kDraftRows for the draft kernel and kPromptRows for the
+// prompt kernel.
+constexpr int kDraftRows = 32;
 constexpr int kPromptRows = 128;
 template <int D, int R>
 constexpr int kPart = R * (D + 2);
+
+// the value of the lane 32 away
+__device__ __forceinline__ float other_half(float x) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, x);
+  const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  return __builtin_bit_cast(float, threadIdx.x & 32 ? r[0] : r[1]);
+}
 
 // ------------------------------------------------------------------- decode
 // Up to 16 query rows (tokens x heads of one group) per workgroup, NW
@@ -244,7 +259,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : D == 128 ? 2 : 3) void kv8_
   const int head = blockIdx.y / blocks, h0 = blockIdx.y % blocks * 16, split = blockIdx.z;
   const int G = min(16, a.G - h0);
   const Kv8& c = a.c;
-  const SeqAt seq = locate(a.q, blockIdx.x, a.unit, a.extra, BT);
+  const SeqAt seq = locate_item(a, blockIdx.x, BT);
   const int s = seq.s, t0 = seq.first, n = seq.count, len = seq.len, item = seq.item;
   const int i0 = item * a.unit;
   if (item < 0 || i0 >= n || (int64_t)n * a.G > a.many) return;
@@ -504,13 +519,14 @@ struct JoinAt {
   int64_t at;
   int parts;
 };
-template <Mask M, bool PROMPT>
+template <Mask M, int R>
 __device__ __forceinline__ JoinAt join_at(const AttnArgs& a, int unit, int r) {
-  const int blocks = PROMPT ? 1 : (a.G + 15) / 16, columns = a.c.heads * blocks;
+  constexpr bool PROMPT = R == kPromptRows;
+  const int blocks = PROMPT ? 1 : (a.G + R - 1) / R, columns = a.c.heads * blocks;
   const int index = unit / columns, column = unit % columns;
-  const int head = column / blocks, h0 = column % blocks * 16;
-  const int G = PROMPT ? a.G : min(16, a.G - h0);
-  const SeqAt q = locate(a.q, index, a.unit, a.extra, a.c.bt_log2);
+  const int head = column / blocks, h0 = column % blocks * R;
+  const int G = PROMPT ? a.G : min(R, a.G - h0);
+  const SeqAt q = locate_item(a, index, a.c.bt_log2);
   const int i0 = q.item * a.unit;
   JoinAt j{0, 0};
   if (q.item < 0 || i0 >= q.count || ((int64_t)q.count * a.G > a.many) != PROMPT) return j;
@@ -544,7 +560,7 @@ __global__ __launch_bounds__(256) void kv8_join_few_kernel(AttnArgs a) {
       ml[w] = *reinterpret_cast<const float2*>(part + w * kFloats + 2 * r);
       v[w] = *reinterpret_cast<const float2*>(part + w * kFloats + 2 * R + r * D + d);
     }
-  const JoinAt j = join_at<M, R == kPromptRows>(a, blockIdx.x, r);
+  const JoinAt j = join_at<M, R>(a, blockIdx.x, r);
   if (j.parts <= 1) return;
   float m = kNone, l = 0.0f, v0 = 0.0f, v1 = 0.0f;
 #pragma unroll
@@ -568,9 +584,9 @@ __global__ __launch_bounds__(256) void kv8_join_few_kernel(AttnArgs a) {
 // them takes as long as memory does, and what lies past the sequence's parts
 // is not used. A kernel of its own: its launch costs less than a counter that
 // every workgroup waits for.
-template <Mask M, class T, int D>
+template <Mask M, class T, int D, int R>
 __global__ __launch_bounds__(256) void kv8_join_kernel(AttnArgs a) {
-  constexpr int R = 16, kFloats = kPart<D, R>;
+  constexpr int kFloats = kPart<D, R>;
   constexpr int kSub = 512 / D, kEach = kMaxSplits / kSub;
   __shared__ float fac[kMaxSplits], half[256][2];
   const int tid = threadIdx.x, lane = tid % 64, r = blockIdx.y;
@@ -585,7 +601,7 @@ __global__ __launch_bounds__(256) void kv8_join_kernel(AttnArgs a) {
   for (int k = 0; k < kEach; k++)
     if (k * kSub + sub < a.splits)
       v[k] = *reinterpret_cast<const float2*>(part + (k * kSub + sub) * kFloats + 2 * R + r * D + d);
-  const JoinAt j = join_at<M, false>(a, blockIdx.x, r);
+  const JoinAt j = join_at<M, R>(a, blockIdx.x, r);
   const int parts = j.parts;
   if (parts <= 1) return;   // written already
   // the parts' factors exp2(m - max) and the sum, by every wavefront
@@ -626,13 +642,294 @@ __global__ __launch_bounds__(256) void kv8_join_kernel(AttnArgs a) {
   join_out<T>(a, j.at, D, d, v0, v1, m, l);
 }
 
-// ------------------------------------------------------------------ prompts
-// the value of the lane 32 away
-__device__ __forceinline__ float other_half(float x) {
-  const uint32_t u = __builtin_bit_cast(uint32_t, x);
-  const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
-  return __builtin_bit_cast(float, threadIdx.x & 32 ? r[0] : r[1]);
+// ------------------------------------------------------------------- drafts
+// Some drafted tokens per sequence: up to 32 query rows (tokens x heads of one
+// group) per workgroup, NW wavefronts. As in the decode kernel a wavefront takes
+// tiles of 64 tokens for itself and holds its whole state in registers, but
+// the products are v_mfma_f32_32x32x16_f16, so that a code is read and turned into
+// f16 once for 32 rows.
+//
+// S^T = K Q^T: row 8 (e/4) + 4 h + e%4 of the A operand is token 16 h + e of 32, so
+// that lane half h gets the scores of 16 tokens in a row, which lie in one page, and
+// its registers are eight by eight the B operand of O^T = V^T P^T, whose A operand is
+// V^T as it is read (16 tokens of one column per 16-byte load). The order of the
+// sum over D is that of 16-byte loads of keys and queries.
+//
+// Row groups of a sequence read the same codes: four that follow each other are
+// numbered eight apart, which puts them on one XCD and its L2.
+constexpr int kBundle = 4;
+// floats from one row to the next where the wavefronts' results are joined: rows
+// start in other banks
+constexpr int draft_row(int D) { return D + 4; }
+template <class T, int D, int BT, int NW>   // pages of 1 << BT tokens
+__global__ __launch_bounds__(64 * NW, 2) void kv8_draft_kernel(AttnArgs a) {
+  constexpr Mask M = Mask::kTree;
+  constexpr int KD = D / 32, VD = D / 32, R = kDraftRows, kRow = draft_row(D);
+  constexpr bool kTwo = __is_same(T, F16);   // two f16 terms of the weights, as in the decode kernel
+  const int tid = threadIdx.x, lane = tid % 64;
+  const int wave = __builtin_amdgcn_readfirstlane(tid / 64);   // uniform: scalar
+  const int col = lane % 32, h = lane / 32;
+  const Kv8& c = a.c;
+  const int blocks = (a.G + R - 1) / R, columns = c.heads * blocks;
+  const int at_unit = blockIdx.x / (8 * kBundle) * 8 + blockIdx.x % 8;   // (bundle, column, part)
+  const int bundles = (a.items + kBundle - 1) / kBundle;
+  const int column = at_unit % columns, split = at_unit / columns / bundles;
+  const int index = at_unit / columns % bundles * kBundle + blockIdx.x / 8 % kBundle;
+  if (split >= a.splits || index >= a.items) return;
+  const int head = column / blocks, h0 = column % blocks * R;
+  const int G = min(R, a.G - h0);
+  const SeqAt seq = locate_item(a, index, BT);
+  const int s = seq.s, t0 = seq.first, n = seq.count, len = seq.len, i0 = seq.item * a.unit;
+  if (seq.item < 0 || i0 >= n || (int64_t)n * a.G > a.many) return;
+  const int ntok = min(n - i0, a.unit);
+  const int rows = ntok * G;                 // <= 32
+  const int most = len - n + i0 + ntok;
+  const int tiles = walk<M>(a, most, len - n + i0).tiles, per = a.per;
+  const int parts = tiles > 0 ? (tiles + per - 1) / per : 1;
+  if (split >= parts) return;
+  const int first = split * per, last = min(first + per, tiles);
+
+  // this lane's query row (columns past the rows repeat the first one)
+  const int ct = col < rows ? col / G : 0, ch = col < rows ? col % G : 0;
+  const int min_limit = len - n + i0, limit = min_limit + ct;
+  const int tree = len - min(n, kTreeTokens);
+  const int parent = tree_parent(a, t0, n);
+  uint4 u[KD][2];
+  {
+    const uint16_t* qr = a.x + (int64_t)(t0 + i0 + ct) * a.ldq + (int64_t)(head * a.G + h0 + ch) * D + h * 16;
+#pragma unroll
+    for (int b = 0; b < KD; b++)
+#pragma unroll
+      for (int m = 0; m < 2; m++) u[b][m] = load_q(qr + b * 32 + m * 8, a.flip);
+  }
+  // the queries wait in the part of the shared memory where this wavefront's result
+  // goes at the end, a lane's pieces 64 pieces apart
+  extern __shared__ __attribute__((aligned(16))) float jo[];   // [NW][R][kRow]
+  half8_t* const qf = reinterpret_cast<half8_t*>(jo + wave * R * kRow) + lane;
+  float qs = a.scale;
+  auto take_queries = [&]() QMM_INLINE {
+    if constexpr (__is_same(T, F16)) {
+#pragma unroll
+      for (int b = 0; b < KD; b++)
+#pragma unroll
+        for (int m = 0; m < 2; m++) qf[(b * 2 + m) * 64] = __builtin_bit_cast(half8_t, u[b][m]);
+    } else {
+      uint32_t top = 0;
+#pragma unroll
+      for (int b = 0; b < KD; b++)
+#pragma unroll
+        for (int m = 0; m < 2; m++)
+          top = amax_pair(amax_pair(amax_pair(amax_pair(top, u[b][m].x), u[b][m].y), u[b][m].z), u[b][m].w);
+      top = amax_halves(top);
+      top = umax(top, (uint32_t)__shfl_xor((int)top, 32));
+      const Pow2 e = row_power(top);
+      qs *= e.up;
+#pragma unroll
+      for (int b = 0; b < KD; b++)
+#pragma unroll
+        for (int m = 0; m < 2; m++) qf[(b * 2 + m) * 64] = bf16_to_f16(u[b][m], e.down);
+    }
+  };
+
+  float16_t o[VD];
+#pragma unroll
+  for (int i = 0; i < VD; i++)
+#pragma unroll
+    for (int e = 0; e < 16; e++) o[i][e] = 0.0f;
+  Refs at{kNone, kNone};   // O relative to 2^at.w, l to 2^at.base
+  float l_run = 0.0f;
+
+  const int32_t* row = a.q.table + (int64_t)s * a.q.W;
+  // pages one per lane, loads ahead of their use: as in the decode kernel
+  constexpr int kPer = kTile >> BT, kIn = (1 << BT) - 1;
+  const int tk = 16 * (col >> 2 & 1) + 4 * (col >> 3) + (col & 3);   // this lane's key row of 32
+  int pages = -1;
+  float pages_ks = 0.0f, pages_vs = 0.0f;
+  auto chunk = [&](int tile) QMM_INLINE {   // pages from this tile's first on
+    const int t = tile * kTile + (lane << BT);
+    const int p = t < most ? row[t >> BT] : -1;   // most <= W << BT
+    pages = p < c.pages ? p : -1;
+    const int64_t blk = (int64_t)(pages < 0 ? 0 : pages) * c.heads + head;
+    pages_ks = c.ks[blk];
+    pages_vs = c.vs[blk];
+  };
+  int pk[2], pv[2];   // this lane's pages of keys and values in a tile's halves
+  auto look_up = [&](int i) QMM_INLINE {   // the chunk's i-th tile
+#pragma unroll
+    for (int j = 0; j < 2; j++) {
+      pk[j] = __shfl(pages, i * kPer + ((32 * j + (tk & 16)) >> BT));
+      pv[j] = __shfl(pages, i * kPer + ((32 * j + 16 * h) >> BT));
+    }
+  };
+  u32x4_t kw[2][KD], vw[2][VD];
+  auto key_at = [&](int j) QMM_INLINE {
+    return c.k + c.block(pk[j] < 0 ? 0 : pk[j], head) + ((32 * j + tk) & kIn) * D + h * 16;
+  };
+  auto fetch_values = [&](int j) QMM_INLINE {
+    const int8_t* vp = c.v + c.block(pv[j] < 0 ? 0 : pv[j], head) + (col << BT) + ((32 * j + 16 * h) & kIn);
+#pragma unroll
+    for (int i = 0; i < VD; i++) vw[j][i] = *reinterpret_cast<const u32x4_t*>(vp + ((i * 32) << BT));
+  };
+  const int run = per / NW;   // tiles of a wavefront
+  const int w_first = first + wave * run, w_last = min(w_first + run, last);
+  auto begin = [&](int tile) QMM_INLINE {
+    chunk(tile);
+    look_up(0);
+#pragma unroll
+    for (int j = 0; j < 2; j++) {
+      const int8_t* kp = key_at(j);
+#pragma unroll
+      for (int b = 0; b < KD; b++) kw[j][b] = *reinterpret_cast<const u32x4_t*>(kp + b * 32);
+    }
+    fetch_values(0);
+    fetch_values(1);
+    // an (empty) use: the wait for the scales belongs here, and not in the loop
+    asm volatile("" : "+v"(pages), "+v"(pages_ks), "+v"(pages_vs));
+  };
+  if (w_first < w_last) begin(w_first);
+  take_queries();
+  const uint64_t line = last * kTile > tree ? tree_path(parent, n, i0 + ct) : 0;   // (no tile before is masked)
+  for (int from = w_first; from < w_last; from += 1 << BT) {   // a chunk: 64 pages
+   const int count = min(w_last - from, 1 << BT);
+   if (from != w_first) begin(from);
+   for (int i = 0; i < count; i++) {
+    const int base = (from + i) * kTile;
+    int page[2];
+    float ks[2], r[2];
+#pragma unroll
+    for (int j = 0; j < 2; j++) {
+      page[j] = pv[j];
+      ks[j] = __shfl(pages_ks, i * kPer + ((32 * j + 16 * h) >> BT)) * qs;
+      r[j] = __shfl(pages_vs, i * kPer + ((32 * j + 16 * h) >> BT));
+    }
+    const bool more = i + 1 < count;
+    if (more) look_up(i + 1);
+    float16_t sc[2];
+#pragma unroll
+    for (int j = 0; j < 2; j++)
+#pragma unroll
+      for (int e = 0; e < 16; e++) sc[j][e] = 0.0f;
+    const int8_t *k0 = key_at(0), *k1 = key_at(1);   // of the next tile
+#pragma unroll
+    for (int b = 0; b < KD; b++) {
+#pragma unroll
+      for (int m = 0; m < 2; m++) {
+        const half8_t q = qf[(b * 2 + m) * 64];
+#pragma unroll
+        for (int j = 0; j < 2; j++)
+          sc[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(codes_f16(kw[j][b][2 * m], kw[j][b][2 * m + 1]), q, sc[j], 0, 0, 0);
+        // (the compiler would convert the whole tile first and run out of registers)
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if (more) {
+        kw[0][b] = *reinterpret_cast<const u32x4_t*>(k0 + b * 32);
+        kw[1][b] = *reinterpret_cast<const u32x4_t*>(k1 + b * 32);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if (!(all_seen<M>(a, base, min_limit, min_limit + ntok - 1, tree) && __all(page[0] >= 0 && page[1] >= 0))) {
+      // what is not seen weighs nothing, whatever its scale
+      const uint64_t tokens = seen_bits<M>(a, base, limit, tree, line) >> (h * 16);
+#pragma unroll
+      for (int j = 0; j < 2; j++) {
+        const uint32_t seen = page[j] < 0 ? 0 : (uint32_t)(tokens >> (32 * j)) & 0xffffu;
+#pragma unroll
+        for (int e = 0; e < 16; e++) sc[j][e] = seen >> e & 1 ? sc[j][e] * ks[j] : -__builtin_inff();
+        r[j] = seen == 0 ? 0.0f : r[j];
+        ks[j] = 1.0f;
+      }
+    }
+    float mx = -__builtin_inff(), wx = -__builtin_inff();
+#pragma unroll
+    for (int j = 0; j < 2; j++) {
+      float top = sc[j][0];
+#pragma unroll
+      for (int e = 1; e < 16; e++) top = fmaxf(top, sc[j][e]);
+      top *= ks[j];   // (no scale is negative)
+      mx = fmaxf(mx, top);
+      // (an infinite or NaN scale leaves the reference, a zero's logarithm is -inf)
+      if (r[j] < __builtin_inff()) wx = fmaxf(wx, top + __builtin_amdgcn_logf(r[j]));
+    }
+    mx = fmaxf(mx, other_half(mx));
+    wx = fmaxf(wx, other_half(wx));
+    // raised when one grows by more than 2^8, as in the prompt kernel
+    const bool raise = mx > at.base + 8.0f || wx > at.w + 8.0f;
+    if (__any(raise)) {   // (a row's results do not depend on the other rows')
+      const Refs to = rise(at, raise ? mx : kNone, raise ? wx : kNone);
+      const float down = __builtin_amdgcn_exp2f(at.w - to.w);   // what the values so far shrink by
+      l_run *= __builtin_amdgcn_exp2f(at.base - to.base);
+      at = to;
+#pragma unroll
+      for (int i = 0; i < VD; i++) o[i] *= down;
+    }
+#pragma unroll
+    for (int j = 0; j < 2; j++) {
+      const float f = weight_scale(r[j], at);
+#pragma unroll
+      for (int m = 0; m < 2; m++) {
+        half8_t pf, pl;
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+          const float x = __builtin_amdgcn_exp2f(fmaf(sc[j][8 * m + e], ks[j], -at.base));
+          l_run += x;
+          const float w = x * f;
+          pf[e] = (_Float16)w;
+          if constexpr (kTwo) pl[e] = (_Float16)(w - (float)pf[e]);
+        }
+#pragma unroll
+        for (int i = 0; i < VD; i++) {
+          const half8_t vf = codes_f16(vw[j][i][2 * m], vw[j][i][2 * m + 1]);
+          o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, pf, o[i], 0, 0, 0);
+          if constexpr (kTwo) o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, pl, o[i], 0, 0, 0);
+          if (i % 2 == 1) __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+      if (more) fetch_values(j);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+   }
+  }
+  l_run += other_half(l_run);
+
+  // join the wavefronts: o[i][4 q + e] is value column 32 i + 8 q + 4 h + e
+  __shared__ float jm[NW][R], jl[NW][R];
+  if (h == 0) {
+    jm[wave][col] = at.base;
+    jl[wave][col] = l_run;
+  }
+  const float vref = __builtin_amdgcn_exp2f(at.w - at.base);
+#pragma unroll
+  for (int i = 0; i < VD; i++)
+#pragma unroll
+    for (int q = 0; q < 4; q++)
+      *reinterpret_cast<float4_t*>(jo + ((wave * R + col) * kRow + i * 32 + q * 8 + h * 4)) =
+          float4_t{o[i][q * 4], o[i][q * 4 + 1], o[i][q * 4 + 2], o[i][q * 4 + 3]} * vref;
+  __syncthreads();
+  float* part = a.ws + (((int64_t)index * columns + column) * a.splits + split) * kPart<D, R>;
+  for (int i = tid; i < rows * (D / 2); i += 64 * NW) {
+    const int q = i / (D / 2), d = i % (D / 2) * 2;
+    float m = kNone;
+#pragma unroll
+    for (int w = 0; w < NW; w++) m = fmaxf(m, jm[w][q]);
+    float l = 0.0f, v0 = 0.0f, v1 = 0.0f;
+#pragma unroll
+    for (int w = 0; w < NW; w++) {
+      const float e = __builtin_amdgcn_exp2f(jm[w][q] - m);
+      const float2 v = *reinterpret_cast<const float2*>(jo + (w * R + q) * kRow + d);
+      l += jl[w][q] * e;
+      v0 += v.x * e;
+      v1 += v.y * e;
+    }
+    if (parts == 1) {
+      join_out<T>(a, (int64_t)(t0 + i0 + q / G) * (c.heads * a.G) + head * a.G + h0 + q % G, D, d, v0, v1, m, l);
+    } else {
+      *reinterpret_cast<float2*>(part + 2 * R + q * D + d) = make_float2(v0, v1);
+      if (d == 0) *reinterpret_cast<float2*>(part + 2 * q) = make_float2(m, l);
+    }
+  }
 }
+
+// ------------------------------------------------------------------ prompts
 // The work items of a prompt batch differ in length by as much as the contexts
 // do, and there are only a few of them per CU: the longest come first. Returns
 // the item of rank `rank` (every workgroup finds the ranks by itself: a few
@@ -933,7 +1230,7 @@ __global__ __launch_bounds__(2 * kPromptRows, D == 256 ? 1 : 2) void kv8_prompt_
       look_up(tile + 2);
     }
     const int base = path.real(tile) * kTile;
-    if (base <= wave_max) {
+    if (base <= wave_max && wave * 32 < rows) {   // (a wavefront without rows only carries codes)
       float f[4], vs[4];
       uint32_t missing = 0;
 #pragma unroll
@@ -1007,14 +1304,14 @@ __global__ __launch_bounds__(2 * kPromptRows, D == 256 ? 1 : 2) void kv8_prompt_
   if (h == 0 && a.lse) a.lse[to] = any ? fmaf(at.base, kLn2, logf(l_run)) : -__builtin_inff();
 }
 
-// Sequences with at most this many query rows (new tokens x heads of a group)
-// go to the decode kernel, 16 rows at a time; the others to the prompt kernel.
+// Sequences with at most this many query rows (new tokens x heads of a group) go
+// to the decode kernel, 16 rows at a time; the others to the prompt kernel.
 constexpr int kFewRows = 64;
 
 struct Plan {
-  int unit, extra, splits, per, nw, many, most_rows;
+  int unit, extra, each, splits, per, nw, many, most_rows;
   int64_t items, columns;   // grid: items x heads and blocks of a group's heads
-  bool prompts;
+  bool prompts, drafts;     // drafts: the draft kernel in the decode kernel's place
   int p_unit, p_splits, p_per;
   int64_t p_items;
 };
@@ -1027,55 +1324,94 @@ int64_t most_tiles(int64_t tiles, int64_t rows, int64_t window, int64_t sinks) {
   return n < tiles ? n : tiles;
 }
 
+template <Mask M>
 Plan plan(const Kv8& c, int64_t T, int64_t Hq, int64_t S, int64_t W, int64_t window = 0,
           int64_t sinks = 0) {
   Plan p{};
   const int64_t G = Hq / c.heads;
   // the packed batch says how many new tokens a sequence can have at most
   const int64_t longest = T;
+  // (D = 256: its state does not fit the registers)
+  p.drafts = M == Mask::kTree && T > S && G <= kDraftRows && c.dim <= 128;
   p.prompts = longest * G > kFewRows && T > S && G <= kPromptRows;
+  // Trees go to the draft kernel whole (the two kernels one after the other, each for
+  // some of the sequences, take longer than either: 215 us for 16 trees of up to 64
+  // tokens behind up to 8128, 8 heads of 4, 153 and 178 by themselves), unless they
+  // are so large that what the prompt kernel's four wavefronts share outweighs its
+  // barriers: from 256 rows (16 trees of up to 64, 8 heads of 8: 238 us, 397; one
+  // of 32 behind 31968, 256 rows: 101 us, 83), from 160 where they fill the chip.
+  if (p.drafts) p.prompts = T * G > 256 * S || (T * G > 160 * S && S * c.heads >= 128);
   p.many = p.prompts ? kFewRows : INT32_MAX;
-  p.unit = T > S && G <= 8 ? (int)(16 / G) : 1;
-  p.extra = p.unit > 1 ? 1 : 0;
-  p.items = T / p.unit + p.extra * S;
-  p.columns = c.heads * ((G + 15) / 16);
-  p.most_rows = (int)(p.unit * (G < 16 ? G : 16));
+  const int64_t all = ((W << c.bt_log2) + kTile - 1) / kTile;
+  if (p.drafts) {
+    p.unit = (int)(kDraftRows / G);
+    p.columns = c.heads;
+    p.most_rows = (int)(p.unit * G);
+    p.extra = 1;
+    p.items = T / p.unit + S;
+    p.nw = 4;
+    // about 1024 workgroups (two rounds) where the contexts are as long as the table
+    const int64_t tiles = most_tiles(all, p.unit, window, sinks);
+    const int64_t groups = (S > T / p.unit ? S : T / p.unit) * p.columns;
+    const int64_t cut = (tiles + kMaxSplits - 1) / kMaxSplits;
+    int64_t per = (groups * tiles + 1023) / 1024;
+    per = per > cut ? per : cut;
+    if (p.items * p.columns * cut > (1 << 20)) per = tiles;
+    p.per = (int)((per + p.nw - 1) / p.nw * p.nw);
+    p.splits = (int)((tiles + p.per - 1) / p.per);
+  } else {
+    p.unit = T > S && G <= 8 ? (int)(16 / G) : 1;
+    p.extra = p.unit > 1 ? 1 : 0;
+    p.items = T / p.unit + p.extra * S;
+    p.columns = c.heads * ((G + 15) / 16);
+    p.most_rows = (int)(p.unit * (G < 16 ? G : 16));
+    const int64_t units = (T < p.items ? T : p.items) * p.columns;
+    const int64_t tiles = most_tiles(all, p.unit, window, sinks);
+    // Every workgroup takes the same number of tiles, so that ragged sequences
+    // load the chip evenly: as many as make 2048 workgroups of sequences that
+    // fill their table rows (1024 for D = 256, whose registers leave room for half
+    // as many wavefronts: 121 against 140 us for 48 contexts to 4096), and no more
+    // than kMaxSplits parts of a sequence.
+    // Contexts of up to 24 tiles are not cut: eight wavefronts walk them in
+    // three steps, which costs less than the second launch that joins parts.
+    // (48 contexts to 8192 tokens, 8 heads: 111 us with parts of 24 tiles and 4
+    // wavefronts, 134 us with 8, 119 us with 10 tiles and 1; one context of
+    // 131071 tokens, 2 heads: 23.8 us with 128 parts, 26.7 with 64, 37 with 1
+    // wavefront.)
+    const int64_t cut = (tiles + kMaxSplits - 1) / kMaxSplits;
+    const int64_t wanted = c.dim == 256 ? 1024 : 2048;
+    int64_t per = (units * tiles + wanted - 1) / wanted;
+    per = per > cut ? per : cut;
+    p.nw = 4;
+    if (tiles <= 24) {
+      p.nw = c.dim == 256 ? 4 : 8;
+      per = tiles;
+    }
+    if (p.items * p.columns * cut > (1 << 20)) per = tiles;
+    per = (per + p.nw - 1) / p.nw * p.nw;
+    p.per = (int)per;
+    p.splits = (int)((tiles + per - 1) / per);
+  }
+  if (p.prompts) {
+    // The sequences of the decode or draft kernel have few tokens then, so that their
+    // items can be counted by sequence: a workgroup for every token of the prompts, to
+    // find that it has nothing to do, takes as long as some prompts' attention (33 us
+    // of 245 under a window of 1024).
+    const int64_t each = (kFewRows / G + p.unit - 1) / p.unit;
+    if (S * each < p.items) {
+      p.each = (int)each;
+      p.items = S * each;
+    }
+  }
   p.p_unit = (int)(kPromptRows / (G < kPromptRows ? G : kPromptRows));
   p.p_items = T / p.p_unit + S;
-  const int64_t units = (T < p.items ? T : p.items) * p.columns;
-  const int64_t all = ((W << c.bt_log2) + kTile - 1) / kTile;
-  const int64_t tiles = most_tiles(all, p.unit, window, sinks);
-  // Every workgroup takes the same number of tiles, so that ragged sequences
-  // load the chip evenly: as many as make 2048 workgroups of sequences that
-  // fill their table rows (1024 for D = 256, whose registers leave room for half
-  // as many wavefronts: 121 against 140 us for 48 contexts to 4096), and no more
-  // than kMaxSplits parts of a sequence.
-  // Contexts of up to 24 tiles are not cut: eight wavefronts walk them in
-  // three steps, which costs less than the second launch that joins parts.
-  // (48 contexts to 8192 tokens, 8 heads: 111 us with parts of 24 tiles and 4
-  // wavefronts, 134 us with 8, 119 us with 10 tiles and 1; one context of
-  // 131071 tokens, 2 heads: 23.8 us with 128 parts, 26.7 with 64, 37 with 1
-  // wavefront.)
-  const int64_t cut = (tiles + kMaxSplits - 1) / kMaxSplits;
-  const int64_t wanted = c.dim == 256 ? 1024 : 2048;
-  int64_t per = (units * tiles + wanted - 1) / wanted;
-  per = per > cut ? per : cut;
-  p.nw = 4;
-  if (tiles <= 24) {
-    p.nw = c.dim == 256 ? 4 : 8;
-    per = tiles;
-  }
-  if (p.items * p.columns * cut > (1 << 20)) per = tiles;
-  per = (per + p.nw - 1) / p.nw * p.nw;
-  p.per = (int)per;
-  const int64_t sp = (tiles + per - 1) / per;
-  p.splits = (int)sp;
   // Prompts: where the items do not fill the chip (two workgroups per CU), the
   // tiles of each are cut, into parts of at least 16 tiles: a part costs a pass
   // over its rows in fp32, there and back. (A chunk of 600 tokens behind 29400,
   // 8 heads of 4: 535 us cut, 949 us whole.)
   const int64_t work = p.p_items * c.heads;
-  int64_t ps = 512 / (work < 1 ? 1 : work);
+  // (Trees hardly ever fill their last item, so that there are fewer.)
+  int64_t ps = (p.drafts ? 1024 : 512) / (work < 1 ? 1 : work);
   const int64_t p_tiles = most_tiles(all, p.p_unit, window, sinks);
   ps = ps < p_tiles / 16 ? ps : p_tiles / 16;
   ps = ps < 1 ? 1 : ps > kFewParts ? kFewParts : ps;
@@ -1084,9 +1420,9 @@ Plan plan(const Kv8& c, int64_t T, int64_t Hq, int64_t S, int64_t W, int64_t win
   return p;
 }
 
-// bytes of the decode kernel's parts, then of the prompt kernel's
+// bytes of the decode or draft kernel's parts, then of the prompt kernel's
 int64_t decode_bytes(const Plan& p, const Kv8& c) {
-  return p.splits > 1 ? p.items * p.columns * p.splits * 16 * (c.dim + 2) * 4 : 0;
+  return p.splits > 1 ? p.items * p.columns * p.splits * (p.drafts ? kDraftRows : 16) * (c.dim + 2) * 4 : 0;
 }
 int64_t prompt_bytes(const Plan& p, const Kv8& c) {
   return p.prompts && p.p_splits > 1
@@ -1094,13 +1430,20 @@ int64_t prompt_bytes(const Plan& p, const Kv8& c) {
 }
 
 template <Mask M>
+int64_t attention_work(const Kv8& c, int64_t T, int64_t Hq, int64_t S, int64_t W, int64_t window = 0,
+                       int64_t sinks = 0) {
+  const Plan p = plan<M>(c, T, Hq, S, W, window, sinks);
+  return decode_bytes(p, c) + prompt_bytes(p, c);
+}
+
+template <Mask M>
 hipError_t launch_attention(const Kv8& c, int dt, const void* q, int64_t ldq, int64_t T, int64_t Hq,
                             const int32_t* table, const int32_t* lens, const int32_t* cu, int64_t S,
                             int64_t W, int64_t window, int64_t sinks, const int32_t* parent,
                             float scale, void* out, float* lse, float* ws, hipStream_t st) {
-  const Plan p = plan(c, T, Hq, S, W, window, sinks);
+  const Plan p = plan<M>(c, T, Hq, S, W, window, sinks);
   AttnArgs a{c, {table, lens, cu, (int)S, (int)W, (int)T}, static_cast<const uint16_t*>(q), ldq,
-             (int)(Hq / c.heads), p.unit, p.extra, p.many, fabsf(scale) * kLog2e,
+             (int)(Hq / c.heads), p.unit, p.extra, (int)p.items, p.each, p.many, fabsf(scale) * kLog2e,
              scale < 0 ? 0x80008000u : 0u, static_cast<uint16_t*>(out), lse, p.splits, p.per, ws,
              (int)window, (int)sinks, parent};
   const dim3 grid((unsigned)p.items, (unsigned)p.columns, (unsigned)p.splits);
@@ -1109,14 +1452,25 @@ hipError_t launch_attention(const Kv8& c, int dt, const void* q, int64_t ldq, in
       hipLaunchKernelGGL((kv8_join_few_kernel<M, T_, D, R>),
                          dim3(units, (unsigned)((rows + 512 / D - 1) / (512 / D))), dim3(256), 0, st, x);
     else
-      hipLaunchKernelGGL((kv8_join_kernel<M, T_, D>), dim3(units, (unsigned)rows), dim3(256), 0, st, x);
+      hipLaunchKernelGGL((kv8_join_kernel<M, T_, D, R == kPromptRows ? 16 : R>), dim3(units, (unsigned)rows),
+                         dim3(256), 0, st, x);
   };
   auto go = [&]<class T_, int D>() {
     auto decode = [&]<int BT>() {
+      if constexpr (M == Mask::kTree && D <= 128)
+        if (p.drafts) {
+          const int64_t units = (p.items + kBundle - 1) / kBundle * p.columns * p.splits;
+          hipLaunchKernelGGL((kv8_draft_kernel<T_, D, BT, 4>), dim3((unsigned)((units + 7) / 8 * 8 * kBundle)), dim3(256),
+                             4 * kDraftRows * draft_row(D) * 4, st, a);
+          if (p.splits > 1)
+            join.template operator()<T_, D, kDraftRows>(a, (unsigned)(p.items * p.columns), p.most_rows);
+          return;
+        }
       auto waves = [&]<int NW>() {
         hipLaunchKernelGGL((kv8_decode_kernel<M, T_, D, BT, NW>), grid, dim3(64 * NW), NW * 16 * D * 4,
                            st, a);
       };
+      if (p.items == 0) return;
       if (p.nw == 4) waves.template operator()<4>();
       else waves.template operator()<D == 256 ? 4 : 8>();
       if (p.splits > 1)
@@ -1129,6 +1483,8 @@ hipError_t launch_attention(const Kv8& c, int dt, const void* q, int64_t ldq, in
     AttnArgs b = a;
     b.unit = p.p_unit;
     b.extra = 1;
+    b.items = (int)p.p_items;
+    b.each = 0;
     b.splits = p.p_splits;
     b.per = p.p_per;
     b.ws = ws + decode_bytes(p, c) / 4;

@@ -5,6 +5,10 @@
 
 namespace qmm {
 
+int64_t kv8_attention_tree_work(const Kv8& c, int64_t T, int64_t Hq, int64_t S, int64_t W) {
+  return attention_work<Mask::kTree>(c, T, Hq, S, W);
+}
+
 hipError_t launch_kv8_attention_tree(const Kv8& c, int dt, const void* q, int64_t ldq, int64_t T,
                                      int64_t Hq, const int32_t* table, const int32_t* lens,
                                      const int32_t* cu, int64_t S, int64_t W, const int32_t* parent,

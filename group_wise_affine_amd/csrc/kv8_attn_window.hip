@@ -7,8 +7,7 @@ namespace qmm {
 
 int64_t kv8_attention_window_work(const Kv8& c, int64_t T, int64_t Hq, int64_t S, int64_t W,
                                   int64_t window, int64_t sinks) {
-  const Plan p = plan(c, T, Hq, S, W, window, sinks);
-  return decode_bytes(p, c) + prompt_bytes(p, c);
+  return attention_work<Mask::kWindow>(c, T, Hq, S, W, window, sinks);
 }
 
 hipError_t launch_kv8_attention_window(const Kv8& c, int dt, const void* q, int64_t ldq, int64_t T,

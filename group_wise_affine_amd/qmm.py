@@ -27,7 +27,8 @@ EXPORTS = ["qmm_quantize", "qmm_dequantize", "qmm_t", "qmv", "qmm_n", "qconv2d_n
            "qmm_affine_pack", "qmv_affine_packed", "qmm_t_affine_packed",
            "qmm_i8_quantize", "qmm_i8_t_work", "qmm_i8_t", "qmm_i8_linear_work", "qmm_i8_linear",
            "qmm_kv8_append", "qmm_kv8_read", "qmm_kv8_attention_work", "qmm_kv8_attention",
-           "qmm_kv8_attention_window_work", "qmm_kv8_attention_window", "qmm_kv8_attention_tree",
+           "qmm_kv8_attention_window_work", "qmm_kv8_attention_window",
+           "qmm_kv8_attention_tree_work", "qmm_kv8_attention_tree",
            "qmm_qk_norm_rope", "qmm_logprobs_work", "qmm_logprobs",
            "qmm_kv8_pages_work", "qmm_kv8_update", "qmm_kv8_compact", "qmm_kv8_copy",
            "qmm_crossover_m", "qmm_route", "qmm_force_kernel", "qmm_last_error"]
@@ -105,12 +106,12 @@ def lib():
                   "qmm_logprobs"):
             getattr(L, f).restype = i32
         L.qmm_i8_t_work.argtypes = L.qmm_i8_linear_work.argtypes = [i64, i64, i64]
-        L.qmm_kv8_attention_work.argtypes = [vp, i64, i64, i64, i64]
+        L.qmm_kv8_attention_tree_work.argtypes = L.qmm_kv8_attention_work.argtypes = [vp, i64, i64, i64, i64]
         L.qmm_kv8_attention_window_work.argtypes = [vp, i64, i64, i64, i64, i64, i64]
         L.qmm_logprobs_work.argtypes = [i32, i64, i64, i64]
         L.qmm_kv8_pages_work.argtypes = [i64]
         for f in ("qmm_i8_t_work", "qmm_i8_linear_work", "qmm_kv8_attention_work",
-                  "qmm_kv8_attention_window_work", "qmm_logprobs_work", "qmm_kv8_pages_work"):
+                  "qmm_kv8_attention_window_work", "qmm_kv8_attention_tree_work", "qmm_logprobs_work", "qmm_kv8_pages_work"):
             getattr(L, f).restype = i64
         L.qmm_crossover_m.argtypes = [i32, i32, i32, i64, i64]
         L.qmm_crossover_m.restype = i64

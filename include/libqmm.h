@@ -583,9 +583,11 @@ qmm_status qmm_kv8_attention_window(const qmm_kv8_cache* cache, const void* q, i
  * the tree (longer prompts in one batch with drafts) are causal, and their
  * parents are not read. Where each token's parent is the one before it this is
  * qmm_kv8_attention. The tokens lie in the cache in the order of the batch, one
- * position each, whatever their depth. Scratch: qmm_kv8_attention_work.
+ * position each, whatever their depth.
  */
 #define QMM_TREE_TOKENS 64
+int64_t qmm_kv8_attention_tree_work(const qmm_kv8_cache* cache, int64_t T, int64_t q_heads, int64_t S,
+                                    int64_t W);
 qmm_status qmm_kv8_attention_tree(const qmm_kv8_cache* cache, const void* q, int64_t ldq,
                                   qmm_dtype dt, int64_t T, int64_t q_heads, const int32_t* table,
                                   const int32_t* lens, const int32_t* cu, int64_t S, int64_t W,

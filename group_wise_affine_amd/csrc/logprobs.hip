@@ -5,7 +5,7 @@
 //
 // A lane holds the running maximum m of what it has seen, S = sum 2^y and
 // Y = sum y 2^y with y = (x - m) log2 e, so that entropy = ln 2 (log2 S - Y / S)
-// and a logarithm of a probability is (x - m) - ln 2 log2 S: no difference of large
+// and a logarithm of a probability is ln 2 (y - log2 S): no difference of large
 // numbers.
 //
 // The K most likely (K <= 64) are a sorted list, one entry per lane of a
@@ -14,7 +14,8 @@
 // first. Each wavefront keeps the list of what it has seen; elements above the
 // list's K-th value go to a buffer, and 64 of them at a time are sorted and merged
 // in (bitonic networks over the lanes). A first bound is the K-th largest of the
-// lanes' maxima.
+// lanes' maxima; of the elements that equal it only the first ones are taken, so
+// that a plateau (a mask of the type's lowest value) does not fill the buffer.
 //
 // A row's elements are cut over wavefronts, and over workgroups where there are
 // few rows; their sums and lists are joined in their order.
@@ -26,8 +27,8 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kWaves = 4;   // of a workgroup
 constexpr int kAhead = 4;   // loads in flight per lane
+constexpr int kBuffer = 32 + 512;   // keys of a wavefront's buffer: what is left, and a load of each lane
 
 struct LogprobArgs {
   const void* x;
@@ -107,12 +108,22 @@ __device__ __forceinline__ float from_ordered(uint32_t o) {
 __device__ __forceinline__ float max_or_nan(float a, float b) { return __builtin_elementwise_maximum(a, b); }
 
 // ------------------------------------------------------------- running sums
+// m: the largest, NaN once a NaN was seen; s and y relative to c = fl(m log2 e)
+// (while that is finite; beyond, differences come before the product)
 struct Sums {
-  float m, s, y;   // m: NaN once a NaN was seen
+  float m, s, y;
 };
-// (differences first: a product with log2 e may leave the range)
+constexpr float kBig = 1e38f;
+// y of an element
+__device__ __forceinline__ float power(float x, float m) {
+  const float c = m * kLog2e;
+  return fabsf(m) < kBig ? fmaf(x, kLog2e, -c) : (x - m) * kLog2e;
+}
+// what y changes by when m goes from `from` to `to`
 __device__ __forceinline__ float shift(float from, float to) {
-  return from == to ? 0.0f : (from - to) * kLog2e;
+#pragma clang fp contract(off)
+  const float a = from * kLog2e, b = to * kLog2e;   // (fused, the two would not be those that were taken)
+  return from == to ? 0.0f : fabsf(to) < kBig && fabsf(from) < kBig ? a - b : (from - to) * kLog2e;
 }
 __device__ __forceinline__ Sums raised(Sums a, float m) {
   const float d = fmaxf(shift(a.m, m), -200.0f), f = __builtin_amdgcn_exp2f(d);
@@ -123,12 +134,24 @@ __device__ __forceinline__ Sums join(const Sums& a, const Sums& b) {
   const Sums p = raised(a, m), q = raised(b, m);
   return {m, p.s + q.s, p.y + q.y};
 }
-template <int X>
-__device__ __forceinline__ Sums join_across(const Sums& a) {
-  const Sums b = {__builtin_bit_cast(float, across<X>(__builtin_bit_cast(uint32_t, a.m))),
-                  __builtin_bit_cast(float, across<X>(__builtin_bit_cast(uint32_t, a.s))),
-                  __builtin_bit_cast(float, across<X>(__builtin_bit_cast(uint32_t, a.y)))};
-  return join(a, b);
+// the lanes' sums joined: the largest first, so that each lane's are scaled once
+template <class F>
+__device__ __forceinline__ float fold(float v, F f) {
+  auto step = [&]<int X>() QMM_INLINE {
+    v = f(v, __builtin_bit_cast(float, across<X>(__builtin_bit_cast(uint32_t, v))));
+  };
+  step.template operator()<1>();
+  step.template operator()<2>();
+  step.template operator()<7>();
+  step.template operator()<15>();
+  step.template operator()<16>();
+  step.template operator()<32>();
+  return v;
+}
+__device__ __forceinline__ Sums join_lanes(const Sums& a) {
+  const Sums b = raised(a, fold(a.m, max_or_nan));
+  auto add = [](float x, float y) QMM_INLINE { return x + y; };
+  return {b.m, fold(b.s, add), fold(b.y, add)};
 }
 
 template <class T>
@@ -152,93 +175,153 @@ __device__ __forceinline__ void unpack(const u32x4_t& u, float* v) {
 template <bool TOP>
 struct Seen {
   Sums sums{-__builtin_inff(), 0.0f, 0.0f};
-  uint64_t list = 0;
-  float above = __builtin_nanf("");   // only larger ones may enter the list (NaN: any)
-  int held = 0;                       // elements in the buffer, below 64
-  uint64_t* buffer;                   // [128], the wavefront's
+  bool big = false;                   // some lane's largest is no factor of log2 e
+  uint64_t list = 0;                  // (-inf never enters: write_row() puts it in where it is needed)
+  float above = -__builtin_inff();    // only larger ones may enter the list,
+  float from = 0.0f;                  // and while `open` the first ones that equal this, the next number
+  bool open = false;
+  int ties = 0;                       // of those seen
+  int held = 0;                       // elements in the buffer, below 32 between loads
+  uint64_t* buffer;                   // [kBuffer], the wavefront's
   int top;
 
-  __device__ __forceinline__ void flush() {   // the first 64 of the buffer
-    const int lane = threadIdx.x % 64;
+  __device__ __forceinline__ void flush() {   // the last 64 of the buffer
+    const int lane = threadIdx.x % 64, first = max(held - 64, 0);
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    const uint64_t k = lane < held ? buffer[lane] : 0, rest = buffer[64 + lane];
+    const uint64_t k = sort64(first + lane < held ? buffer[first + lane] : 0);
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    buffer[lane] = rest;
-    held = max(held - 64, 0);
-    list = merge64(list, sort64(k));
-    bound(__builtin_amdgcn_readlane((uint32_t)(list >> 32), top - 1));
-  }
-  // elements equal to the K-th of the list come later than it
-  __device__ __forceinline__ void bound(uint32_t kth) {
-    if (kth != 0) above = from_ordered(kth);
-  }
-  // N elements of each lane, the first with index i; none where !valid
-  template <int N>
-  __device__ __forceinline__ void take(const float* x, uint32_t i, bool valid) {
-    float mx = x[0];
-    if constexpr (N == 4) mx = max_or_nan(max_or_nan(x[0], x[1]), max_or_nan(x[2], x[3]));
-    if constexpr (N == 8)
-      mx = max_or_nan(max_or_nan(max_or_nan(max_or_nan(x[0], x[1]), x[2]), max_or_nan(max_or_nan(x[3], x[4]), x[5])),
-                      max_or_nan(x[6], x[7]));
-    if (__any(valid && !(mx <= sums.m))) {
-      const float m = valid ? max_or_nan(sums.m, mx) : sums.m;
-      sums = raised(sums, m);
-    }
-#pragma unroll
-    for (int j = 0; j < N; j++) {
-      // (what is -inf weighs nothing; 2^-200 is 0)
-      const float y = valid ? fmaxf((x[j] - sums.m) * kLog2e, -200.0f) : -200.0f, e = __builtin_amdgcn_exp2f(y);
-      sums.s += e;
-      sums.y = fmaf(e, y, sums.y);
-    }
-    if constexpr (!TOP) return;
-    if (__any(valid && !(mx <= above))) {
-      const float at = above;   // (the same for all, in whatever order they come)
-#pragma unroll
-      for (int j = 0; j < N; j++) {
-        const bool in = valid && !(x[j] <= at);
-        const uint64_t who = __ballot(in);
-        if (who != 0) {
-          const int to = held + __builtin_amdgcn_mbcnt_hi((uint32_t)(who >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)who, 0));
-          if (in) buffer[to] = (uint64_t)ordered(x[j]) << 32 | (uint32_t)~(i + j);
-          held += __builtin_popcountll(who);
-          if (held >= 64) flush();
-        }
-      }
+    held = first;
+    list = merge64(list, k);
+    const uint32_t kth = __builtin_amdgcn_readlane((uint32_t)(list >> 32), top - 1);
+    if (kth != 0) {   // (what equals it and comes with a later load comes later than it)
+      above = from_ordered(kth);
+      open = false;
     }
   }
-  // a first bound: the K-th largest of the lanes' maxima (0: a lane without any)
+  // a first bound: the K-th largest of the lanes' maxima
   __device__ __forceinline__ void first_bound(uint32_t largest) {
     const uint32_t kth = __builtin_amdgcn_readlane(sort64(largest), top - 1);
-    if (kth == 0) return;
-    // from it on: above the number before it, which is not -0
-    above = from_ordered(kth - (kth == 0x80000000u ? 2 : 1));
+    if (kth <= 0x007fffffu) return;   // -inf
+    from = from_ordered(kth);
+    above = from_ordered(kth - (kth == 0x80000000u ? 2 : 1));   // (the number before 0 is not -0)
+    open = true;
+  }
+  // the sums of N elements of each lane, -inf where there is none; whether some may
+  // enter the list
+  template <int N>
+  __device__ __forceinline__ bool take(const float* x) {
+    float mx = max_or_nan(max_or_nan(max_or_nan(x[0], x[1]), x[2]), x[3]);
+    if constexpr (N == 8) mx = max_or_nan(max_or_nan(mx, max_or_nan(max_or_nan(x[4], x[5]), x[6])), x[7]);
+    if (__any(!(mx <= sums.m))) {
+      sums = raised(sums, max_or_nan(sums.m, mx));
+      big = __any(fabsf(sums.m) >= kBig && sums.m > -__builtin_inff());
+    }
+    // (what is -inf weighs nothing; 2^-200 is 0)
+    auto add = [&](float p) QMM_INLINE {
+      const float y = fmaxf(p, -200.0f), e = __builtin_amdgcn_exp2f(y);
+      sums.s += e;
+      sums.y = fmaf(e, y, sums.y);
+    };
+    if (!big) {
+      const float c = -sums.m * kLog2e;
+#pragma unroll
+      for (int j = 0; j < N; j++) add(fmaf(x[j], kLog2e, c));
+    } else {
+#pragma unroll
+      for (int j = 0; j < N; j++) add(power(x[j], sums.m));
+    }
+    return TOP && __any(mx > above);
+  }
+  // the first element's index is i
+  template <int N>
+  __device__ __forceinline__ void push(const float* x, uint32_t i) {
+    auto enter = [&](int j, bool in) QMM_INLINE {
+      const uint64_t who = __ballot(in);
+      if (who == 0) return;
+      if (in) buffer[held + below(who)] = (uint64_t)ordered(x[j]) << 32 | (uint32_t)~(i + j);
+      held += __builtin_popcountll(who);
+    };
+    if (!open) {
+#pragma unroll
+      for (int j = 0; j < N; j++) enter(j, x[j] > above);
+    } else {
+      // of many equal ones the first lanes' are enough
+      bool any = false;
+#pragma unroll
+      for (int j = 0; j < N; j++) any |= x[j] == from;
+      const bool mine = (int)below(__ballot(any)) < top;
+#pragma unroll
+      for (int j = 0; j < N; j++) {
+        ties += __builtin_popcountll(__ballot(mine && x[j] == from));
+        enter(j, x[j] > above && (mine || x[j] != from));
+      }
+      if (ties >= top) {
+        above = from;
+        open = false;
+      }
+    }
+    // (an old bound lets more in than a new one costs: 32 rather than 64)
+    while (held >= 32) flush();
+  }
+  static __device__ __forceinline__ uint32_t below(uint64_t who) {   // how many of them are lanes before this one
+    return __builtin_amdgcn_mbcnt_hi((uint32_t)(who >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)who, 0));
   }
 };
 
+template <class T>
 __device__ __forceinline__ void write_row(const LogprobArgs& a, int64_t row, const Sums& r, uint64_t list, float x_token) {
   const int lane = threadIdx.x % 64;
-  const bool bad = !(r.m < __builtin_inff()), none = r.s == 0.0f;
-  const float nan = __builtin_nanf(""), ls = none ? 0.0f : __log2f(r.s);
-  auto lp = [&](float x) QMM_INLINE {
-    return bad ? nan : x == -__builtin_inff() ? x : fmaf(-kLn2, ls, x - r.m);
-  };
+  const float inf = __builtin_inff(), nan = __builtin_nanf("");
+  const bool bad = !(r.m < inf), none = r.s == 0.0f;
+  const float ls = none ? 0.0f : __log2f(r.s);
+  auto lp = [&](float x) QMM_INLINE { return bad ? nan : x == -inf ? x : kLn2 * (power(x, r.m) - ls); };
   if (lane == 0) {
     a.logprob[row] = lp(x_token);
     a.entropy[row] = bad ? nan : none ? 0.0f : fmaxf(kLn2 * (ls - r.y / r.s), 0.0f);
   }
-  if (lane < a.top) {
+  const bool there = lane < a.top && (bad || list != 0);
+  if (there) {
     a.ids[row * a.top + lane] = bad ? -1 : (int32_t)~(uint32_t)list;
     a.top_lp[row * a.top + lane] = lp(from_ordered((uint32_t)(list >> 32)));
   }
+  // fewer than K that can be: the first of the others, which are as many as it takes
+  int have = __builtin_popcountll(__ballot(there));
+  for (int i = lane; have < a.top && __any(i < a.V); i += 64) {
+    const bool in = i < a.V && element<T>(a.x, row * a.ld + i) == -inf;
+    const uint64_t who = __ballot(in);
+    const int to = have + (int)Seen<true>::below(who);
+    if (in && to < a.top) {
+      a.ids[row * a.top + to] = i;
+      a.top_lp[row * a.top + to] = -inf;
+    }
+    have += __builtin_popcountll(who);
+  }
 }
 
-// One part of a row. Wavefronts take steps of kAhead loads in turn.
-template <class T, bool TOP>
-__global__ __launch_bounds__(64 * kWaves) void logprobs_kernel(LogprobArgs a) {
+// Joins W wavefronts' sums and lists in pairs; the first one has the result. Lists
+// go through lists, `stride` keys per wavefront.
+template <int W, bool TOP>
+__device__ __forceinline__ void join_waves(Sums& s, uint64_t& list, Sums* sums, uint64_t* lists, int stride, int wave) {
+  const int lane = threadIdx.x % 64;
+#pragma unroll
+  for (int d = W / 2; d >= 1; d >>= 1) {
+    if (wave >= d && wave < 2 * d) {
+      if (lane == 0) sums[wave] = s;
+      if (TOP) lists[wave * stride + lane] = list;
+    }
+    __syncthreads();
+    if (wave < d) {
+      s = join(s, sums[wave + d]);
+      if (TOP) list = merge64(list, lists[(wave + d) * stride + lane]);
+    }
+  }
+}
+
+// One part of a row; each wavefront takes a run of loads, kAhead of them in flight.
+template <class T, bool TOP, int kWaves>
+__global__ __launch_bounds__(64 * kWaves, 8) void logprobs_kernel(LogprobArgs a) {
   constexpr int N = __is_same(T, F32) ? 4 : 8;   // elements of a load
-  constexpr int kStep = 64 * kAhead;             // loads of a wavefront's step
-  __shared__ uint64_t buffers[kWaves][128];
+  __shared__ uint64_t buffers[TOP ? kWaves * kBuffer : 1];
   __shared__ Sums sums[kWaves];
   const int tid = threadIdx.x, lane = tid % 64;
   const int wave = __builtin_amdgcn_readfirstlane(tid / 64);
@@ -251,114 +334,150 @@ __global__ __launch_bounds__(64 * kWaves) void logprobs_kernel(LogprobArgs a) {
   const int head = min(V, (int)((16 - (reinterpret_cast<uintptr_t>(x) & 15)) & 15) / (int)sizeof(W));
   const int loads = (V - head) / N, tail = V - head - loads * N;
   const u32x4_t* body = reinterpret_cast<const u32x4_t*>(x + head);
-  const int steps = (loads + kStep - 1) / kStep, per = (steps + a.parts - 1) / a.parts;
-  const int first = part * per, last = min(first + per, steps);
+  // the part's loads; the wavefronts take 64 of them in turn
+  const int run = ((loads + a.parts - 1) / a.parts + 63) / 64 * 64;
+  const int first = min(part * run, loads), last = min(first + run, loads);
+  const int turns = max(((last - first + 63) / 64 - wave + kWaves - 1) / kWaves, 0);
+  const int batches = (turns + kAhead - 1) / kAhead;
+  const bool has_head = part == 0 && wave == 0 && head > 0;
+  const bool has_tail = part == a.parts - 1 && wave == kWaves - 1 && tail > 0;
   const int32_t token = a.tokens[row];
   float x_token = -__builtin_inff();
   if (a.parts == 1 && token >= 0 && token < V) x_token = element<T>(x, token);
 
+  constexpr uint32_t kNone = __is_same(T, F16) ? 0xfc00fc00u : __is_same(T, BF16) ? 0xff80ff80u : 0xff800000u;   // -inf
+  const u32x4_t none = {kNone, kNone, kNone, kNone};
   Seen<TOP> seen;
-  seen.buffer = buffers[wave];
+  seen.buffer = buffers + wave * kBuffer;
   seen.top = a.top;
-  if (part == 0 && wave == 0 && head > 0) {
-    const float e = element<T>(x, lane < head ? lane : 0);
-    seen.template take<1>(&e, lane, lane < head);
-  }
-  bool fresh = true;
-  for (int step = first + wave; step < last; step += kWaves) {
+  // the elements before, the loads, the elements after, in one loop: the code that
+  // enters elements into the list stands once (as often as there are loads ahead, it
+  // does not fit the instruction cache: 167 us for 2048 rows of 128000, 131 so)
+  for (int b = has_head ? -1 : 0; b < batches + (has_tail ? 1 : 0); b++) {
     u32x4_t u[kAhead];
-    const int at = step * kStep + lane;
-    const bool whole = (step + 1) * kStep <= loads;
+    int count = 1, at = 0, next = 0;   // loads, the first one's first element, from one to the next
+    if (b >= 0 && b < batches) {
+      constexpr int kTurn = 64 * kWaves;
+      const int from = first + b * (kTurn * kAhead) + wave * 64 + lane;
+      count = min(turns - b * kAhead, kAhead);
+      at = head + from * N;
+      next = kTurn * N;
 #pragma unroll
-    for (int i = 0; i < kAhead; i++) u[i] = body[whole ? at + i * 64 : min(at + i * 64, loads - 1)];
-    if (TOP && fresh) {
-      fresh = false;
-      uint32_t largest = 0;
+      for (int i = 0; i < kAhead; i++)
+        if (i < count) u[i] = body[min(from + i * kTurn, last - 1)];
+      if (b == batches - 1)
 #pragma unroll
-      for (int i = 0; i < kAhead; i++) {
+        for (int i = 0; i < kAhead; i++)
+          if (from + i * kTurn >= last) u[i] = none;
+      if (TOP && b == 0) {
+        uint32_t largest = 0;
+#pragma unroll
+        for (int i = 0; i < kAhead; i++) {
+          float v[N];
+          unpack<T>(u[i], v);
+#pragma unroll
+          for (int j = 0; j < N; j++) {
+            const uint32_t o = ordered(v[j]);
+            largest = o > largest ? o : largest;
+          }
+        }
+        seen.first_bound(largest);
+      }
+    } else {
+      const int edge = b < 0 ? lane : V - tail + lane;
+      at = edge;
+      u[0] = none;
+      if (lane < (b < 0 ? head : tail)) {
+        if constexpr (__is_same(T, F32)) u[0][0] = __builtin_bit_cast(uint32_t, x[edge]);
+        else u[0][0] = x[edge] | (kNone & 0xffff0000u);
+      }
+    }
+    uint32_t enter = 0;   // loads with elements for the list
+#pragma unroll
+    for (int i = 0; i < kAhead; i++)
+      if (i < count) {
         float v[N];
         unpack<T>(u[i], v);
-#pragma unroll
-        for (int j = 0; j < N; j++) {
-          const uint32_t o = ordered(v[j]);
-          if (at + i * 64 < loads && o > largest) largest = o;
-        }
+        enter |= seen.template take<N>(v) ? 1u << i : 0;
       }
-      if (!(seen.above == seen.above)) seen.first_bound(largest);
-    }
+    while (enter != 0) {
+      const int i = __builtin_ctz(enter);
+      enter &= enter - 1;
+      u32x4_t w = u[0];
 #pragma unroll
-    for (int i = 0; i < kAhead; i++) {
+      for (int j = 1; j < kAhead; j++)
+        if (i == j) {
+          w = u[j];
+          asm volatile("" : "+v"(w));   // (moved where it is, rather than chosen lane by lane)
+        }
       float v[N];
-      unpack<T>(u[i], v);
-      seen.template take<N>(v, (uint32_t)(head + (at + i * 64) * N), whole || at + i * 64 < loads);
+      unpack<T>(w, v);
+      seen.template push<N>(v, (uint32_t)(at + i * next));
     }
-  }
-  if (part == a.parts - 1 && wave == kWaves - 1 && tail > 0) {
-    const int i = V - tail + lane;
-    const float e = element<T>(x, lane < tail ? i : 0);
-    seen.template take<1>(&e, i, lane < tail);
   }
   if (TOP && seen.held > 0) seen.flush();
-  Sums s = join_across<32>(join_across<16>(join_across<8>(join_across<4>(join_across<2>(join_across<1>(seen.sums))))));
-  if (lane == 0) sums[wave] = s;
-  if (TOP) buffers[wave][lane] = seen.list;
-  __syncthreads();
-  if (wave > 0) return;
-  s = sums[0];
+  Sums s = join_lanes(seen.sums);
   uint64_t list = seen.list;
-#pragma unroll
-  for (int w = 1; w < kWaves; w++) {
-    s = join(s, sums[w]);
-    if (TOP) list = merge64(list, buffers[w][lane]);
-  }
+  join_waves<kWaves, TOP>(s, list, sums, buffers, kBuffer, wave);
+  if (wave > 0) return;
   if (a.parts == 1) {
-    write_row(a, row, s, list, x_token);
+    write_row<T>(a, row, s, list, x_token);
   } else {
     if (lane == 0) a.sums[blockIdx.x] = make_float4(s.m, s.s, s.y, 0.0f);
     if (lane < a.top) a.lists[(int64_t)blockIdx.x * a.top + lane] = list;
   }
 }
 
-// Joins a row's parts.
-constexpr int kJoinWaves = 8;
-template <class T>
+// Joins a row's parts: all of them are asked for at once.
+constexpr int kJoinWaves = 8, kMaxParts = 16;
+template <class T, bool TOP>
 __global__ __launch_bounds__(64 * kJoinWaves) void logprobs_join_kernel(LogprobArgs a) {
-  __shared__ uint64_t lists[kJoinWaves][64];
+  constexpr int kEach = kMaxParts / kJoinWaves;
+  __shared__ uint64_t lists[kJoinWaves * 64];
   __shared__ Sums sums[kJoinWaves];
   const int tid = threadIdx.x, lane = tid % 64;
   const int wave = __builtin_amdgcn_readfirstlane(tid / 64);
   const int64_t row = blockIdx.x;
+  float4 v[kEach];
+  uint64_t k[kEach];
+#pragma unroll
+  for (int i = 0; i < kEach; i++) {
+    const int p = i * kJoinWaves + wave;
+    if (p < a.parts) {
+      v[i] = a.sums[row * a.parts + p];
+      if (TOP) k[i] = lane < a.top ? a.lists[(row * a.parts + p) * a.top + lane] : 0;
+    }
+  }
   const int32_t token = a.tokens[row];
   float x_token = -__builtin_inff();
   if (token >= 0 && token < a.V) x_token = element<T>(a.x, row * a.ld + token);
   Sums s{-__builtin_inff(), 0.0f, 0.0f};
   uint64_t list = 0;
-  for (int p = wave; p < a.parts; p += kJoinWaves) {
-    const float4 v = a.sums[row * a.parts + p];
-    const uint64_t k = lane < a.top ? a.lists[(row * a.parts + p) * a.top + lane] : 0;
-    s = join(s, Sums{v.x, v.y, v.z});
-    if (a.top > 0) list = merge64(list, k);
-  }
-  if (lane == 0) sums[wave] = s;
-  lists[wave][lane] = list;
-  __syncthreads();
-  if (wave > 0) return;
 #pragma unroll
-  for (int w = 1; w < kJoinWaves; w++) {
-    s = join(s, sums[w]);
-    if (a.top > 0) list = merge64(list, lists[w][lane]);
-  }
-  write_row(a, row, s, list, x_token);
+  for (int i = 0; i < kEach; i++)
+    if (i * kJoinWaves + wave < a.parts) {
+      s = join(s, Sums{v[i].x, v[i].y, v[i].z});
+      if (TOP) list = i == 0 ? k[i] : merge64(list, k[i]);
+    }
+  join_waves<kJoinWaves, TOP>(s, list, sums, lists, 64, wave);
+  if (wave == 0) write_row<T>(a, row, s, list, x_token);
 }
 
-// Parts of a row: enough workgroups for the chip (1024), a step at least for each
-// wavefront of a part, and no more parts than the join takes well.
+// A row is a workgroup's where there are many, and cut into parts where there are
+// few: up to 512 workgroups of 16 parts at most, and a load at least for each lane of
+// them. (64 rows of 128000 in bf16, 20 tokens: 20 us with 8 parts, 29 with 2, 38 whole;
+// 256 rows: 39 with 2, 40 whole, 46 with 8.)
+constexpr int kSomeWaves = 8;
 int parts_of(int dt, int64_t M, int64_t V) {
-  const int64_t step = (int64_t)64 * kAhead * (dt == 2 ? 4 : 8);
-  int64_t p = (1024 + M - 1) / M, most = V / (step * kWaves);
+  const int64_t each = (int64_t)64 * (dt == 2 ? 4 : 8) * kSomeWaves;
+  int64_t p = 512 / M, most = V / each;
   p = p < most ? p : most;
-  return (int)(p < 1 ? 1 : p > 64 ? 64 : p);
+  return (int)(p < 1 ? 1 : p > kMaxParts ? kMaxParts : p);
 }
+// Eight wavefronts of a workgroup, fewer where the rows fill the chip: what a list
+// costs a wavefront is then paid less often (2048 rows of 128000 in bf16, 20 tokens:
+// 129 us with two, 138 with four; without a list 125 and 102; 1024 rows: 79 with eight).
+constexpr int64_t kManyRows = 2048;
 
 }  // namespace
 
@@ -375,10 +494,16 @@ hipError_t launch_logprobs(int dt, const void* x, int64_t ld, int64_t M, int64_t
   a.lists = reinterpret_cast<uint64_t*>(a.sums + M * a.parts);
   auto go = [&]<class T>() {
     const dim3 grid((unsigned)(M * a.parts));
-    if (top > 0) hipLaunchKernelGGL((logprobs_kernel<T, true>), grid, dim3(64 * kWaves), 0, st, a);
-    else hipLaunchKernelGGL((logprobs_kernel<T, false>), grid, dim3(64 * kWaves), 0, st, a);
-    if (a.parts > 1)
-      hipLaunchKernelGGL((logprobs_join_kernel<T>), dim3((unsigned)M), dim3(64 * kJoinWaves), 0, st, a);
+    auto rows = [&]<bool TOP, int W>() {
+      hipLaunchKernelGGL((logprobs_kernel<T, TOP, W>), grid, dim3(64 * W), 0, st, a);
+    };
+    if (M < kManyRows && top > 0) rows.template operator()<true, kSomeWaves>();
+    else if (M < kManyRows) rows.template operator()<false, kSomeWaves>();
+    else if (top > 0) rows.template operator()<true, 2>();
+    else rows.template operator()<false, 4>();
+    if (a.parts == 1) return;
+    if (top > 0) hipLaunchKernelGGL((logprobs_join_kernel<T, true>), dim3((unsigned)M), dim3(64 * kJoinWaves), 0, st, a);
+    else hipLaunchKernelGGL((logprobs_join_kernel<T, false>), dim3((unsigned)M), dim3(64 * kJoinWaves), 0, st, a);
   };
   if (dt == 0) go.template operator()<F16>();
   else if (dt == 1) go.template operator()<BF16>();

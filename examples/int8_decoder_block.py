@@ -1,11 +1,13 @@
-"""An attention block served in 8 bits: int8 projections, a paged 8-bit
-key/value cache, and its page bookkeeping, as a generation loop uses them.
+"""An attention block served in 8 bits: int8 projections, norm and rotation of
+queries and keys, a paged 8-bit key/value cache, and its page bookkeeping, as a
+generation loop uses them.
 
     python examples/int8_decoder_block.py [--steps N]
 
 Three prompts are written and answered token by token; then the first sequence
 is forked (two continuations of one prompt share its full pages), one sequence
-ends, and the pool is packed. Each step is checked against the same block
+ends, and the pool is packed. At last a tree of drafted tokens is verified in one
+step, with the log probabilities of a head's tokens. Each step is checked against the same block
 computed densely in fp32 from the unquantized weights: the block's outputs stay
 within the error that 8-bit weights, activations and cache make.
 
@@ -21,11 +23,11 @@ import torch
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 from group_wise_affine_amd import qmm  # noqa: E402
 
-HIDDEN, Q_HEADS, KV_HEADS, DIM, PAGE = 2048, 16, 4, 128, 32
+HIDDEN, Q_HEADS, KV_HEADS, DIM, PAGE, VOCABULARY = 2048, 16, 4, 128, 32, 4000
 
 
 class Block:
-    """qkv projection -> cache -> attention -> output projection."""
+    """qkv projection -> norm and rotation -> cache -> attention -> output projection."""
 
     def __init__(self, gen):
         def weight(n, k):
@@ -33,19 +35,39 @@ class Block:
             return w, *qmm.i8_quantize(w)   # one scale per output channel, once
         self.w_qkv, self.qkv, self.qkv_scale = weight((Q_HEADS + 2 * KV_HEADS) * DIM, HIDDEN)
         self.w_out, self.out, self.out_scale = weight(HIDDEN, Q_HEADS * DIM)
+        _, self.head, self.head_scale = weight(VOCABULARY, HIDDEN)
+        self.q_norm, self.k_norm = ((1 + 0.2 * torch.randn(DIM, generator=gen)).to(torch.bfloat16).cuda() for _ in range(2))
+        self.inv_freq = (10000.0 ** (-torch.arange(0, DIM, 2) / DIM)).cuda()
 
-    def __call__(self, x, cache, table, lens, cu):
-        """x [T, HIDDEN]: the new tokens of every sequence, packed."""
+    def __call__(self, x, positions, cache, table, lens, cu, parent=None):
+        """x [T, HIDDEN]: the new tokens of every sequence, packed; with parent they
+        are trees of drafts."""
         t = qmm.i8_linear(x, self.qkv, self.qkv_scale).view(len(x), Q_HEADS + 2 * KV_HEADS, DIM)
         q, k, v = t[:, :Q_HEADS], t[:, Q_HEADS:Q_HEADS + KV_HEADS], t[:, Q_HEADS + KV_HEADS:]
+        qmm.qk_norm_rope(q, k, positions, self.inv_freq, self.q_norm, self.k_norm, out=(q, k))
         qmm.kv8_append(cache, k, v, table, lens, cu)
-        a = qmm.kv8_attention(cache, q, table, lens, cu)
+        if parent is None:
+            a = qmm.kv8_attention(cache, q, table, lens, cu)
+        else:
+            a = qmm.kv8_attention_tree(cache, q, table, lens, cu, parent)
         return qmm.i8_linear(a.view(len(x), Q_HEADS * DIM), self.out, self.out_scale)
+
+    def scores(self, y, tokens):
+        """Log probabilities of the next tokens, and the three most likely ones."""
+        return qmm.logprobs(qmm.i8_linear(y, self.head, self.head_scale), tokens, top=3)
 
     def dense(self, x):
         """The same for one whole sequence, fp32, causal."""
         t = (x.float() @ self.w_qkv.float().t()).view(len(x), Q_HEADS + 2 * KV_HEADS, DIM).transpose(0, 1)
         q, k, v = t[:Q_HEADS], t[Q_HEADS:Q_HEADS + KV_HEADS], t[Q_HEADS + KV_HEADS:]
+        angle = torch.arange(len(x), device=x.device)[:, None] * self.inv_freq
+        cos, sin = angle.cos(), angle.sin()
+
+        def turned(y, weight):
+            y = y * torch.rsqrt(y.square().mean(2, keepdim=True) + 1e-6) * weight.float()
+            a, b = y.chunk(2, 2)
+            return torch.cat([a * cos - b * sin, b * cos + a * sin], 2)
+        q, k = turned(q, self.q_norm), turned(k, self.k_norm)
         k, v = (y.repeat_interleave(Q_HEADS // KV_HEADS, 0).contiguous() for y in (k, v))
         s = (q.contiguous() @ k.transpose(1, 2).contiguous()) * DIM ** -0.5
         s = s.masked_fill(torch.ones(len(x), len(x), device=x.device).triu(1).bool(), -torch.inf)
@@ -84,10 +106,16 @@ def run(steps=40, seed=0):
     seqs = [token(77), token(130), token(1), token(0)]   # what each slot has read
     worst = 0.0
 
+    def batch(new):
+        """Where each sequence's new tokens start, and their positions."""
+        pos = [i for x, n in zip(seqs, new) for i in range(len(x) - len(n), len(x))]
+        return (torch.tensor([0] + [len(x) for x in new], device="cuda").cumsum(0).int(),
+                torch.tensor(pos, device="cuda", dtype=torch.int32))
+
     def forward(new):
         nonlocal worst
-        cu = torch.tensor([0] + [len(x) for x in new], device="cuda").cumsum(0).int()
-        y = block(torch.cat(new), pool.cache, pool.table, pool.lens, cu)
+        cu, pos = batch(new)
+        y = block(torch.cat(new), pos, pool.cache, pool.table, pool.lens, cu)
         at = 0
         for x, n in zip(seqs, new):
             if len(n):
@@ -112,6 +140,24 @@ def run(steps=40, seed=0):
         decode([0, -1, 2, 3])
     used = pool.pack()
     decode([0, -1, 2, 3])
+
+    # drafts behind the first sequence: two ways to go on, one of them for three tokens
+    tree, drafts = [-1, 0, 1, 0, 3], token(5)
+    before = seqs[0]
+    seqs = [torch.cat([before, drafts])] + seqs[1:]
+    pool.step([0, -1, 2, 3], [len(x) for x in seqs])
+    cu, pos = batch([drafts, token(0), token(0), token(0)])
+    paths = []
+    for i, p in enumerate(tree):
+        paths.append((paths[p] if p >= 0 else []) + [i])
+        pos[i] = len(before) + len(paths[i]) - 1   # its depth, not its place
+    parent = torch.tensor(tree, dtype=torch.int32, device="cuda")
+    y = block(drafts, pos, pool.cache, pool.table, pool.lens, cu, parent)
+    for i, path in enumerate(paths):
+        want = block.dense(torch.cat([before, drafts[path]]))[-1]
+        worst = max(worst, ((y[i].float() - want).norm() / want.norm()).item())
+    logprob, entropy, ids, top = block.scores(y, torch.arange(5, dtype=torch.int32, device="cuda"))
+    assert bool((logprob < 0).all() and (entropy > 0).all() and (top[:, 0] >= logprob).all())
     return worst, used
 
 

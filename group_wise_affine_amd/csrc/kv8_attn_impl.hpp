@@ -671,10 +671,11 @@ __global__ __launch_bounds__(64 * NW, 2) void kv8_draft_kernel(AttnArgs a) {
   const int col = lane % 32, h = lane / 32;
   const Kv8& c = a.c;
   const int blocks = (a.G + R - 1) / R, columns = c.heads * blocks;
-  const int at_unit = blockIdx.x / (8 * kBundle) * 8 + blockIdx.x % 8;   // (bundle, column, part)
+  const int id = blockIdx.y * gridDim.x + blockIdx.x;
+  const int at_unit = id / (8 * kBundle) * 8 + id % 8;   // (bundle, column, part)
   const int bundles = (a.items + kBundle - 1) / kBundle;
   const int column = at_unit % columns, split = at_unit / columns / bundles;
-  const int index = at_unit / columns % bundles * kBundle + blockIdx.x / 8 % kBundle;
+  const int index = at_unit / columns % bundles * kBundle + id / 8 % kBundle;
   if (split >= a.splits || index >= a.items) return;
   const int head = column / blocks, h0 = column % blocks * R;
   const int G = min(R, a.G - h0);
@@ -1185,7 +1186,10 @@ __global__ __launch_bounds__(2 * kPromptRows, D == 256 ? 1 : 2) void kv8_prompt_
     asm volatile("" : "+v"(piece));
 #pragma unroll
     for (int g = 0; g < 4; g++) {
-      const float r = weight_scale(vs[g], at);
+      float r = weight_scale(vs[g], at);
+      // (of a page that the row does not see a scale may be anything; seen in part, its
+      // scale is the row's too, and the exponentials of the rest are 0)
+      if constexpr (MASK && M != Mask::kCausal) r = seen >> (g * 8) & 0xff ? r : 0.0f;
       half8_t hi, lo;
 #pragma unroll
       for (int e = 0; e < 8; e++) {
@@ -1193,7 +1197,7 @@ __global__ __launch_bounds__(2 * kPromptRows, D == 256 ? 1 : 2) void kv8_prompt_
         const float p = __builtin_amdgcn_exp2f(MASK ? x - at.base : fmaf(x, f[g], -at.base));
         l_run += p;
         float w = p * r;
-        if constexpr (MASK) w = sees(g, e) ? w : 0.0f;
+        if constexpr (MASK && M == Mask::kCausal) w = sees(g, e) ? w : 0.0f;
         hi[e] = (_Float16)w;
         if constexpr (kTwo) lo[e] = (_Float16)(w - (float)hi[e]);
       }
@@ -1460,7 +1464,9 @@ hipError_t launch_attention(const Kv8& c, int dt, const void* q, int64_t ldq, in
       if constexpr (M == Mask::kTree && D <= 128)
         if (p.drafts) {
           const int64_t units = (p.items + kBundle - 1) / kBundle * p.columns * p.splits;
-          hipLaunchKernelGGL((kv8_draft_kernel<T_, D, BT, 4>), dim3((unsigned)((units + 7) / 8 * 8 * kBundle)), dim3(256),
+          const int64_t ids = (units + 7) / 8 * 8 * kBundle;
+          const unsigned wide = (unsigned)(ids < (1 << 20) ? ids : 1 << 20);   // (a row of a grid is short of 2^32 threads)
+          hipLaunchKernelGGL((kv8_draft_kernel<T_, D, BT, 4>), dim3(wide, (unsigned)((ids + wide - 1) / wide)), dim3(256),
                              4 * kDraftRows * draft_row(D) * 4, st, a);
           if (p.splits > 1)
             join.template operator()<T_, D, kDraftRows>(a, (unsigned)(p.items * p.columns), p.most_rows);

@@ -169,6 +169,64 @@ def test_tree_more_new_tokens_than_tokens(new):
     tree(dev, ref, tab, lens, cu, q, "f16", grown(news, 9), "short")
 
 
+@pytest.mark.parametrize("new", [1, 7, 90])
+@pytest.mark.parametrize("G", [4, 40])
+def test_negative_scale(new, G):
+    """Few and many query rows, and groups of more heads than the draft kernel takes."""
+    lens, news = [130 + new, 60], [new, 1]
+    dev, ref, tab, cu, q = batch(lens, news, 16, 64, 1, G, "bf16")
+    parent, args = grown(news, 4), (dev, q.cuda(), i32(tab), i32(lens), i32(cu))
+    out, lse = Q.kv8_attention_tree(*args, i32(parent), scale=-0.2, return_lse=True)
+    check_attention(out, lse, S.Masked.of(ref, S.tree_sees(lens, cu, parent)), q, tab, lens, cu, -0.2, "bf16", "tree")
+    out, lse = Q.kv8_attention_window(*args, 50, 3, scale=-0.2, return_lse=True)
+    check_attention(out, lse, S.Masked.of(ref, S.window_sees(lens, cu, 50, 3)), q, tab, lens, cu, -0.2, "bf16", "window")
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("power", [118, -118, -126])
+def test_tree_queries_of_any_magnitude(power, D):
+    """bf16 queries near the ends of their range, brought back by the scale."""
+    lens, new = [100], [9]
+    dev, ref, tab, cu, q = batch(lens, new, 16, D, 1, 2, "bf16")
+    q = q.float().clamp(-15, 15) * 2.0 ** power
+    if power > 0:
+        q[0, 0, 3] = 3.38953e38
+    q, parent, scale = q.to(torch.bfloat16), grown(new, 5), 2.0 ** (-4 - power)
+    out, lse = Q.kv8_attention_tree(dev, q.cuda(), i32(tab), i32(lens), i32(cu), i32(parent), scale=scale, return_lse=True)
+    check_attention(out, lse, S.Masked.of(ref, S.tree_sees(lens, cu, parent)), q, tab, lens, cu, scale, "bf16", f"2^{power}")
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("new", [6, 80])
+def test_value_scales_far_apart(new, dt):
+    """Value scales over twelve orders of magnitude, zero among them, and large scores:
+    the references of the weights and of their sum move apart."""
+    lens = [470 + new]
+    dev, ref, tab, cu, q = batch(lens, [new], 16, 64, 1, 4, dt)
+    for p in range(ref.P):
+        x = [1e-6, 3.0, 0.0, 1e6 if dt == "bf16" else 30.0, 1e-2][p % 5]
+        dev.v_scales[p, 0], ref.vs[p, 0] = x, x
+    q, parent = (q.float() * 4).to(q.dtype), grown([new], 6)
+    args = (dev, q.cuda(), i32(tab), i32(lens), i32(cu))
+    out, lse = Q.kv8_attention_tree(*args, i32(parent), scale=0.5, return_lse=True)
+    check_attention(out, lse, S.Masked.of(ref, S.tree_sees(lens, cu, parent)), q, tab, lens, cu, 0.5, dt, "tree")
+    out, lse = Q.kv8_attention_window(*args, 200, 40, scale=0.5, return_lse=True)
+    check_attention(out, lse, S.Masked.of(ref, S.window_sees(lens, cu, 200, 40)), q, tab, lens, cu, 0.5, dt, "window")
+
+
+@pytest.mark.parametrize("new", [1, 9, 70])
+def test_rows_behind_the_last_sequence_stay(new):
+    """Tokens of the batch that no sequence owns, and outputs past a shorter one."""
+    lens, news = [300 + new, 40], [new, 1]
+    dev, ref, tab, cu, q = batch(lens, news, 16, 128, 2, 4, "bf16")
+    more = torch.cat([q, fresh(25, 8, 128, "bf16", 8)]).cuda()
+    args = (i32(tab), i32(lens), i32(cu))
+    for f, m in ((Q.kv8_attention_window, (100, 5)), (Q.kv8_attention_tree, (i32(grown(news, 2) + [-1] * 25),))):
+        out = torch.full_like(more, 7.0)
+        f(dev, more, *args, *m, out=out)
+        assert bool((out[cu[-1]:] == 7).all()) and bool(torch.isfinite(out[:cu[-1]]).all()) and not bool((out[:cu[-1]] == 7).all())
+
+
 def test_strided_queries_other_stream_and_out():
     lens, new = [150, 40, 300], [4, 1, 2]
     dev, ref, tab, cu, q = batch(lens, new, 32, 128, 2, 4, "bf16")

@@ -656,7 +656,15 @@ __global__ __launch_bounds__(256) void kv8_join_kernel(AttnArgs a) {
 // sum over D is that of 16-byte loads of keys and queries.
 //
 // Row groups of a sequence read the same codes: four that follow each other are
-// numbered eight apart, which puts them on one XCD and its L2.
+// numbered eight apart, which puts them on one XCD and its L2 (62 % of the requests
+// hit it).
+//
+// Bound: the vector unit (conversions and exponentials, 580 instructions per tile and
+// wavefront), two wavefronts to a SIMD: 3.0 us per tile of 64 tokens, and 11 us of a
+// workgroup's 40 are its start and its end. 16 trees of up to 26 tokens behind up to
+// 8166, 8 heads of 4 of 128, bf16: 86 us and 10 to join the parts, 1.9 TB/s of the codes
+// (the prompt kernel 124 us and, for the smaller trees, the decode kernel 49; a first form
+// that asked for all keys at once and held the queries in registers 96).
 constexpr int kBundle = 4;
 // floats from one row to the next where the wavefronts' results are joined: rows
 // start in other banks
@@ -1018,7 +1026,11 @@ __global__ __launch_bounds__(2 * kPromptRows, D == 256 ? 1 : 2) void kv8_prompt_
   const int col = lane % 32, h = lane / 32;
   const Kv8& c = a.c;
   const int head = blockIdx.x % c.heads, items = gridDim.x / c.heads, split = blockIdx.y;
-  const int index = longest_first<kThreads>(a, blockIdx.x / c.heads, items);
+  // (Under a window items differ little in length, and neighbours share tiles, in
+  // their L2 when they run together: four chunks of up to 2048 under 1024 tokens, 213 us
+  // sorted, 190 in order.)
+  const int rank = blockIdx.x / c.heads;
+  const int index = M == Mask::kWindow ? rank : longest_first<kThreads>(a, rank, items);
   const SeqAt seq = locate(a.q, index, a.unit, a.extra, c.bt_log2);
   const int s = seq.s, t0 = seq.first, n = seq.count, len = seq.len, item = seq.item;
   const int i0 = item * a.unit;

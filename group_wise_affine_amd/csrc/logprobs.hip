@@ -198,9 +198,20 @@ struct Seen {
       open = false;
     }
   }
-  // a first bound: the K-th largest of the lanes' maxima
-  __device__ __forceinline__ void first_bound(uint32_t largest) {
-    const uint32_t kth = __builtin_amdgcn_readlane(sort64(largest), top - 1);
+  // A first bound: the K-th largest of the lanes' maxima, bit by bit from the top: the
+  // largest number that K of them reach. The BITS high bits tell the type's values
+  // apart; those below are a negative number's ones.
+  template <int BITS>
+  __device__ __forceinline__ void first_bound(float largest) {
+    const uint32_t mine = ordered(largest);
+    uint32_t kth = 0;
+#pragma unroll
+    for (int i = 31; i >= 32 - BITS; i--) {
+      const uint32_t next = kth | 1u << i;
+      if (__builtin_popcountll(__ballot(mine >= next)) >= top) kth = next;
+    }
+    if constexpr (BITS < 32)
+      if (kth < 0x80000000u) kth |= (1u << (32 - BITS)) - 1;
     if (kth <= 0x007fffffu) return;   // -inf
     from = from_ordered(kth);
     above = from_ordered(kth - (kth == 0x80000000u ? 2 : 1));   // (the number before 0 is not -0)
@@ -370,18 +381,16 @@ __global__ __launch_bounds__(64 * kWaves, 8) void logprobs_kernel(LogprobArgs a)
         for (int i = 0; i < kAhead; i++)
           if (from + i * kTurn >= last) u[i] = none;
       if (TOP && b == 0) {
-        uint32_t largest = 0;
+        float largest = -__builtin_inff();
 #pragma unroll
-        for (int i = 0; i < kAhead; i++) {
-          float v[N];
-          unpack<T>(u[i], v);
+        for (int i = 0; i < kAhead; i++)
+          if (i < count) {
+            float v[N];
+            unpack<T>(u[i], v);
 #pragma unroll
-          for (int j = 0; j < N; j++) {
-            const uint32_t o = ordered(v[j]);
-            largest = o > largest ? o : largest;
+            for (int j = 0; j < N; j += 2) largest = max_or_nan(max_or_nan(largest, v[j]), v[j + 1]);
           }
-        }
-        seen.first_bound(largest);
+        seen.template first_bound<__is_same(T, F32) ? 32 : __is_same(T, F16) ? 19 : 16>(largest);
       }
     } else {
       const int edge = b < 0 ? lane : V - tail + lane;

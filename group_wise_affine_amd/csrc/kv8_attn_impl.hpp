@@ -663,8 +663,7 @@ __global__ __launch_bounds__(256) void kv8_join_kernel(AttnArgs a) {
 // wavefront), two wavefronts to a SIMD: 3.0 us per tile of 64 tokens, and 11 us of a
 // workgroup's 40 are its start and its end. 16 trees of up to 26 tokens behind up to
 // 8166, 8 heads of 4 of 128, bf16: 86 us and 10 to join the parts, 1.9 TB/s of the codes
-// (the prompt kernel 124 us and, for the smaller trees, the decode kernel 49; a first form
-// that asked for all keys at once and held the queries in registers 96).
+// (the prompt kernel 124 us and, for the smaller trees, the decode kernel 49 more).
 constexpr int kBundle = 4;
 // floats from one row to the next where the wavefronts' results are joined: rows
 // start in other banks
@@ -1366,7 +1365,9 @@ Plan plan(const Kv8& c, int64_t T, int64_t Hq, int64_t S, int64_t W, int64_t win
     p.extra = 1;
     p.items = T / p.unit + S;
     p.nw = 4;
-    // about 1024 workgroups (two rounds) where the contexts are as long as the table
+    // about 1024 workgroups (two rounds) where the contexts are as long as the table (16
+    // trees of up to 26 tokens behind up to 8166: 96 us, 113 with 512, 105 with 700, 100
+    // with 1400)
     const int64_t tiles = most_tiles(all, p.unit, window, sinks);
     const int64_t groups = (S > T / p.unit ? S : T / p.unit) * p.columns;
     const int64_t cut = (tiles + kMaxSplits - 1) / kMaxSplits;

@@ -439,7 +439,7 @@ qmm_status qmm_qk_norm_rope(const void* q, int64_t ldq, const void* k, int64_t l
 }
 
 static bool logprobs_sizes(qmm_dtype dt, int64_t M, int64_t V, int64_t top) {
-  return (dt == QMM_F16 || dt == QMM_BF16 || dt == QMM_F32) && M >= 1 && M <= (1 << 24) && V >= 1 &&
+  return (dt == QMM_F16 || dt == QMM_BF16 || dt == QMM_F32) && M >= 1 && M <= (1 << 23) && V >= 1 &&
          V <= (1 << 30) && top >= 0 && top <= 64 && top <= V;
 }
 
@@ -465,7 +465,7 @@ qmm_status qmm_logprobs(const void* logits, int64_t ld, qmm_dtype dt, int64_t M,
                 tag, (int)dt);
   if (!logprobs_sizes(dt, M, V, top))
     return fail(QMM_E_SHAPE,
-                "%s: rows (%lld) must be in [1, 2^24], V (%lld) in [1, 2^30], top (%lld) in [0, 64] "
+                "%s: rows (%lld) must be in [1, 2^23], V (%lld) in [1, 2^30], top (%lld) in [0, 64] "
                 "and at most V",
                 tag, (long long)M, (long long)V, (long long)top);
   if (ld < V)

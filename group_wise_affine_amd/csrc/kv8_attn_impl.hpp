@@ -46,6 +46,7 @@ struct AttnArgs {
   int G;               // query heads per cache head, 16 at a time
   int unit, extra;     // new tokens per workgroup, spare items per sequence
   int items, each;     // of the batch; of every sequence, or 0: as many as its tokens need
+  int bundle_log2;     // draft kernel: items that follow each other on one XCD
   int many;            // sequences with more query rows than this are the prompt kernel's
   float scale;         // magnitude of the scores' scale, times log2 e
   uint32_t flip;       // its sign, as the sign bits of two queries
@@ -548,14 +549,15 @@ __device__ __forceinline__ void join_out(const AttnArgs& a, int64_t at, int D, i
 // Few parts (at most kFewParts): a thread joins two values of a row by itself.
 // (48 contexts of up to 6 parts: 8.5 us with the kernel below, 4.9 with this.)
 constexpr int kFewParts = 16;
+constexpr int few_parts(int R) { return R == kDraftRows ? 32 : kFewParts; }
 template <Mask M, class T, int D, int R>
 __global__ __launch_bounds__(256) void kv8_join_few_kernel(AttnArgs a) {
-  constexpr int kFloats = kPart<D, R>;
+  constexpr int kFloats = kPart<D, R>, kFew = few_parts(R);
   const int r = blockIdx.y * (512 / D) + threadIdx.x / (D / 2), d = threadIdx.x % (D / 2) * 2;
   const float* part = a.ws + (int64_t)blockIdx.x * a.splits * kFloats;
-  float2 v[kFewParts], ml[kFewParts];
+  float2 v[kFew], ml[kFew];
 #pragma unroll
-  for (int w = 0; w < kFewParts; w++)
+  for (int w = 0; w < kFew; w++)
     if (w < a.splits) {
       ml[w] = *reinterpret_cast<const float2*>(part + w * kFloats + 2 * r);
       v[w] = *reinterpret_cast<const float2*>(part + w * kFloats + 2 * R + r * D + d);
@@ -564,10 +566,10 @@ __global__ __launch_bounds__(256) void kv8_join_few_kernel(AttnArgs a) {
   if (j.parts <= 1) return;
   float m = kNone, l = 0.0f, v0 = 0.0f, v1 = 0.0f;
 #pragma unroll
-  for (int w = 0; w < kFewParts; w++)
+  for (int w = 0; w < kFew; w++)
     if (w < j.parts) m = fmaxf(m, ml[w].x);
 #pragma unroll
-  for (int w = 0; w < kFewParts; w++)
+  for (int w = 0; w < kFew; w++)
     if (w < j.parts) {
       const float e = __builtin_amdgcn_exp2f(ml[w].x - m);
       l += ml[w].y * e;
@@ -655,8 +657,8 @@ __global__ __launch_bounds__(256) void kv8_join_kernel(AttnArgs a) {
 // V^T as it is read (16 tokens of one column per 16-byte load). The order of the
 // sum over D is that of 16-byte loads of keys and queries.
 //
-// Row groups of a sequence read the same codes: four that follow each other are
-// numbered eight apart, which puts them on one XCD and its L2 (62 % of the requests
+// Row groups of a sequence read the same codes: up to four that follow each other
+// are numbered eight apart, which puts them on one XCD and its L2 (62 % of the requests
 // hit it).
 //
 // Bound: the vector unit (conversions and exponentials, 580 instructions per tile and
@@ -664,7 +666,6 @@ __global__ __launch_bounds__(256) void kv8_join_kernel(AttnArgs a) {
 // workgroup's 40 are its start and its end. 16 trees of up to 26 tokens behind up to
 // 8166, 8 heads of 4 of 128, bf16: 86 us and 10 to join the parts, 1.9 TB/s of the codes
 // (the prompt kernel 124 us and, for the smaller trees, the decode kernel 49 more).
-constexpr int kBundle = 4;
 // floats from one row to the next where the wavefronts' results are joined: rows
 // start in other banks
 constexpr int draft_row(int D) { return D + 4; }
@@ -678,11 +679,11 @@ __global__ __launch_bounds__(64 * NW, 2) void kv8_draft_kernel(AttnArgs a) {
   const int col = lane % 32, h = lane / 32;
   const Kv8& c = a.c;
   const int blocks = (a.G + R - 1) / R, columns = c.heads * blocks;
-  const int id = blockIdx.y * gridDim.x + blockIdx.x;
-  const int at_unit = id / (8 * kBundle) * 8 + id % 8;   // (bundle, column, part)
-  const int bundles = (a.items + kBundle - 1) / kBundle;
+  const int id = blockIdx.y * gridDim.x + blockIdx.x, log2 = a.bundle_log2;
+  const int at_unit = (id >> (3 + log2)) * 8 + id % 8;   // (bundle, column, part)
+  const int bundles = (a.items + (1 << log2) - 1) >> log2;
   const int column = at_unit % columns, split = at_unit / columns / bundles;
-  const int index = at_unit / columns % bundles * kBundle + id / 8 % kBundle;
+  const int index = ((at_unit / columns % bundles) << log2) + (id >> 3 & ((1 << log2) - 1));
   if (split >= a.splits || index >= a.items) return;
   const int head = column / blocks, h0 = column % blocks * R;
   const int G = min(R, a.G - h0);
@@ -1324,7 +1325,7 @@ __global__ __launch_bounds__(2 * kPromptRows, D == 256 ? 1 : 2) void kv8_prompt_
 constexpr int kFewRows = 64;
 
 struct Plan {
-  int unit, extra, each, splits, per, nw, many, most_rows;
+  int unit, extra, each, bundle_log2, splits, per, nw, many, most_rows;
   int64_t items, columns;   // grid: items x heads and blocks of a group's heads
   bool prompts, drafts;     // drafts: the draft kernel in the decode kernel's place
   int p_unit, p_splits, p_per;
@@ -1346,8 +1347,11 @@ Plan plan(const Kv8& c, int64_t T, int64_t Hq, int64_t S, int64_t W, int64_t win
   const int64_t G = Hq / c.heads;
   // the packed batch says how many new tokens a sequence can have at most
   const int64_t longest = T;
-  // (D = 256: its state does not fit the registers)
-  p.drafts = M == Mask::kTree && T > S && G <= kDraftRows && c.dim <= 128;
+  // (For large batches of few rows the decode kernel is quicker: 48 trees of up to 4
+  // tokens, 8 heads of 4, 113 us, 128 with the draft kernel; 16 of up to 5, 39 and 31; one
+  // of 4 behind 31996, 44 and 24. D = 256: its state does not fit the registers.)
+  p.drafts = M == Mask::kTree && T > S && G <= kDraftRows && c.dim <= 128 &&
+             (T * G > 14 * S || S * c.heads < 128);
   p.prompts = longest * G > kFewRows && T > S && G <= kPromptRows;
   // Trees go to the draft kernel whole (the two kernels one after the other, each for
   // some of the sequences, take longer than either: 215 us for 16 trees of up to 64
@@ -1364,14 +1368,26 @@ Plan plan(const Kv8& c, int64_t T, int64_t Hq, int64_t S, int64_t W, int64_t win
     p.most_rows = (int)(p.unit * G);
     p.extra = 1;
     p.items = T / p.unit + S;
+    const int64_t all_rows = (T + p.unit - 1) / p.unit;   // of one sequence with all the tokens
+    if (S * all_rows <= p.items) {
+      p.each = (int)all_rows;
+      p.items = S * all_rows;
+    }
+    p.bundle_log2 = p.items >= 3 * S ? 2 : p.items >= 2 * S ? 1 : 0;
     p.nw = 4;
-    // about 1024 workgroups (two rounds) where the contexts are as long as the table (16
-    // trees of up to 26 tokens behind up to 8166: 96 us, 113 with 512, 105 with 700, 100
-    // with 1400)
+    // A workgroup's start and end take as long as 16 tiles, so that parts are 32 tiles
+    // where that leaves one for each CU, more where it makes over 1024 of them (two
+    // rounds) of contexts as long as the table, and no more than 32 of a context. (16
+    // trees of up to 26 tokens behind up to 8166, 8 heads of 4: 97 us with parts of 40
+    // tiles, 114 with 80; 4 of 12 behind 7988: 33 us with 20, 39 with 8; one of 8 behind
+    // 31992: 26 us in 32 parts, 30 in 16, 36 in 126.)
     const int64_t tiles = most_tiles(all, p.unit, window, sinks);
-    const int64_t groups = (S > T / p.unit ? S : T / p.unit) * p.columns;
-    const int64_t cut = (tiles + kMaxSplits - 1) / kMaxSplits;
-    int64_t per = (groups * tiles + 1023) / 1024;
+    const int64_t work = (S > T / p.unit ? S : T / p.unit) * p.columns * tiles;
+    const int64_t cut = (tiles + few_parts(kDraftRows) - 1) / few_parts(kDraftRows);
+    int64_t per = work / 256 < 32 ? work / 256 : 32;
+    const int64_t least = tiles < 64 ? 4 : 8;
+    per = per > least ? per : least;
+    per = per > work / 1024 ? per : work / 1024;
     per = per > cut ? per : cut;
     if (p.items * p.columns * cut > (1 << 20)) per = tiles;
     p.per = (int)((per + p.nw - 1) / p.nw * p.nw);
@@ -1460,12 +1476,12 @@ hipError_t launch_attention(const Kv8& c, int dt, const void* q, int64_t ldq, in
                             float scale, void* out, float* lse, float* ws, hipStream_t st) {
   const Plan p = plan<M>(c, T, Hq, S, W, window, sinks);
   AttnArgs a{c, {table, lens, cu, (int)S, (int)W, (int)T}, static_cast<const uint16_t*>(q), ldq,
-             (int)(Hq / c.heads), p.unit, p.extra, (int)p.items, p.each, p.many, fabsf(scale) * kLog2e,
+             (int)(Hq / c.heads), p.unit, p.extra, (int)p.items, p.each, p.bundle_log2, p.many, fabsf(scale) * kLog2e,
              scale < 0 ? 0x80008000u : 0u, static_cast<uint16_t*>(out), lse, p.splits, p.per, ws,
              (int)window, (int)sinks, parent};
   const dim3 grid((unsigned)p.items, (unsigned)p.columns, (unsigned)p.splits);
   auto join = [&]<class T_, int D, int R>(const AttnArgs& x, unsigned units, int rows) {
-    if (R == kPromptRows || x.splits <= kFewParts)
+    if (R == kPromptRows || x.splits <= few_parts(R))
       hipLaunchKernelGGL((kv8_join_few_kernel<M, T_, D, R>),
                          dim3(units, (unsigned)((rows + 512 / D - 1) / (512 / D))), dim3(256), 0, st, x);
     else
@@ -1476,8 +1492,9 @@ hipError_t launch_attention(const Kv8& c, int dt, const void* q, int64_t ldq, in
     auto decode = [&]<int BT>() {
       if constexpr (M == Mask::kTree && D <= 128)
         if (p.drafts) {
-          const int64_t units = (p.items + kBundle - 1) / kBundle * p.columns * p.splits;
-          const int64_t ids = (units + 7) / 8 * 8 * kBundle;
+          const int64_t bundle = 1 << p.bundle_log2;
+          const int64_t units = (p.items + bundle - 1) / bundle * p.columns * p.splits;
+          const int64_t ids = (units + 7) / 8 * 8 * bundle;
           const unsigned wide = (unsigned)(ids < (1 << 20) ? ids : 1 << 20);   // (a row of a grid is short of 2^32 threads)
           hipLaunchKernelGGL((kv8_draft_kernel<T_, D, BT, 4>), dim3(wide, (unsigned)((ids + wide - 1) / wide)), dim3(256),
                              4 * kDraftRows * draft_row(D) * 4, st, a);

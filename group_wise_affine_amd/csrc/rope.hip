@@ -75,10 +75,11 @@ __global__ __launch_bounds__(256) void qk_rope_kernel(RopeArgs a) {
   constexpr int kRows = 64 / L;
   const int lane = threadIdx.x % 64, li = lane % L;
   const int blocks = (a.heads + kRows * PASSES - 1) / (kRows * PASSES);
-  const int64_t unit = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-  const int64_t t = unit / blocks;
+  // (T * heads < 2^31)
+  const uint32_t unit = (blockIdx.y * gridDim.x + blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const int64_t t = unit / (uint32_t)blocks;
   if (t >= a.T) return;
-  const int h0 = (int)(unit % blocks) * (kRows * PASSES) + lane / L;
+  const int h0 = (int)(unit % (uint32_t)blocks) * (kRows * PASSES) + lane / L;
   const bool mine = li * 8 < a.D;
   const int turned = a.half / 4;   // lanes of a row whose elements turn
   const bool turns = li < turned;
@@ -174,9 +175,11 @@ hipError_t launch_qk_norm_rope(int dt, const void* q, int64_t ldq, const void* k
                    static_cast<uint16_t*>(qo), static_cast<uint16_t*>(ko), ldqo, ldko, pos, freq, T,
                    (int)hq, (int)(hq + hk), (int)D, (int)(rot / 2), eps};
   auto go = [&]<class T_, bool N, int L, int PASSES>() {
-    const int64_t per = 64 / L * PASSES, units = T * ((a.heads + per - 1) / per);
-    hipLaunchKernelGGL((qk_rope_kernel<T_, N, L, PASSES>), dim3((unsigned)((units + 3) / 4)), dim3(256),
-                       0, st, a);
+    const int64_t per = 64 / L * PASSES, units = T * ((a.heads + per - 1) / per), groups = (units + 3) / 4;
+    // (a row of a grid is short of 2^32 threads)
+    const unsigned wide = (unsigned)(groups < (1 << 20) ? groups : 1 << 20);
+    hipLaunchKernelGGL((qk_rope_kernel<T_, N, L, PASSES>), dim3(wide, (unsigned)((groups + wide - 1) / wide)),
+                       dim3(256), 0, st, a);
   };
   auto passes = [&]<class T_, bool N, int L>() {
     // wavefronts of one pass: the chip holds 8192. (Rows of 40 heads of 128 in bf16, 1, 2

@@ -660,8 +660,8 @@ qmm_status qmm_qk_norm_rope(const void* q, int64_t ldq, const void* k, int64_t l
                             void* q_out, int64_t ldqo, void* k_out, int64_t ldko, void* stream);
 
 /*
- * For each row of logits [M, V] (f16, bf16 or f32; row r starts at logits + r*ld
- * elements, any stride >= V and the alignment of the type): with lse = ln sum
+ * For each row of logits [M, V] (f16, bf16 or f32; M <= 2^23, V <= 2^30; row r
+ * starts at logits + r*ld elements, any stride >= V and the alignment of the type): with lse = ln sum
  * exp(x), logprob [M] = x[tokens[r]] - lse (tokens [M] int32; -inf for one
  * outside [0, V)), entropy [M] = lse - sum softmax(x) x, and the `top` (0 to 64,
  * at most V) most likely tokens, top_ids [M, top] int32 and top_logprobs [M, top],

@@ -272,6 +272,16 @@ def test_graph_replays():
         assert all(torch.equal(a, b) for a, b in zip(want, out))
 
 
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("B,D,G", [(16, 64, 4), (16, 128, 32), (32, 128, 3), (64, 64, 16)])
+@pytest.mark.parametrize("lens,new", [([2600], [5]), ([5003], [9]), ([2300, 700, 1200], [4, 1, 20])])
+def test_drafts_in_few_and_many_parts(lens, new, B, D, G, dt):
+    """One context in up to 32 parts and several in fewer, row groups of every size and
+    number, items counted by sequence and by tokens."""
+    b = batch(lens, new, B, D, 1, G, dt, W=-(-max(lens) // B) + 40)
+    tree(*b[:3], lens, b[3], b[4], dt, grown(new, 8), f"{lens} {new} B{B} D{D} G{G} {dt}")
+
+
 @pytest.mark.parametrize("S_", [65, 700])
 def test_many_sequences(S_):
     r = np.random.default_rng(S_)

@@ -88,7 +88,7 @@ def test_rotation(L):
 
 def test_logprobs(L):
     fn = "qmm_logprobs"
-    for kw in (dict(M=0), dict(M=1 << 25), dict(V=0), dict(V=1 << 31, ld=1 << 31), dict(top=-1), dict(top=65), dict(V=3, top=5),
+    for kw in (dict(M=0), dict(M=(1 << 23) + 1), dict(V=0), dict(V=1 << 31, ld=1 << 31), dict(top=-1), dict(top=65), dict(V=3, top=5),
                dict(ld=999)):
         refused(L, fn, Q.QMM_E_SHAPE, **kw)
     for n in ("x", "tokens", "lp", "h", "ids", "tl"):

@@ -246,6 +246,28 @@ def test_strided_queries_other_stream_and_out():
         assert torch.equal(want, out)
 
 
+def test_two_streams_at_once():
+    """Calls on two streams, each with parts in scratch memory of its own."""
+    side = torch.cuda.Stream()
+    lens, new = [4000, 900], [6, 3]
+    dev, ref, tab, cu, q = batch(lens, new, 32, 128, 2, 4, "bf16")
+    qs = [q.cuda(), fresh(9, 8, 128, "bf16", 9).cuda()]
+    parent, args = i32(grown(new, 1)), (i32(tab), i32(lens), i32(cu))
+
+    def both(i, st):
+        return (Q.kv8_attention_tree(dev, qs[i], *args, parent, stream=st),
+                Q.kv8_attention_window(dev, qs[i], *args, 3000, 4, stream=st))
+    want = [both(i, None) for i in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, st in enumerate((None, side)):
+            got[i].append(both(i, st))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(a, b) for g in got[i] for a, b in zip(g, want[i]))
+
+
 def test_graph_replays():
     """Captured once, both masks; lengths, queries and the tree change in between."""
     lens, new = [1900, 900], [6, 6]

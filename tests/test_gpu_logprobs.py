@@ -55,6 +55,33 @@ def test_rows(M, V, dt):
 
 
 @pytest.mark.parametrize("dt", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("M,V", [(2048, 300), (2100, 3001), (40, 20001), (130, 9000)])
+def test_many_rows(M, V, dt):
+    """Rows that fill the chip, a workgroup each, and rows in a few parts."""
+    x, t = rows(M, V, dt, M + V), toks(M, V)
+    x[5, V // 2:] = x[6] = -torch.inf
+    x[7, 3] = float("nan")
+    x[8] = 1.0
+    for top in (0, 5, 64):
+        check(x, t, top, Q.logprobs(x, t, top=top), f"{M}x{V} {dt} top {top}")
+
+
+def test_two_streams_at_once():
+    """Calls on two streams, each with parts in scratch memory of its own."""
+    side = torch.cuda.Stream()
+    xs, ts = [rows(3, 60000, "bf16", s) for s in (1, 2)], [toks(3, 60000, s) for s in (1, 2)]
+    want = [Q.logprobs(x, t, top=20) for x, t in zip(xs, ts)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, st in enumerate((None, side)):
+            got[i].append(Q.logprobs(xs[i], ts[i], top=20, stream=st))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(a, b) for g in got[i] for a, b in zip(g, want[i]))
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16", "f32"])
 @pytest.mark.parametrize("V", [300, 5000, 70001])
 def test_rows_in_awkward_orders(V, dt):
     """Rising, falling and equal logits; most equal; two values; masked tails, heads and

@@ -60,6 +60,21 @@ def test_norm_and_rotation(T, Hq, Hk, D, rot, inter, dt):
 
 
 @pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("T,Hq,Hk,D,rot", [(9000, 30, 2, 8, 8), (3000, 8, 1, 64, 64), (2403, 12, 3, 128, 64), (9001, 13, 3, 72, 72),
+                                           (4000, 3, 1, 200, 200), (9000, 4, 4, 136, 136), (8000, 1, 1, 512, 512),
+                                           (9000, 3, 1, 264, 16)])
+def test_many_tokens(T, Hq, Hk, D, rot, inter):
+    """Wavefronts that take several of a token's heads, the last ones partly."""
+    q, k = draw(T, Hq, D, "bf16", 6), draw(T, Hk, D, "bf16", 7)
+    w = draw(1, 1, D, "bf16", 8)[0, 0]
+    pos = torch.randint(0, 100000, (T,), generator=torch.Generator().manual_seed(9), dtype=torch.int32)
+    f = freqs(rot)
+    qo, ko = Q.qk_norm_rope(*[t.cuda() for t in (q, k, pos, f)], w.cuda(), None, eps=1e-5, interleaved=inter)
+    check(qo, q, pos, f, w, 1e-5, inter, "bf16", f"q T{T} {Hq}+{Hk}x{D}")
+    check(ko, k, pos, f, None, 1e-5, inter, "bf16", f"k T{T} {Hq}+{Hk}x{D}")
+
+
+@pytest.mark.parametrize("inter", [False, True])
 def test_far_and_negative_positions(inter):
     pos = torch.tensor([0, 1, -1, 2 ** 31 - 1, -2 ** 31, 1 << 24, 12345678, 131071, -131071], dtype=torch.int32)
     q, k = draw(len(pos), 2, 64, "f16", 10), draw(len(pos), 1, 64, "f16", 11)

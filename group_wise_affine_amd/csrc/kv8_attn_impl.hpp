@@ -1351,7 +1351,7 @@ Plan plan(const Kv8& c, int64_t T, int64_t Hq, int64_t S, int64_t W, int64_t win
   // tokens, 8 heads of 4, 113 us, 128 with the draft kernel; 16 of up to 5, 39 and 31; one
   // of 4 behind 31996, 44 and 24. D = 256: its state does not fit the registers.)
   p.drafts = M == Mask::kTree && T > S && G <= kDraftRows && c.dim <= 128 &&
-             (T * G > 14 * S || S * c.heads < 128);
+             (T * G > 13 * S || S * c.heads < 128);
   p.prompts = longest * G > kFewRows && T > S && G <= kPromptRows;
   // Trees go to the draft kernel whole (the two kernels one after the other, each for
   // some of the sequences, take longer than either: 215 us for 16 trees of up to 64
@@ -1443,10 +1443,17 @@ Plan plan(const Kv8& c, int64_t T, int64_t Hq, int64_t S, int64_t W, int64_t win
   // over its rows in fp32, there and back. (A chunk of 600 tokens behind 29400,
   // 8 heads of 4: 535 us cut, 949 us whole.)
   const int64_t work = p.p_items * c.heads;
-  // (Trees hardly ever fill their last item, so that there are fewer.)
-  int64_t ps = (p.drafts ? 1024 : 512) / (work < 1 ? 1 : work);
+  // Trees hardly ever fill their last item and are few, so that they are cut finer, into
+  // parts of at least 8 tiles (4 of up to 40 tokens behind 3960, D = 256: 65 us, 98 with 16;
+  // 3 of up to 200 behind 2800, D = 128: 36 us, 47), and for D = 256, of which a CU holds
+  // one, fewer (5 of up to 118 behind 7160, one head of 8: 96 us in 7 parts, 125 in 9).
+  // Small trees are not theirs, and would only wait for more of them to leave.
+  const bool trees = M == Mask::kTree && T * G > kFewRows * S;
+  const int64_t least = trees ? 8 : 16;
+  const int64_t wanted = !trees ? 512 : c.dim == 256 ? 288 : 1024;
+  int64_t ps = wanted / (work < 1 ? 1 : work);
   const int64_t p_tiles = most_tiles(all, p.p_unit, window, sinks);
-  ps = ps < p_tiles / 16 ? ps : p_tiles / 16;
+  ps = ps < p_tiles / least ? ps : p_tiles / least;
   ps = ps < 1 ? 1 : ps > kFewParts ? kFewParts : ps;
   p.p_per = (int)((p_tiles + ps - 1) / ps);
   p.p_splits = (int)((p_tiles + p.p_per - 1) / p.p_per);

@@ -44,8 +44,9 @@ struct AttnArgs {
   const uint16_t* x;   // queries, row t at x + t * ldq
   int64_t ldq;
   int G;               // query heads per cache head, 16 at a time
-  int unit, extra;     // new tokens per workgroup, spare items per sequence
-  int items, each;     // of the batch; of every sequence, or 0: as many as its tokens need
+  int unit;            // new tokens per workgroup
+  int step, extra;     // items of a sequence: one for each `step` new tokens, and so many
+  int items;           // of the batch
   int bundle_log2;     // draft kernel: items that follow each other on one XCD
   int many;            // sequences with more query rows than this are the prompt kernel's
   float scale;         // magnitude of the scores' scale, times log2 e
@@ -57,11 +58,6 @@ struct AttnArgs {
   int window, sinks;       // kWindow; sinks <= 2^30
   const int32_t* parent;   // kTree: [T]
 };
-
-__device__ __forceinline__ SeqAt locate_item(const AttnArgs& a, int i, int bt_log2) {
-  return a.each > 0 ? of_sequence(a.q, i / a.each, i % a.each, bt_log2)
-                    : locate(a.q, i, a.unit, a.extra, bt_log2);
-}
 
 // The tiles that an item looks at: those of its sequence up to `most`, without
 // the ones that lie between the sinks and the window of its first row (at
@@ -260,7 +256,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : D == 128 ? 2 : 3) void kv8_
   const int head = blockIdx.y / blocks, h0 = blockIdx.y % blocks * 16, split = blockIdx.z;
   const int G = min(16, a.G - h0);
   const Kv8& c = a.c;
-  const SeqAt seq = locate_item(a, blockIdx.x, BT);
+  const SeqAt seq = locate(a.q, blockIdx.x, a.step, a.extra, BT);
   const int s = seq.s, t0 = seq.first, n = seq.count, len = seq.len, item = seq.item;
   const int i0 = item * a.unit;
   if (item < 0 || i0 >= n || (int64_t)n * a.G > a.many) return;
@@ -527,7 +523,7 @@ __device__ __forceinline__ JoinAt join_at(const AttnArgs& a, int unit, int r) {
   const int index = unit / columns, column = unit % columns;
   const int head = column / blocks, h0 = column % blocks * R;
   const int G = PROMPT ? a.G : min(R, a.G - h0);
-  const SeqAt q = locate_item(a, index, a.c.bt_log2);
+  const SeqAt q = locate(a.q, index, a.step, a.extra, a.c.bt_log2);
   const int i0 = q.item * a.unit;
   JoinAt j{0, 0};
   if (q.item < 0 || i0 >= q.count || ((int64_t)q.count * a.G > a.many) != PROMPT) return j;
@@ -687,7 +683,7 @@ __global__ __launch_bounds__(64 * NW, 2) void kv8_draft_kernel(AttnArgs a) {
   if (split >= a.splits || index >= a.items) return;
   const int head = column / blocks, h0 = column % blocks * R;
   const int G = min(R, a.G - h0);
-  const SeqAt seq = locate_item(a, index, BT);
+  const SeqAt seq = locate(a.q, index, a.step, a.extra, BT);
   const int s = seq.s, t0 = seq.first, n = seq.count, len = seq.len, i0 = seq.item * a.unit;
   if (seq.item < 0 || i0 >= n || (int64_t)n * a.G > a.many) return;
   const int ntok = min(n - i0, a.unit);
@@ -1031,7 +1027,7 @@ __global__ __launch_bounds__(2 * kPromptRows, D == 256 ? 1 : 2) void kv8_prompt_
   // sorted, 190 in order.)
   const int rank = blockIdx.x / c.heads;
   const int index = M == Mask::kWindow ? rank : longest_first<kThreads>(a, rank, items);
-  const SeqAt seq = locate(a.q, index, a.unit, a.extra, c.bt_log2);
+  const SeqAt seq = locate(a.q, index, a.step, a.extra, c.bt_log2);
   const int s = seq.s, t0 = seq.first, n = seq.count, len = seq.len, item = seq.item;
   const int i0 = item * a.unit;
   if (item < 0 || i0 >= n || (int64_t)n * a.G <= a.many) return;
@@ -1325,7 +1321,7 @@ __global__ __launch_bounds__(2 * kPromptRows, D == 256 ? 1 : 2) void kv8_prompt_
 constexpr int kFewRows = 64;
 
 struct Plan {
-  int unit, extra, each, bundle_log2, splits, per, nw, many, most_rows;
+  int unit, step, extra, bundle_log2, splits, per, nw, many, most_rows;
   int64_t items, columns;   // grid: items x heads and blocks of a group's heads
   bool prompts, drafts;     // drafts: the draft kernel in the decode kernel's place
   int p_unit, p_splits, p_per;
@@ -1368,10 +1364,10 @@ Plan plan(const Kv8& c, int64_t T, int64_t Hq, int64_t S, int64_t W, int64_t win
     p.most_rows = (int)(p.unit * G);
     p.extra = 1;
     p.items = T / p.unit + S;
-    const int64_t all_rows = (T + p.unit - 1) / p.unit;   // of one sequence with all the tokens
-    if (S * all_rows <= p.items) {
-      p.each = (int)all_rows;
-      p.items = S * all_rows;
+    p.step = p.unit;
+    if (S == 1) {   // all the tokens are its
+      p.step = INT32_MAX;
+      p.items = p.extra = (int)((T + p.unit - 1) / p.unit);
     }
     p.bundle_log2 = p.items >= 3 * S ? 2 : p.items >= 2 * S ? 1 : 0;
     p.nw = 4;
@@ -1394,6 +1390,7 @@ Plan plan(const Kv8& c, int64_t T, int64_t Hq, int64_t S, int64_t W, int64_t win
     p.splits = (int)((tiles + p.per - 1) / p.per);
   } else {
     p.unit = T > S && G <= 8 ? (int)(16 / G) : 1;
+    p.step = p.unit;
     p.extra = p.unit > 1 ? 1 : 0;
     p.items = T / p.unit + p.extra * S;
     p.columns = c.heads * ((G + 15) / 16);
@@ -1432,7 +1429,8 @@ Plan plan(const Kv8& c, int64_t T, int64_t Hq, int64_t S, int64_t W, int64_t win
     // of 245 under a window of 1024).
     const int64_t each = (kFewRows / G + p.unit - 1) / p.unit;
     if (S * each < p.items) {
-      p.each = (int)each;
+      p.step = INT32_MAX;   // (no sequence has so many tokens)
+      p.extra = (int)each;
       p.items = S * each;
     }
   }
@@ -1483,7 +1481,7 @@ hipError_t launch_attention(const Kv8& c, int dt, const void* q, int64_t ldq, in
                             float scale, void* out, float* lse, float* ws, hipStream_t st) {
   const Plan p = plan<M>(c, T, Hq, S, W, window, sinks);
   AttnArgs a{c, {table, lens, cu, (int)S, (int)W, (int)T}, static_cast<const uint16_t*>(q), ldq,
-             (int)(Hq / c.heads), p.unit, p.extra, (int)p.items, p.each, p.bundle_log2, p.many, fabsf(scale) * kLog2e,
+             (int)(Hq / c.heads), p.unit, p.step, p.extra, (int)p.items, p.bundle_log2, p.many, fabsf(scale) * kLog2e,
              scale < 0 ? 0x80008000u : 0u, static_cast<uint16_t*>(out), lse, p.splits, p.per, ws,
              (int)window, (int)sinks, parent};
   const dim3 grid((unsigned)p.items, (unsigned)p.columns, (unsigned)p.splits);
@@ -1524,10 +1522,9 @@ hipError_t launch_attention(const Kv8& c, int dt, const void* q, int64_t ldq, in
     else decode.template operator()<6>();
     if (!p.prompts) return;
     AttnArgs b = a;
-    b.unit = p.p_unit;
+    b.unit = b.step = p.p_unit;
     b.extra = 1;
     b.items = (int)p.p_items;
-    b.each = 0;
     b.splits = p.p_splits;
     b.per = p.p_per;
     b.ws = ws + decode_bytes(p, c) / 4;

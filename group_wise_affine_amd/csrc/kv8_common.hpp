@@ -72,13 +72,6 @@ __device__ __forceinline__ SeqAt locate(const Kv8Seqs& q, int i, int unit, int e
   return r;
 }
 
-// the item'th work item of sequence s
-__device__ __forceinline__ SeqAt of_sequence(const Kv8Seqs& q, int s, int item, int bt_log2) {
-  const int first = q.clip_row(q.cu[s]), len = max(q.lens[s], 0);
-  const int64_t most = (int64_t)q.W << bt_log2;
-  return {s, first, max(q.clip_row(q.cu[s + 1]) - first, 0), len > most ? (int)most : len, item};
-}
-
 // Copies part `part` of `parts` of a page (codes, and with part 0 the scales)
 // with 256 threads, eight 16-byte pieces in flight per thread.
 constexpr int kCopyBytes = 16384;   // of keys and of values each, per part

@@ -288,7 +288,7 @@ __device__ __forceinline__ void write_row(const LogprobArgs& a, int64_t row, con
   auto lp = [&](float x) QMM_INLINE { return bad ? nan : x == -inf ? x : kLn2 * (power(x, r.m) - ls); };
   if (lane == 0) {
     a.logprob[row] = lp(x_token);
-    a.entropy[row] = bad ? nan : none ? 0.0f : fmaxf(kLn2 * (ls - r.y / r.s), 0.0f);
+    a.entropy[row] = bad ? nan : none ? 0.0f : max_or_nan(kLn2 * (ls - r.y / r.s), 0.0f);
   }
   const bool there = lane < a.top && (bad || list != 0);
   if (there) {

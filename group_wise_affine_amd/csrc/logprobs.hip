@@ -108,22 +108,29 @@ __device__ __forceinline__ float from_ordered(uint32_t o) {
 __device__ __forceinline__ float max_or_nan(float a, float b) { return __builtin_elementwise_maximum(a, b); }
 
 // ------------------------------------------------------------- running sums
-// m: the largest, NaN once a NaN was seen; s and y relative to c = fl(m log2 e)
-// (while that is finite; beyond, differences come before the product)
+// m: the largest, NaN once a NaN was seen; s and y relative to m log2 e. Below kBig that is
+// c = fl(m log2 e), so that an element costs one product and addition; the difference
+// y - (x - m) log2 e, half an ulp of c, is at most 2^-8 there, and the same in every term.
+// From kBig on (masks of -1e9 or of a type's lowest value, of f16 none) it would not stay
+// small (440 for -1e10), and differences come before the product.
 struct Sums {
   float m, s, y;
 };
-constexpr float kBig = 1e38f;
+constexpr float kBig = 65536.0f;
 // y of an element
 __device__ __forceinline__ float power(float x, float m) {
   const float c = m * kLog2e;
   return fabsf(m) < kBig ? fmaf(x, kLog2e, -c) : (x - m) * kLog2e;
 }
-// what y changes by when m goes from `from` to `to`
+// what y changes by when m goes from `from` to `to`: each one's reference is the rounded
+// product below kBig, the exact one from there on
 __device__ __forceinline__ float shift(float from, float to) {
 #pragma clang fp contract(off)
   const float a = from * kLog2e, b = to * kLog2e;   // (fused, the two would not be those that were taken)
-  return from == to ? 0.0f : fabsf(to) < kBig && fabsf(from) < kBig ? a - b : (from - to) * kLog2e;
+  const bool ra = fabsf(from) < kBig, rb = fabsf(to) < kBig;
+  if (from == to) return 0.0f;
+  if (ra && rb) return a - b;
+  return ra ? fmaf(-to, kLog2e, a) : rb ? fmaf(from, kLog2e, -b) : (from - to) * kLog2e;
 }
 __device__ __forceinline__ Sums raised(Sums a, float m) {
   const float d = fmaxf(shift(a.m, m), -200.0f), f = __builtin_amdgcn_exp2f(d);
@@ -175,7 +182,7 @@ __device__ __forceinline__ void unpack(const u32x4_t& u, float* v) {
 template <bool TOP>
 struct Seen {
   Sums sums{-__builtin_inff(), 0.0f, 0.0f};
-  bool big = false;                   // some lane's largest is no factor of log2 e
+  bool big = false;                   // some lane's largest is kBig or more
   uint64_t list = 0;                  // (-inf never enters: write_row() puts it in where it is needed)
   float above = -__builtin_inff();    // only larger ones may enter the list,
   float from = 0.0f;                  // and while `open` the first ones that equal this, the next number

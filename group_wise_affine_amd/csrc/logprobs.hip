@@ -292,7 +292,12 @@ __device__ __forceinline__ void write_row(const LogprobArgs& a, int64_t row, con
   const float inf = __builtin_inff(), nan = __builtin_nanf("");
   const bool bad = !(r.m < inf), none = r.s == 0.0f;
   const float ls = none ? 0.0f : __log2f(r.s);
-  auto lp = [&](float x) QMM_INLINE { return bad ? nan : x == -inf ? x : kLn2 * (power(x, r.m) - ls); };
+  // (of a mask near the type's lowest value only the difference stays in range: times log2 e
+  // it need not, and what the sum adds, below 30, is no bit of it)
+  auto lp = [&](float x) QMM_INLINE {
+    const float d = x - r.m;
+    return bad ? nan : x == -inf ? x : d < -1e30f ? d : kLn2 * (power(x, r.m) - ls);
+  };
   if (lane == 0) {
     a.logprob[row] = lp(x_token);
     a.entropy[row] = bad ? nan : none ? 0.0f : max_or_nan(kLn2 * (ls - r.y / r.s), 0.0f);

@@ -1,5 +1,6 @@
 """Log probabilities and entropy of rows whose finite logits are far from zero: masks of
 any value, peaks, both forms of the sums."""
+import numpy as np
 import pytest
 import torch
 
@@ -62,3 +63,25 @@ def test_logits_on_both_sides_of_a_sums_form(V, top):
     x = torch.cat([x - 4.5, x, x.sort(1).values, x.sort(1, descending=True).values]).cuda()
     t = toks(len(x), V, 2)
     check(x, t, top, Q.logprobs(x, t, top=top), f"V{V} top {top}")
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("V", [70, 5000, 70001])
+def test_probabilities_of_the_lowest_logits(V, dt):
+    """Tokens under a mask of the type's lowest value, asked for and among the top:
+    x - lse is finite wherever fp32 can hold it."""
+    low = float(torch.finfo(DT[dt]).min)
+    x = torch.full((4, V), low).to(DT[dt])
+    x[0, :3] = torch.tensor([1.0, 2.0, 3.0])
+    x[1, V // 2] = -2.9e38
+    x[2, V - 1] = 3.0e38   # the others: past the range of fp32
+    x[3, 1] = -2.4e38
+    t = torch.tensor([V - 1, 0, 0, 0], dtype=torch.int32)
+    lp, _, ids, tl = (o.double().cpu().numpy() for o in Q.logprobs(x.cuda(), t.cuda(), top=6))
+    d = x.double().numpy()
+    for r, lse in enumerate((3.40760596444438, d[1].max(), d[2].max(), d[3].max())):
+        for got, want in ((lp[r], d[r, t[r]] - lse), *zip(tl[r], np.sort(d[r])[::-1][:6] - lse)):
+            if want < -3.4028235e38:
+                assert got == -np.inf
+            else:
+                assert abs(got - want) <= 2.0 ** -22 * abs(want) + 1e-5, (r, got, want)

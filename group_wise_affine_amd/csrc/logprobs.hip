@@ -234,11 +234,14 @@ struct Seen {
       sums = raised(sums, max_or_nan(sums.m, mx));
       big = __any(fabsf(sums.m) >= kBig && sums.m > -__builtin_inff());
     }
+    // A load's terms are added up first: one by one, those of a plateau would be rounded the
+    // same way at each step of a long row (1.4e-5 off in a sum of 1000, 2.7e-6 so).
     // (what is -inf weighs nothing; 2^-200 is 0)
+    float s = 0.0f, t = 0.0f;
     auto add = [&](float p) QMM_INLINE {
       const float y = fmaxf(p, -200.0f), e = __builtin_amdgcn_exp2f(y);
-      sums.s += e;
-      sums.y = fmaf(e, y, sums.y);
+      s += e;
+      t = fmaf(e, y, t);
     };
     if (!big) {
       const float c = -sums.m * kLog2e;
@@ -248,6 +251,8 @@ struct Seen {
 #pragma unroll
       for (int j = 0; j < N; j++) add(power(x[j], sums.m));
     }
+    sums.s += s;
+    sums.y += t;
     return TOP && __any(mx > above);
   }
   // the first element's index is i

@@ -1,5 +1,5 @@
 """Log probabilities and entropy of rows whose finite logits are far from zero: masks of
-any value, peaks, both forms of the sums."""
+any value, peaks, both forms of the sums; and the accuracy of long rows' sums."""
 import numpy as np
 import pytest
 import torch
@@ -85,3 +85,76 @@ def test_probabilities_of_the_lowest_logits(V, dt):
                 assert got == -np.inf
             else:
                 assert abs(got - want) <= 2.0 ** -22 * abs(want) + 1e-5, (r, got, want)
+
+
+def final(lp):
+    """Roundings behind the sums, of a log probability `lp`: the logarithm's (an ulp), the
+    token's exponent, the difference's, the product's and its factor's."""
+    return 6 * 2.0 ** -24 * np.maximum(np.abs(lp), 1.0)
+
+
+def lane_sum(rest, n0, n1, N):
+    """Half an ulp of each partial sum of a lane that adds n0 ones and n1 terms `rest`, N of
+    them at a time, relative to its sum."""
+    s, off = np.zeros_like(rest), np.zeros_like(rest)
+    for k in range((n0 + n1) // N):
+        s = s + N * (1.0 if k < n0 // N else rest)
+        off += 2.0 ** (np.floor(np.log2(s)) - 24)
+    return off / s
+
+
+@pytest.mark.parametrize("dt,N", [("bf16", 8), ("f32", 4)])
+def test_long_sums_are_not_taken_term_by_term(dt, N):
+    """Rows of a plateau behind some larger logits, many plateaus: added one by one, its
+    terms are rounded the same way in every step of a lane, up to 1000 times. Bound: half
+    an ulp of each of a lane's partial sums, a load's N terms added first (N - 1
+    roundings, as many as 2^-24 each); the exponential's ulp and its exponent's rounding
+    (4 * 2^-24); lanes and wavefronts joined (7 sums, and as many scalings)."""
+    M, lanes = 2048, 128
+    V = 1000 * lanes
+    n0 = 4 * N   # terms of a lane's first four loads
+    c = torch.linspace(-0.7, -0.2, M).to(DT[dt])
+    x = c[:, None].repeat(1, V)
+    x[:, :n0 * lanes] = 0.0
+    t = torch.full((M,), V - 1, dtype=torch.int32)
+    t[::2] = 0
+    lp, h, _, _ = (o.double().cpu().numpy() for o in Q.logprobs(x.cuda(), t.cuda(), top=3))
+    c = c.double().numpy()
+    s = lanes * (n0 + (1000 - n0) * np.exp(c))
+    want = np.where(t.numpy() == 0, 0.0, c) - np.log(s)
+    u = lane_sum(np.exp(c), n0, 1000 - n0, N) + (N - 1 + 4 + 14) * 2.0 ** -24
+    off = np.abs(lp - want) / (u + final(want))
+    assert off.max() <= 1, f"log probability off by {off.max()} tolerances"
+    # the mean of x - max: numerator (as many additions, 2^-24 each, a product more) and
+    # denominator
+    mean = lanes * (1000 - n0) * np.exp(c) * -c / s
+    v = (1000 / N + N + 20) * 2.0 ** -24
+    off = np.abs(h - (np.log(s) + mean)) / (u + (u + v) * mean + final(np.log(s)) + final(mean))
+    assert off.max() <= 1, f"entropy off by {off.max()} tolerances"
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("M,V", [(1, 131071), (3, 20000), (40, 50001), (300, 9999), (2048, 32000), (2100, 5001)])
+def test_accuracy_of_plain_rows(M, V, dt):
+    """Rows without masks, a bound from the number of additions that there are: a lane
+    takes A loads of N elements, and its sums are raised at most once per load (three
+    roundings); then as above, with 14 joins of four roundings at most. An exponent's
+    rounding and its factor's make a term off by 2^-23 |x - max| of it. The mean of x -
+    max has such a sum above and below the line."""
+    N = 4 if dt == "f32" else 8
+    lanes = 512 if M < 2048 else 128
+    A = -(-V // (N * lanes)) + 2
+    x, t = rows(M, V, dt, M + V), toks(M, V, 5)
+    d = x.double().cpu().numpy()
+    top = d.max(1)
+    z = np.exp(d - top[:, None])
+    s = z.sum(1)
+    mag, square = (z * (top[:, None] - d)).sum(1) / s, (z * (top[:, None] - d) ** 2).sum(1) / s
+    lp, h = d[np.arange(M), t.cpu().numpy()] - top - np.log(s), np.log(s) + mag
+    u = (4 * A + N - 1 + 4 + 56) * 2.0 ** -24
+    for n in (0, 5):
+        a, b, _, _ = (o.double().cpu().numpy() for o in Q.logprobs(x, t, top=n))
+        off = np.abs(a - lp) / (u + 2.0 ** -23 * mag + final(lp))
+        assert off.max() <= 1, f"log probability, top {n}: {off.max()} tolerances"
+        off = np.abs(b - h) / (u * (1 + 2 * mag) + 2.0 ** -23 * (mag + mag ** 2 + square) + final(np.log(s)) + final(mag))
+        assert off.max() <= 1, f"entropy, top {n}: {off.max()} tolerances"

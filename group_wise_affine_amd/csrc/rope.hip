@@ -170,10 +170,14 @@ hipError_t launch_qk_norm_rope(int dt, const void* q, int64_t ldq, const void* k
                                const float* freq, int64_t rot, bool neighbours, const void* wq,
                                const void* wk, float eps, void* qo, int64_t ldqo, void* ko,
                                int64_t ldko, hipStream_t st) {
-  const RopeArgs a{static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k),
-                   static_cast<const uint16_t*>(wq), static_cast<const uint16_t*>(wk), ldq, ldk,
-                   static_cast<uint16_t*>(qo), static_cast<uint16_t*>(ko), ldqo, ldko, pos, freq, T,
-                   (int)hq, (int)(hq + hk), (int)D, (int)(rot / 2), eps};
+  RopeArgs a{static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k),
+             static_cast<const uint16_t*>(wq), static_cast<const uint16_t*>(wk), ldq, ldk,
+             static_cast<uint16_t*>(qo), static_cast<uint16_t*>(ko), ldqo, ldko, pos, freq, T,
+             (int)hq, (int)(hq + hk), (int)D, (int)(rot / 2), eps};
+  // (an f16 head that is not all zeros has a mean square above 2^-58, and of zeros the result
+  // is 0 for any eps but 0: a subnormal one, of which the reciprocal root would be infinite,
+  // need not be met)
+  if (dt == 0 && eps > 0.0f && eps < 0x1p-126f) a.eps = 0x1p-126f;
   auto go = [&]<class T_, bool N, int L, int PASSES>() {
     const int64_t per = 64 / L * PASSES, units = T * ((a.heads + per - 1) / per), groups = (units + 3) / 4;
     // (a row of a grid is short of 2^32 threads)

@@ -132,9 +132,11 @@ __global__ __launch_bounds__(256) void qk_rope_kernel(RopeArgs a) {
       };
       float ss = squares(), eps = a.eps;
       if constexpr (__is_same(T, BF16)) {
-        // squares that leave the range of 32 bits: the row by a power of two
-        // (where eps outweighs small ones, they need no bits)
-        const float f = h >= a.heads ? 1.0f : ss > 0x1p100f ? 0x1p-70f : ss < 0x1p-90f && eps < 0x1p-60f ? 0x1p70f : 1.0f;
+        // squares that leave the range of 32 bits: the row by a power of two (where eps
+        // outweighs small ones, they need no bits). Up by 2^92: the square of 2^-133 is then
+        // far from the subnormal numbers, of which the reciprocal root would be infinite,
+        // and 2^-90 or an eps of 2^-60 still finite
+        const float f = h >= a.heads ? 1.0f : ss > 0x1p100f ? 0x1p-70f : ss < 0x1p-90f && eps < 0x1p-60f ? 0x1p92f : 1.0f;
         if (__any(f != 1.0f)) {
 #pragma unroll
           for (int j = 0; j < 8; j++) x[j] *= f;

@@ -89,12 +89,14 @@ __device__ __forceinline__ Walk walk(const AttnArgs& a, int most, int low) {
 // ends.
 __device__ __forceinline__ int tree_parent(const AttnArgs& a, int t0, int n) {
   const int lane = threadIdx.x % 64, b = max(n - kTreeTokens, 0);
-  return b + lane < n ? a.parent[t0 + b + lane] - b : -1;
+  return b + lane < n ? a.parent[t0 + b + lane] : -1;
 }
 __device__ __forceinline__ uint64_t tree_path(int parent, int n, int i) {
-  const int lane = threadIdx.x % 64;
-  parent = parent < lane ? parent : -1;
-  int at = i - max(n - kTreeTokens, 0);
+  const int lane = threadIdx.x % 64, b = max(n - kTreeTokens, 0);
+  // (unsigned: any number may stand there, and one below b becomes a large one)
+  const uint32_t earlier = (uint32_t)parent - (uint32_t)b;
+  parent = earlier < (uint32_t)lane ? (int)earlier : -1;
+  int at = i - b;
   uint64_t path = 0;
   while (__any(at >= 0)) {
     path |= at >= 0 ? 1ull << at : 0;

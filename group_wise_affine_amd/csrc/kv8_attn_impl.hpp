@@ -594,6 +594,7 @@ __global__ __launch_bounds__(256) void kv8_join_few_kernel(AttnArgs a) {
 // every workgroup waits for.
 template <Mask M, class T, int D, int R>
 __global__ __launch_bounds__(256) void kv8_join_kernel(AttnArgs a) {
+  static_assert(R == 16, "only the decode kernel's parts are many");
   constexpr int kFloats = kPart<D, R>;
   constexpr int kSub = 512 / D, kEach = kMaxSplits / kSub;
   __shared__ float fac[kMaxSplits], half[256][2];
@@ -1496,12 +1497,17 @@ hipError_t launch_attention(const Kv8& c, int dt, const void* q, int64_t ldq, in
              (int)window, (int)sinks, parent};
   const dim3 grid((unsigned)p.items, (unsigned)p.columns, (unsigned)p.splits);
   auto join = [&]<class T_, int D, int R>(const AttnArgs& x, unsigned units, int rows) {
-    if (R == kPromptRows || x.splits <= few_parts(R))
+    auto few = [&]() {
       hipLaunchKernelGGL((kv8_join_few_kernel<M, T_, D, R>),
                          dim3(units, (unsigned)((rows + 512 / D - 1) / (512 / D))), dim3(256), 0, st, x);
-    else
-      hipLaunchKernelGGL((kv8_join_kernel<M, T_, D, R == kPromptRows ? 16 : R>), dim3(units, (unsigned)rows),
-                         dim3(256), 0, st, x);
+    };
+    if constexpr (R == 16) {
+      if (x.splits > few_parts(R)) {
+        hipLaunchKernelGGL((kv8_join_kernel<M, T_, D, R>), dim3(units, (unsigned)rows), dim3(256), 0, st, x);
+        return;
+      }
+    }
+    few();   // (plan() cuts drafts and prompts into no more parts than that)
   };
   auto go = [&]<class T_, int D>() {
     auto decode = [&]<int BT>() {

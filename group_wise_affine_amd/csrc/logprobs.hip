@@ -500,10 +500,16 @@ int parts_of(int dt, int64_t M, int64_t V) {
   p = p < most ? p : most;
   return (int)(p < 1 ? 1 : p > kMaxParts ? kMaxParts : p);
 }
-// Eight wavefronts of a workgroup, fewer where the rows fill the chip: what a list
-// costs a wavefront is then paid less often (2048 rows of 128000 in bf16, 20 tokens:
-// 129 us with two, 138 with four; without a list 125 and 102; 1024 rows: 79 with eight).
-constexpr int64_t kManyRows = 2048;
+// Eight wavefronts of a workgroup, fewer where the rows fill the chip: two with a list, of
+// which each wavefront pays the start and the end, and four without. (bf16, few and eight
+// wavefronts, us:
+//   rows            1024      1280      1536      1800      2048      2560      4096
+//   V 32000,  20   39, 37    44, 44    49, 50    50, 62    51, 63    63, 75    78, 114
+//   V 128000, 20   97, 78   109, 94   122, 108  124, 133  126, 138  158, 167  218, 255
+//   V 200064, 20  134, 105  149, 127  168, 147  171, 181  177, 190  222, 231  319, 358
+//   V 128000, 0    61, 52    68, 73    75, 79    88, 90    98, 98   137, 120  187, 186
+// and with 5 or 64 tokens as with 20.)
+constexpr int64_t kManyRows = 1537;
 
 }  // namespace
 

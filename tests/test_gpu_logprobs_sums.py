@@ -158,3 +158,15 @@ def test_accuracy_of_plain_rows(M, V, dt):
         assert off.max() <= 1, f"log probability, top {n}: {off.max()} tolerances"
         off = np.abs(b - h) / (u * (1 + 2 * mag) + 2.0 ** -23 * (mag + mag ** 2 + square) + final(np.log(s)) + final(mag))
         assert off.max() <= 1, f"entropy, top {n}: {off.max()} tolerances"
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("M", [256, 257, 1536, 1537])
+def test_rows_beside_a_change_of_workgroups(M, dt):
+    """Numbers of rows on both sides of where a row is no longer cut, and of where a
+    workgroup has fewer wavefronts."""
+    V = 8500
+    x, t = rows(M, V, dt, M), toks(M, V, 6)
+    x[M - 1, V // 2:] = -1e4
+    for top in (0, 20):
+        check(x, t, top, Q.logprobs(x, t, top=top), f"{M}x{V} {dt} top {top}")

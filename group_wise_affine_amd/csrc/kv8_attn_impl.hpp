@@ -668,11 +668,13 @@ __global__ __launch_bounds__(256) void kv8_join_kernel(AttnArgs a) {
 // are numbered eight apart, which puts them on one XCD and its L2 (62 % of the requests
 // hit it).
 //
-// Bound: the vector unit (conversions and exponentials, 580 instructions per tile and
-// wavefront), two wavefronts to a SIMD: 3.0 us per tile of 64 tokens, and 11 us of a
-// workgroup's 40 are its start and its end. 16 trees of up to 26 tokens behind up to
-// 8166, 8 heads of 4 of 128, bf16: 86 us and 10 to join the parts, 1.9 TB/s of the codes
-// (the prompt kernel 124 us and, for the smaller trees, the decode kernel 49 more).
+// Bound: no unit. With two wavefronts to a SIMD a wavefront waits for its loads 41 % of
+// its time and for its turn 22 %; the vector unit (conversions and exponentials, 580
+// instructions per tile and wavefront) is busy 37 % of the cycles, the matrix unit 12 %.
+// A tile of 64 tokens takes 3.0 us, and 11 us of a workgroup's 40 are its start and its
+// end. 16 trees of up to 26 tokens behind up to 8166, 8 heads of 4 of 128, bf16: 856
+// parts on 512 places, 86 us and 15 to join them, 1.9 TB/s of the codes (the prompt
+// kernel 124 us and, for the smaller trees, the decode kernel 49 more).
 // floats from one row to the next where the wavefronts' results are joined: rows
 // start in other banks
 constexpr int draft_row(int D) { return D + 4; }
@@ -1295,7 +1297,7 @@ __global__ __launch_bounds__(2 * kPromptRows, D == 256 ? 1 : 2) void kv8_prompt_
   }
   if (wave * 32 + col >= rows) return;
   l_run += __shfl_xor(l_run, 32);
-  if (parts > 1) {   // kv8_join_kernel adds them up
+  if (parts > 1) {   // kv8_join_few_kernel adds them up
     const int64_t unit = (int64_t)index * c.heads + head;
     float* part = a.ws + (unit * a.splits + split) * kPart<D, kPromptRows>;
     const float vref = __builtin_amdgcn_exp2f(at.w - at.base);

@@ -10,8 +10,9 @@
 // bits a position of 10^5 leaves an error of 0.004), its sine and cosine are
 // polynomials in 32 bits.
 //
-// Bound: memory (8192 tokens, 40 heads of 128, bf16: 168 MB in 34.9 us, 4.8 TB/s), for
-// few tokens the launch (1 token: 2.4 us, of which a call from Python takes 5.4).
+// Bound: memory (8192 tokens, 40 heads of 128, bf16: 168 MB in 34 to 37 us, 4.5 to 4.9
+// TB/s), for few tokens the launch (1 token: 2.5 us; a call of it from Python takes the
+// host 6).
 #include "int8_common.hpp"
 #include "kernels.hpp"
 

@@ -200,6 +200,35 @@ __device__ __forceinline__ float weight_scale(float vs, const Refs& at) {
   return r > 0x1.fffffep+127f ? 0x1.fffffep+127f : r;
 }
 
+// Two weights as two f16 terms each, the rounding and what it leaves. The compiler is not
+// to know how the first came to be: it would round the product that a weight is once more
+// for the second, by v_fma_mix of the exact product where the first is v_cvt of the one
+// rounded to fp32, and where these differ (one weight in 2^13) a bit of eleven is lost.
+struct Terms {
+  half2_t hi, lo;
+};
+__device__ __forceinline__ Terms two_terms(float w0, float w1) {
+  uint32_t h = __builtin_bit_cast(uint32_t, half2_t{(_Float16)w0, (_Float16)w1});
+  asm("" : "+v"(h));
+  const half2_t hi = __builtin_bit_cast(half2_t, h);
+  return {hi, half2_t{(_Float16)(w0 - (float)hi[0]), (_Float16)(w1 - (float)hi[1])}};
+}
+// weight i of eight, in two terms when the next one is there too
+template <bool TWO>
+__device__ __forceinline__ void put_weight(half8_t& hi, half8_t& lo, int i, float w, float& before) {
+  if constexpr (!TWO) {
+    hi[i] = (_Float16)w;
+  } else if (i % 2 == 0) {
+    before = w;
+  } else {
+    const Terms t = two_terms(before, w);
+    hi[i - 1] = t.hi[0];
+    hi[i] = t.hi[1];
+    lo[i - 1] = t.lo[0];
+    lo[i] = t.lo[1];
+  }
+}
+
 // two outputs of a row, and whether it has seen a key at all
 struct Share {
   uint32_t pair;
@@ -454,13 +483,12 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : D == 128 ? 2 : 3) void kv8_
 #pragma unroll
     for (int h = 0; h < 2; h++) {
       half8_t pf, pl;
+      float before;
 #pragma unroll
       for (int i = 0; i < 8; i++) {
         const float e = __builtin_amdgcn_exp2f(p[8 * h + i] - at.base);
         l_run += e;
-        const float w = e * r;
-        pf[i] = (_Float16)w;
-        if constexpr (kTwo) pl[i] = (_Float16)(w - (float)pf[i]);
+        put_weight<kTwo>(pf, pl, i, e * r, before);
       }
 #pragma unroll
       for (int i = 0; i < VD; i++) {
@@ -886,13 +914,12 @@ __global__ __launch_bounds__(64 * NW, 2) void kv8_draft_kernel(AttnArgs a) {
 #pragma unroll
       for (int m = 0; m < 2; m++) {
         half8_t pf, pl;
+        float before;
 #pragma unroll
         for (int e = 0; e < 8; e++) {
           const float x = __builtin_amdgcn_exp2f(fmaf(sc[j][8 * m + e], ks[j], -at.base));
           l_run += x;
-          const float w = x * f;
-          pf[e] = (_Float16)w;
-          if constexpr (kTwo) pl[e] = (_Float16)(w - (float)pf[e]);
+          put_weight<kTwo>(pf, pl, e, x * f, before);
         }
 #pragma unroll
         for (int i = 0; i < VD; i++) {
@@ -1212,6 +1239,7 @@ __global__ __launch_bounds__(2 * kPromptRows, D == 256 ? 1 : 2) void kv8_prompt_
       // scale is the row's too, and the exponentials of the rest are 0)
       if constexpr (MASK && M != Mask::kCausal) r = seen >> (g * 8) & 0xff ? r : 0.0f;
       half8_t hi, lo;
+      float before;
 #pragma unroll
       for (int e = 0; e < 8; e++) {
         const float x = sc[g / 2][g % 2 * 8 + e];
@@ -1219,8 +1247,7 @@ __global__ __launch_bounds__(2 * kPromptRows, D == 256 ? 1 : 2) void kv8_prompt_
         l_run += p;
         float w = p * r;
         if constexpr (MASK && M == Mask::kCausal) w = sees(g, e) ? w : 0.0f;
-        hi[e] = (_Float16)w;
-        if constexpr (kTwo) lo[e] = (_Float16)(w - (float)hi[e]);
+        put_weight<kTwo>(hi, lo, e, w, before);
       }
 #pragma unroll
       for (int i = 0; i < VD; i++) {

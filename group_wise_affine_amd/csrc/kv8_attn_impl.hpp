@@ -1028,9 +1028,9 @@ __device__ __forceinline__ int longest_first(const AttnArgs& a, int rank, int it
 //
 // Bound: the vector unit (conversions, exponentials, maxima: 61 % of the cycles)
 // and after it the matrix unit (34 %). Of visible pairs, four chunks of 2048 tokens
-// behind 3952, 8 heads of 4: 760 to 805 TFLOP/s for D = 128 in bf16, 600 to 635 in
-// f16 (two products per value), 655 and 485 for D = 64; 580 and 505 for D = 256
-// (two chunks of 1024 behind 4976). Eight wavefronts that share a tile, and two
+// behind 3952, 8 heads of 4: 760 to 830 TFLOP/s for D = 128 in bf16, 645 in f16 (two
+// products per value), 660 and 530 for D = 64; 580 to 605 and 535 for D = 256 (two
+// chunks of 1024 behind 4976). Eight wavefronts that share a tile, and two
 // groups of wavefronts of which one multiplies while the other weighs, took the
 // same time. The references of the weights and of the sum that follow each row by
 // itself cost 2 % (822 us, 806 with the largest value scale of a tile as the only
